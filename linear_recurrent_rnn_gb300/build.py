@@ -17,8 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "librglru.so")
 SOURCES = ["api.cu", "scan_simt.cu", "gemm_simt.cu", "noalloc.cu", "host_util.cu", "fused_fwd.cu", "fused_bwd.cu",
-           "decode.cu", "varlen.cu", "delta_rule.cu", "proj_tc.cu"]
-HEADERS = ["common.cuh", "internal.h", "tc.cuh", "host_util.h", "lookback.cuh"]
+           "decode.cu", "varlen.cu", "delta_rule.cu", "proj_tc.cu", "paged.cu", "paged_attn_simt.cu"]
+HEADERS = ["common.cuh", "internal.h", "tc.cuh", "host_util.h", "lookback.cuh",
+           "paged.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -33,6 +34,7 @@ def _deps():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
     files.append(os.path.join(ROOT, "include", "librglru.h"))
     files.append(os.path.join(ROOT, "include", "delta_rule.h"))
+    files.append(os.path.join(ROOT, "include", "paged_attn.h"))
     files.append(os.path.abspath(__file__))
     return files
 

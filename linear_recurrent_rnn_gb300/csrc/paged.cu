@@ -1,0 +1,402 @@
+// The paged key/value cache (include/paged_attn.h): the step's plan, the write of new keys and
+// values, and the host side of the attention.
+#include <math.h>
+
+#include <algorithm>
+
+#include "host_util.h"
+#include "paged.cuh"
+#include "tc.cuh"
+
+namespace rglru {
+
+namespace {
+
+// ---------------------------------------------------------------- plan
+// One launch, one cluster.  Every CTA scans all requests (new tokens and pages wanted) into its
+// own shared memory, the cluster meets, and only then is anything written: so kv_lens and the
+// free state may be updated in place, and the CTAs share the new table entries and the token
+// rows between them without waiting for one another again.  A token finds its request by a
+// binary search over the offsets; the page of a token in a new page is read from the ring
+// itself, not from the table.  Latency-bound: the floor is a launch, two dependent reads
+// (lengths, then table or ring) and the writes.
+struct PlanArgs {
+  int N, T, P, s, width;
+  const int32_t* cached;
+  const int32_t* fresh;
+  const int32_t* ring;
+  const int32_t* state;
+  int32_t* table;
+  int32_t* cu;
+  int32_t* kv_lens;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* state_out;
+};
+
+constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_CLUSTER = 8;
+
+__device__ __forceinline__ int plan_ceil(int64_t x, int s) { return (int)((x + s - 1) / s); }
+
+__global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
+  // per request: first row, first of its places in the ring's order, tokens cached
+  extern __shared__ int32_t plan_sm[];
+  int32_t* s_cu = plan_sm;
+  int32_t* s_off = s_cu + a.N + 1;
+  int32_t* s_c = s_off + a.N + 1;
+  __shared__ int64_t s_warp[2][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  const int head = a.state[0], count = min(max(a.state[1], 0), a.P);
+  int64_t base_q = 0, base_p = 0, over = 0;  // over: pages wanted past the table's width
+  for (int n0 = 0; n0 < a.N; n0 += blockDim.x) {
+    const int n = n0 + tid;
+    int c = 0, q = 0, need = 0;
+    if (n < a.N) {
+      c = max(a.cached[n], 0);
+      q = max(a.fresh[n], 0);
+      const int held = min(plan_ceil(c, a.s), a.width);
+      const int want = plan_ceil((int64_t)c + q, a.s);
+      need = max(min(want, a.width) - held, 0);
+      over += max(want - max(plan_ceil(c, a.s), a.width), 0);
+    }
+    int64_t sq = q, sp = need;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, sq, d), v = __shfl_up_sync(0xffffffffu, sp, d);
+      if (lane >= d) {
+        sq += u;
+        sp += v;
+      }
+    }
+    if (lane == 31) {
+      s_warp[0][warp] = sq;
+      s_warp[1][warp] = sp;
+    }
+    __syncthreads();
+    for (int k = 0; k < nw; ++k) {
+      const int64_t u = s_warp[0][k], v = s_warp[1][k];
+      if (k < warp) {
+        sq += u;
+        sp += v;
+      }
+    }
+    if (n < a.N) {
+      s_cu[n] = (int)min(base_q + sq - q, (int64_t)0x7fffffff);
+      s_off[n] = (int)min(base_p + sp - need, (int64_t)0x7fffffff);
+      s_c[n] = c;
+    }
+    for (int k = 0; k < nw; ++k) {
+      base_q += s_warp[0][k];
+      base_p += s_warp[1][k];
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    s_cu[a.N] = (int)min(base_q, (int64_t)0x7fffffff);
+    s_off[a.N] = (int)min(base_p, (int64_t)0x7fffffff);
+  }
+  for (int d = 16; d; d >>= 1) over += __shfl_xor_sync(0xffffffffu, over, d);
+  if (lane == 0) s_warp[0][warp] = over;
+  // every CTA has read its inputs before any CTA writes
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __syncthreads();
+  const int h0 = a.P > 0 ? ((head % a.P) + a.P) % a.P : 0;
+  const int stride = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + tid;
+  if (first == 0) {
+    int64_t o = 0;
+    for (int k = 0; k < nw; ++k) o += s_warp[0][k];
+    const int taken = min(s_off[a.N], count);
+    a.state_out[0] = (int)(((int64_t)h0 + taken) % a.P);
+    a.state_out[1] = count - taken;
+    a.state_out[2] = (int)min((int64_t)s_off[a.N] - taken + o, (int64_t)0x7fffffff);
+  }
+  auto owner = [&](const int32_t* v, int x) {  // the last n with v[n] <= x
+    int l = 0, h = a.N - 1;
+    while (l < h) {
+      const int mid = (l + h + 1) >> 1;
+      if (v[mid] <= x) l = mid; else h = mid - 1;
+    }
+    return l;
+  };
+  auto ring = [&](int i) { return i < count ? a.ring[(int)(((int64_t)h0 + i) % a.P)] : -1; };
+  for (int n = first; n <= a.N; n += stride) {
+    a.cu[n] = s_cu[n];
+    if (n < a.N)
+      a.kv_lens[n] = (int)min((int64_t)s_c[n] + (s_cu[n + 1] - s_cu[n]), (int64_t)0x7fffffff);
+  }
+  for (int i = first; i < s_off[a.N]; i += stride) {
+    const int n = owner(s_off, i);
+    a.table[(size_t)n * a.width + plan_ceil(s_c[n], a.s) + (i - s_off[n])] = ring(i);
+  }
+  for (int t = first; t < a.T; t += stride) {
+    int pos = 0;
+    int64_t slot = -1;
+    if (t < s_cu[a.N]) {
+      const int n = owner(s_cu, t), c = s_c[n];
+      pos = (int)min((int64_t)c + (t - s_cu[n]), (int64_t)0x7fffffff);
+      const int pg = pos / a.s, held = plan_ceil(c, a.s);
+      if (pg < a.width) {
+        const int id = pg < held ? a.table[(size_t)n * a.width + pg] : ring(s_off[n] + pg - held);
+        if (id >= 0) slot = (int64_t)id * a.s + pos % a.s;
+      }
+    }
+    a.positions[t] = pos;
+    a.slots[t] = slot;
+  }
+}
+
+// ---------------------------------------------------------------- write
+// A copy whose destination rows are chosen by the slots: a warp takes a token, its lanes the
+// 16-byte pieces of the token's keys and then its values, so that a warp has all of a token's
+// loads in flight at once.  Bound by memory bandwidth (and by latency for few tokens).
+struct WriteArgs {
+  int T, pieces, head_pieces, s_log2;  // 16-byte pieces of a token's keys, of one head
+  int64_t slots_end;                   // num_pages * page_size
+  const uint8_t* src[2];
+  uint8_t* dst[2];
+  int64_t src_token[2], src_head[2], dst_page[2], dst_token[2], dst_head[2];  // bytes
+  const int64_t* slots;
+};
+
+constexpr int WRITE_THREADS = 256;
+
+__global__ void __launch_bounds__(WRITE_THREADS) k_paged_write(const WriteArgs a) {
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int nwarps = gridDim.x * (WRITE_THREADS / 32);
+  for (int t = blockIdx.x * (WRITE_THREADS / 32) + (threadIdx.x >> 5); t < a.T; t += nwarps) {
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.slots_end) continue;
+    const int64_t page = slot >> a.s_log2, off = slot & ((1 << a.s_log2) - 1);
+#pragma unroll 4
+    for (int i = lane; i < 2 * a.pieces; i += 32) {
+      const int kv = i >= a.pieces, c = kv ? i - a.pieces : i;
+      const int h = c / a.head_pieces, b = (c - h * a.head_pieces) * 16;
+      const uint4 x = *reinterpret_cast<const uint4*>(a.src[kv] + t * a.src_token[kv] + h * a.src_head[kv] + b);
+      *reinterpret_cast<uint4*>(a.dst[kv] + page * a.dst_page[kv] + off * a.dst_token[kv] +
+                                h * a.dst_head[kv] + b) = x;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+int elem_bytes(const paged_shape* s) { return s->io == RGLRU_BF16 ? 2 : 4; }
+
+int log2_exact(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+rglru_status check_cache(const paged_shape* s) {
+  if (!s || s->num_seqs < 1 || s->tokens < 0 || s->num_pages < 1 || s->page_size < 1 ||
+      s->table_width < 1)
+    return RGLRU_ERR_INVALID_ARG;
+  if ((s->page_size & (s->page_size - 1)) || s->page_size < 8 || s->page_size > 4096 ||
+      s->num_seqs > PG_MAX_SEQS || (int64_t)s->num_pages * s->page_size > 0x7fffffffLL)
+    return RGLRU_ERR_UNSUPPORTED;
+  return RGLRU_OK;
+}
+
+rglru_status check_heads(const paged_shape* s) {
+  if (s->Hkv < 1 || s->D < 1 || (s->io != RGLRU_F32 && s->io != RGLRU_BF16))
+    return RGLRU_ERR_INVALID_ARG;
+  if (s->D < 8 || s->D > 256 || s->D * elem_bytes(s) % 16) return RGLRU_ERR_UNSUPPORTED;
+  return RGLRU_OK;
+}
+
+rglru_status check_queries(const paged_shape* s) {
+  if (s->Hq < 1 || s->Hq % s->Hkv || s->window < 0) return RGLRU_ERR_INVALID_ARG;
+  if (s->Hq / s->Hkv > 64) return RGLRU_ERR_UNSUPPORTED;
+  return RGLRU_OK;
+}
+
+bool aligned(const void* p, size_t n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+paged_strides strides_of(const paged_shape* s, const paged_strides* given) {
+  if (given) return *given;
+  paged_strides t;
+  t.q_token = t.o_token = (int64_t)s->Hq * s->D;
+  t.k_token = t.v_token = t.kc_token = t.vc_token = (int64_t)s->Hkv * s->D;
+  t.q_head = t.o_head = t.k_head = t.v_head = t.kc_head = t.vc_head = s->D;
+  t.kc_page = t.vc_page = (int64_t)s->page_size * s->Hkv * s->D;
+  return t;
+}
+
+// Strides are positive multiples of 16 bytes (16-byte loads, tensor maps).
+bool strides_ok(const paged_shape* s, std::initializer_list<int64_t> v) {
+  for (int64_t x : v)
+    if (x <= 0 || x * elem_bytes(s) % 16) return false;
+  return true;
+}
+
+}  // namespace
+
+cudaError_t launch_pdl(const void* f, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                       void** args, int cluster) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelExC(&cfg, f, args);
+  if (e != cudaSuccess) return e;
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace rglru
+
+using namespace rglru;
+
+extern "C" rglru_status paged_plan(const paged_shape* s, const int32_t* cached_lens,
+                                   const int32_t* new_lens, const int32_t* free_pages,
+                                   const int32_t* free_state, int32_t* block_table,
+                                   int32_t* cu_seqlens, int32_t* kv_lens, int32_t* positions,
+                                   int64_t* slots, int32_t* free_state_out, rglru_stream stream) {
+  const rglru_status st = check_cache(s);
+  if (st != RGLRU_OK) return st;
+  if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) ||
+      !aligned(free_state, 4) || !aligned(block_table, 4) || !aligned(cu_seqlens, 4) ||
+      !aligned(kv_lens, 4) || !aligned(free_state_out, 4))
+    return RGLRU_ERR_INVALID_ARG;
+  if (s->tokens > 0 && (!aligned(positions, 4) || !aligned(slots, 8))) return RGLRU_ERR_INVALID_ARG;
+  PlanArgs a;
+  a.N = s->num_seqs;
+  a.T = s->tokens;
+  a.P = s->num_pages;
+  a.s = s->page_size;
+  a.width = s->table_width;
+  a.cached = cached_lens;
+  a.fresh = new_lens;
+  a.ring = free_pages;
+  a.state = free_state;
+  a.table = block_table;
+  a.cu = cu_seqlens;
+  a.kv_lens = kv_lens;
+  a.positions = positions;
+  a.slots = slots;
+  a.state_out = free_state_out;
+  const size_t smem = (size_t)(3 * a.N + 2) * 4;
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_paged_plan),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return cuda_status(e);
+  // one CTA up to a row a thread, the whole cluster beyond
+  const int ctas = s->tokens > PLAN_THREADS ? PLAN_CLUSTER : 1;
+  void* args[] = {&a};
+  return cuda_status(launch_pdl(reinterpret_cast<const void*>(k_paged_plan), dim3(ctas),
+                                dim3(PLAN_THREADS), smem, stream, args, ctas));
+}
+
+extern "C" rglru_status paged_kv_write(const paged_shape* s, const paged_strides* strides,
+                                       const void* k, const void* v, const int64_t* slots,
+                                       void* k_cache, void* v_cache, rglru_stream stream) {
+  rglru_status st = check_cache(s);
+  if (st == RGLRU_OK) st = check_heads(s);
+  if (st != RGLRU_OK) return st;
+  if (s->tokens == 0) return RGLRU_OK;
+  if (!req(k) || !req(v) || !aligned(slots, 8) || !req(k_cache) || !req(v_cache))
+    return RGLRU_ERR_INVALID_ARG;
+  const paged_strides t = strides_of(s, strides);
+  if (!strides_ok(s, {t.k_token, t.k_head, t.v_token, t.v_head, t.kc_page, t.kc_token, t.kc_head,
+                      t.vc_page, t.vc_token, t.vc_head}))
+    return RGLRU_ERR_UNSUPPORTED;
+  const int es = elem_bytes(s);
+  WriteArgs a;
+  a.T = s->tokens;
+  a.head_pieces = s->D * es / 16;
+  a.pieces = s->Hkv * a.head_pieces;
+  a.s_log2 = log2_exact(s->page_size);
+  a.slots_end = (int64_t)s->num_pages * s->page_size;
+  a.src[0] = static_cast<const uint8_t*>(k);
+  a.src[1] = static_cast<const uint8_t*>(v);
+  a.dst[0] = static_cast<uint8_t*>(k_cache);
+  a.dst[1] = static_cast<uint8_t*>(v_cache);
+  const int64_t str[2][5] = {{t.k_token, t.k_head, t.kc_page, t.kc_token, t.kc_head},
+                             {t.v_token, t.v_head, t.vc_page, t.vc_token, t.vc_head}};
+  for (int i = 0; i < 2; ++i) {
+    a.src_token[i] = str[i][0] * es;
+    a.src_head[i] = str[i][1] * es;
+    a.dst_page[i] = str[i][2] * es;
+    a.dst_token[i] = str[i][3] * es;
+    a.dst_head[i] = str[i][4] * es;
+  }
+  a.slots = slots;
+  const int per = WRITE_THREADS / 32;
+  const int blocks = (int)std::min<int64_t>(((int64_t)a.T + per - 1) / per, 1 << 16);
+  void* args[] = {&a};
+  return cuda_status(launch_pdl(reinterpret_cast<const void*>(k_paged_write), dim3(blocks),
+                                dim3(WRITE_THREADS), 0, stream, args, 1));
+}
+
+extern "C" size_t paged_attention_workspace_bytes(const paged_shape* s) {
+  if (check_cache(s) != RGLRU_OK || check_heads(s) != RGLRU_OK || check_queries(s) != RGLRU_OK)
+    return 0;
+  return paged_attn_simt_ws_bytes(s);
+}
+
+extern "C" rglru_status paged_attention(const paged_shape* s, const paged_strides* strides,
+                                        const void* q, const void* k_cache, const void* v_cache,
+                                        const int32_t* block_table, const int32_t* cu_seqlens,
+                                        const int32_t* kv_lens, float scale, void* o, float* lse,
+                                        void* workspace, rglru_stream stream) {
+  rglru_status st = check_cache(s);
+  if (st == RGLRU_OK) st = check_heads(s);
+  if (st == RGLRU_OK) st = check_queries(s);
+  if (st != RGLRU_OK) return st;
+  if (!(scale > 0.0f) || !isfinite(scale)) return RGLRU_ERR_INVALID_ARG;
+  if (s->tokens == 0) return RGLRU_OK;
+  if (!req(q) || !req(k_cache) || !req(v_cache) || !aligned(block_table, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) || !req(o) ||
+      (lse && !aligned(lse, 4)) || !req(workspace))
+    return RGLRU_ERR_INVALID_ARG;
+  const paged_strides t = strides_of(s, strides);
+  if (!strides_ok(s, {t.q_token, t.q_head, t.o_token, t.o_head, t.kc_page, t.kc_token, t.kc_head,
+                      t.vc_page, t.vc_token, t.vc_head}))
+    return RGLRU_ERR_UNSUPPORTED;
+  PagedArgs a = {};
+  a.N = s->num_seqs;
+  a.T = s->tokens;
+  a.Hq = s->Hq;
+  a.Hkv = s->Hkv;
+  a.g = s->Hq / s->Hkv;
+  a.D = s->D;
+  a.P = s->num_pages;
+  a.ps_log2 = log2_exact(s->page_size);
+  a.table_width = s->table_width;
+  a.window = s->window;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.q = q;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.table = block_table;
+  a.cu = cu_seqlens;
+  a.kv_lens = kv_lens;
+  a.o = o;
+  a.lse = lse;
+  a.q_token = t.q_token;
+  a.q_head = t.q_head;
+  a.o_token = t.o_token;
+  a.o_head = t.o_head;
+  a.kc_page = t.kc_page;
+  a.kc_token = t.kc_token;
+  a.kc_head = t.kc_head;
+  a.vc_page = t.vc_page;
+  a.vc_token = t.vc_token;
+  a.vc_head = t.vc_head;
+  a.ws = static_cast<uint8_t*>(workspace);
+  return cuda_status(launch_paged_attn_simt(a, s->io, stream));
+}

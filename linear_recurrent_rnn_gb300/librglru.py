@@ -1,9 +1,11 @@
-"""Thin ctypes binding of librglru (include/librglru.h and include/delta_rule.h).
+"""Thin ctypes binding of librglru (include/librglru.h, include/delta_rule.h and
+include/paged_attn.h).
 
 Argument marshalling only: every function here checks that its tensors are contiguous CUDA
-tensors, passes their device pointers and the current CUDA stream to the C ABI call of the
-same name, and raises ``RglruError`` on a non-OK status.  No arithmetic runs in Python and
-there is no fallback: if the shared library is missing, the first call raises.
+tensors (the paged-cache calls also take strided ones, and check types and shapes), passes their
+device pointers and the current CUDA stream to the C ABI call of the same name, and raises
+``RglruError`` on a non-OK status.  No arithmetic runs in Python and there is no fallback: if
+the shared library is missing, the first call raises.
 """
 from __future__ import annotations
 
@@ -47,6 +49,18 @@ class DeltaShape(ctypes.Structure):
                 ("state_v_first", ctypes.c_int32)]
 
 
+class PagedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("num_seqs", "tokens", "Hq", "Hkv", "D", "num_pages", "page_size", "table_width",
+                 "io", "window")]
+
+
+class PagedStrides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("q_token", "q_head", "o_token", "o_head", "k_token", "k_head", "v_token",
+                 "v_head", "kc_page", "kc_token", "kc_head", "vc_page", "vc_token", "vc_head")]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -58,6 +72,9 @@ EXPORTS = ("rglru_status_string", "rglru_saved_bytes", "rglru_workspace_bytes",
            "rglru_debug_kernel_events", "rglru_step", "rglru_fused_forward_varlen",
            "rglru_fused_backward_varlen", "delta_rule_saved_bytes", "delta_rule_workspace_bytes",
            "delta_rule_forward", "delta_rule_backward", "delta_rule_state_fp8_qdq")
+
+EXPORTS_PAGED = ("paged_plan", "paged_kv_write", "paged_attention_workspace_bytes",
+                 "paged_attention")
 
 # Static look-back scratch of rglru_forward_noalloc, per GPU (RGLRU_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -119,6 +136,14 @@ def lib():
             L.delta_rule_state_fp8_qdq.restype = ctypes.c_int
             L.delta_rule_forward.restype = ctypes.c_int
             L.delta_rule_backward.restype = ctypes.c_int
+            PS, ST = ctypes.POINTER(PagedShape), ctypes.POINTER(PagedStrides)
+            L.paged_plan.argtypes = [PS] + [P] * 11
+            L.paged_kv_write.argtypes = [PS, ST] + [P] * 6
+            L.paged_attention_workspace_bytes.argtypes = [PS]
+            L.paged_attention_workspace_bytes.restype = ctypes.c_size_t
+            L.paged_attention.argtypes = [PS, ST] + [P] * 6 + [ctypes.c_float] + [P] * 4
+            for n in ("paged_plan", "paged_kv_write", "paged_attention"):
+                getattr(L, n).restype = ctypes.c_int
             L.rglru_kernel_launches.argtypes = []
             L.rglru_kernel_launches.restype = ctypes.c_uint64
             for n in ("rglru_gate_proj", "rglru_forward", "rglru_backward",
@@ -324,3 +349,105 @@ def delta_rule_state_fp8_qdq(state, out, block_v=64, stream=None):
     n = state.numel() // (Dk * Dv)
     _check("delta_rule_state_fp8_qdq", lib().delta_rule_state_fp8_qdq(
         _p(state), _p(out), int(n), int(Dk), int(Dv), int(block_v), _stream(stream)))
+
+
+# ---------------------------------------------------------------- paged cache and attention
+
+def make_paged_shape(num_seqs, tokens, Hq=1, Hkv=1, D=8, num_pages=1, page_size=16,
+                     table_width=1, io=BF16, window=0):
+    """Sizes of one step over a paged cache (paged_plan ignores the heads, D, io and window)."""
+    if isinstance(io, torch.dtype):
+        io = _DT[io]
+    return PagedShape(int(num_seqs), int(tokens), int(Hq), int(Hkv), int(D), int(num_pages),
+                      int(page_size), int(table_width), int(io), int(window))
+
+
+def paged_attention_workspace_bytes(shape: PagedShape) -> int:
+    return int(lib().paged_attention_workspace_bytes(ctypes.byref(shape)))
+
+
+def alloc_paged_workspace(shape: PagedShape, device="cuda") -> torch.Tensor:
+    """Scratch of paged_attention, zeroed as its first use wants it; one per stream."""
+    return torch.zeros(max(1, paged_attention_workspace_bytes(shape)), dtype=torch.uint8,
+                       device=device)
+
+
+def _arg(t, name, dtype, shape):
+    """A contiguous CUDA tensor of this dtype and shape (the entry points read it through its
+    address alone)."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, want {tuple(shape)} {dtype}")
+    return _p(t)
+
+
+def _view(t, name, dtype, shape):
+    """A CUDA tensor of this dtype and shape whose last dimension is contiguous; the others may
+    have any stride."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, want {tuple(shape)} {dtype}")
+    if not t.is_cuda:
+        raise ValueError("librglru takes CUDA tensors")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _steps(t):
+    """Strides of all dimensions but the last, in elements (a dimension of one element has the
+    stride that a contiguous tensor would have)."""
+    out, n = [], t.shape[-1]
+    for size, st in zip(t.shape[-2::-1], t.stride()[-2::-1]):
+        out.append(st if size > 1 else n)
+        n *= size
+    return out[::-1]
+
+
+def paged_plan(shape, cached_lens, new_lens, free_pages, free_state, block_table, cu_seqlens,
+               kv_lens, positions, slots, free_state_out, stream=None):
+    N, T, i32 = shape.num_seqs, shape.tokens, torch.int32
+    _check("paged_plan", lib().paged_plan(
+        ctypes.byref(shape), _arg(cached_lens, "cached_lens", i32, (N,)),
+        _arg(new_lens, "new_lens", i32, (N,)),
+        _arg(free_pages, "free_pages", i32, (shape.num_pages,)),
+        _arg(free_state, "free_state", i32, (3,)),
+        _arg(block_table, "block_table", i32, (N, shape.table_width)),
+        _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,)), _arg(kv_lens, "kv_lens", i32, (N,)),
+        _arg(positions, "positions", i32, (T,)), _arg(slots, "slots", torch.int64, (T,)),
+        _arg(free_state_out, "free_state_out", i32, (3,)), _stream(stream)))
+
+
+def paged_kv_write(shape, k, v, slots, k_cache, v_cache, stream=None):
+    """k, v [tokens, Hkv, D] and the caches [num_pages, page_size, Hkv, D] may be strided views
+    (slices of a fused projection, a cache stored head by head)."""
+    dt, T, H, D = TORCH_DT[shape.io], shape.tokens, shape.Hkv, shape.D
+    cache = (shape.num_pages, shape.page_size, H, D)
+    kp, vp = _view(k, "k", dt, (T, H, D)), _view(v, "v", dt, (T, H, D))
+    kc, vc = _view(k_cache, "k_cache", dt, cache), _view(v_cache, "v_cache", dt, cache)
+    st = None
+    if not (k.is_contiguous() and v.is_contiguous() and k_cache.is_contiguous() and
+            v_cache.is_contiguous()):
+        st = PagedStrides(0, 0, 0, 0, *_steps(k), *_steps(v), *_steps(k_cache), *_steps(v_cache))
+    _check("paged_kv_write", lib().paged_kv_write(
+        ctypes.byref(shape), st, kp, vp, _arg(slots, "slots", torch.int64, (T,)), kc, vc,
+        _stream(stream)))
+
+
+def paged_attention(shape, q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, scale, o, lse,
+                    workspace, stream=None):
+    """q, o [tokens, Hq, D] and the caches [num_pages, page_size, Hkv, D] may be strided views;
+    lse float32 [tokens, Hq] or None; workspace from alloc_paged_workspace."""
+    dt, T, D, i32 = TORCH_DT[shape.io], shape.tokens, shape.D, torch.int32
+    N, Hq = shape.num_seqs, shape.Hq
+    cache = (shape.num_pages, shape.page_size, shape.Hkv, D)
+    qp, op = _view(q, "q", dt, (T, Hq, D)), _view(o, "o", dt, (T, Hq, D))
+    kc, vc = _view(k_cache, "k_cache", dt, cache), _view(v_cache, "v_cache", dt, cache)
+    st = None
+    if not (q.is_contiguous() and o.is_contiguous() and k_cache.is_contiguous() and
+            v_cache.is_contiguous()):
+        st = PagedStrides(*_steps(q), *_steps(o), 0, 0, 0, 0, *_steps(k_cache), *_steps(v_cache))
+    _check("paged_attention", lib().paged_attention(
+        ctypes.byref(shape), st, qp, kc, vc,
+        _arg(block_table, "block_table", i32, (N, shape.table_width)),
+        _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,)), _arg(kv_lens, "kv_lens", i32, (N,)),
+        float(scale), op, None if lse is None else _arg(lse, "lse", torch.float32, (T, Hq)),
+        _p(workspace), _stream(stream)))
