@@ -345,7 +345,7 @@ extern "C" rglru_status paged_kv_write(const paged_shape* s, const paged_strides
 extern "C" size_t paged_attention_workspace_bytes(const paged_shape* s) {
   if (check_cache(s) != RGLRU_OK || check_heads(s) != RGLRU_OK || check_queries(s) != RGLRU_OK)
     return 0;
-  return paged_attn_simt_ws_bytes(s);
+  return s->io == RGLRU_BF16 ? paged_attn_tc_ws_bytes(s) : paged_attn_simt_ws_bytes(s);
 }
 
 extern "C" rglru_status paged_attention(const paged_shape* s, const paged_strides* strides,
@@ -377,7 +377,7 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
   a.P = s->num_pages;
   a.ps_log2 = log2_exact(s->page_size);
   a.table_width = s->table_width;
-  a.window = s->window;
+  a.window = s->window < 1 << 30 ? s->window : 0;  // (lengths are clamped to 2^30)
   a.scale_log2 = scale * 1.4426950408889634f;
   a.q = q;
   a.kc = k_cache;
@@ -398,5 +398,7 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
   a.vc_token = t.vc_token;
   a.vc_head = t.vc_head;
   a.ws = static_cast<uint8_t*>(workspace);
-  return cuda_status(launch_paged_attn_simt(a, s->io, stream));
+  return cuda_status(s->io == RGLRU_BF16
+                         ? launch_paged_attn_tc(a, s->num_pages, s->page_size, stream)
+                         : launch_paged_attn_simt(a, stream));
 }

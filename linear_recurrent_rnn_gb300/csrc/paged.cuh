@@ -73,7 +73,7 @@ __device__ __forceinline__ PgReq pg_request(const PagedArgs& a, int n) {
   const int s = min(max(a.cu[n], 0), a.T), e = min(max(a.cu[n + 1], s), a.T);
   r.first = s;
   r.q = e - s;
-  r.kv = max(a.kv_lens[n], 0);
+  r.kv = min(max(a.kv_lens[n], 0), 1 << 30);
   return r;
 }
 
@@ -238,8 +238,11 @@ struct PgWalk {
   __device__ __forceinline__ static int slot(int c, int first) { return 2 * c + (c == first); }
 };
 
-// CUDA-core attention (paged_attn_simt.cu): launches on `s`; bytes of its workspace.
-cudaError_t launch_paged_attn_simt(PagedArgs a, int io, cudaStream_t s);
+// Tensor-core attention (paged_attn_tc.cu, bf16 I/O).
+cudaError_t launch_paged_attn_tc(PagedArgs a, int num_pages, int page_size, cudaStream_t s);
+size_t paged_attn_tc_ws_bytes(const paged_shape* s);
+// CUDA-core attention (paged_attn_simt.cu, float32 I/O).
+cudaError_t launch_paged_attn_simt(PagedArgs a, cudaStream_t s);
 size_t paged_attn_simt_ws_bytes(const paged_shape* s);
 
 // One kernel on `s` with programmatic stream serialisation (and clusters of `cluster` CTAs).

@@ -20,17 +20,9 @@ constexpr int SA_THREADS = 256;
 constexpr int SA_BN = 64;
 
 __device__ __forceinline__ float4 sa_load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 sa_load4(const bf16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
-__device__ __forceinline__ void sa_store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void sa_store(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 // BM rows, DP columns (D rounded up).  Threads: TX along keys / columns, TY along rows, 4 rows a
 // thread.
-template <typename T, int BM, int DP>
+template <int BM, int DP>
 struct Sa {
   static constexpr int TY = BM / 4, TX = SA_THREADS / TY;
   static constexpr int KS = SA_BN / TX;        // keys a thread
@@ -40,9 +32,9 @@ struct Sa {
   static constexpr size_t smem = (size_t)((BM + 2 * SA_BN) * LD + BM * LS + 3 * BM) * 4;
 };
 
-template <typename T, int BM, int DP>
+template <int BM, int DP>
 __global__ void __launch_bounds__(SA_THREADS) k_paged_attn_simt(const PagedArgs a) {
-  using C = Sa<T, BM, DP>;
+  using C = Sa<BM, DP>;
   extern __shared__ float sa_sm[];
   float* s_q = sa_sm;
   float* s_k = s_q + BM * C::LD;
@@ -77,7 +69,7 @@ __global__ void __launch_bounds__(SA_THREADS) k_paged_attn_simt(const PagedArgs 
       const int r = i / (DP / 4), c = i % (DP / 4);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows && c < dv)
-        x = sa_load4(static_cast<const T*>(a.q) + (int64_t)(it.r.first + t0 + r / a.g) * a.q_token +
+        x = sa_load4(static_cast<const float*>(a.q) + (int64_t)(it.r.first + t0 + r / a.g) * a.q_token +
                      (int64_t)(it.h * a.g + r % a.g) * a.q_head + 4 * c);
       *reinterpret_cast<float4*>(s_q + r * C::LD + 4 * c) = x;
     }
@@ -101,8 +93,8 @@ __global__ void __launch_bounds__(SA_THREADS) k_paged_attn_simt(const PagedArgs 
           const int64_t pg = pos >> a.ps_log2, off = pos & ((1 << a.ps_log2) - 1);
           const int id = pg < a.table_width ? a.table[(int64_t)it.n * a.table_width + pg] : -1;
           if (id >= 0 && id < a.P) {
-            k = sa_load4(static_cast<const T*>(a.kc) + id * a.kc_page + off * a.kc_token + it.h * a.kc_head + 4 * c);
-            v = sa_load4(static_cast<const T*>(a.vc) + id * a.vc_page + off * a.vc_token + it.h * a.vc_head + 4 * c);
+            k = sa_load4(static_cast<const float*>(a.kc) + id * a.kc_page + off * a.kc_token + it.h * a.kc_head + 4 * c);
+            v = sa_load4(static_cast<const float*>(a.vc) + id * a.vc_page + off * a.vc_token + it.h * a.vc_head + 4 * c);
           }
         }
         *reinterpret_cast<float4*>(s_k + r * C::LD + 4 * c) = k;
@@ -251,11 +243,11 @@ __global__ void __launch_bounds__(SA_THREADS) k_paged_attn_simt(const PagedArgs 
         const int64_t t = it.r.first + t0 + r / a.g;
         const int hq = it.h * a.g + r % a.g;
         const float inv = l[i] > 0.0f ? 1.0f / l[i] : l[i] == 0.0f ? 0.0f : l[i];
-        T* o = static_cast<T*>(a.o) + t * a.o_token + hq * a.o_head;
+        float* o = static_cast<float*>(a.o) + t * a.o_token + hq * a.o_head;
 #pragma unroll
         for (int c = 0; c < C::CS; ++c) {
           const int col = tx + C::TX * c;
-          if (col < a.D) sa_store(o + col, acc[i][c] * inv);
+          if (col < a.D) o[col] = acc[i][c] * inv;
         }
         if (a.lse && tx == 0)
           a.lse[t * a.Hq + hq] = l[i] == 0.0f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
@@ -265,11 +257,11 @@ __global__ void __launch_bounds__(SA_THREADS) k_paged_attn_simt(const PagedArgs 
   } while (w.next(a));
 }
 
-template <typename T, int BM, int DP>
+template <int BM, int DP>
 cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
-  using C = Sa<T, BM, DP>;
+  using C = Sa<BM, DP>;
   const size_t smem = std::max(C::smem, (size_t)(a.N + 1) * 8);
-  const void* f = reinterpret_cast<const void*>(k_paged_attn_simt<T, BM, DP>);
+  const void* f = reinterpret_cast<const void*>(k_paged_attn_simt<BM, DP>);
   cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const PagedWs L = paged_ws(sms, BM, DP);
@@ -281,19 +273,19 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   return launch_pdl(f, dim3(sms), dim3(SA_THREADS), smem, s, args, 1);
 }
 
-template <typename T, int BM>
+template <int BM>
 cudaError_t run_d(PagedArgs& a, cudaStream_t s, int sms) {
-  if (a.D <= 64) return run<T, BM, 64>(a, s, sms);
-  if (a.D <= 128) return run<T, BM, 128>(a, s, sms);
-  return run<T, BM, 256>(a, s, sms);
+  if (a.D <= 64) return run<BM, 64>(a, s, sms);
+  if (a.D <= 128) return run<BM, 128>(a, s, sms);
+  return run<BM, 256>(a, s, sms);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attn_simt(PagedArgs a, int io, cudaStream_t s) {
+cudaError_t launch_paged_attn_simt(PagedArgs a, cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1 || sms > PG_MAX_CTAS) return cudaErrorNotSupported;
-  return io == RGLRU_BF16 ? run_d<bf16, 64>(a, s, sms) : run_d<float, 64>(a, s, sms);
+  return run_d<64>(a, s, sms);
 }
 
 size_t paged_attn_simt_ws_bytes(const paged_shape* s) {

@@ -1,0 +1,738 @@
+// Attention over the paged cache on the tensor cores (bf16 I/O): tcgen05 MMAs with accumulators
+// and softmax weights in TMEM, operands by TMA.
+//
+// One pass over the keys with a running maximum and sum.  Per row tile (up to 128 rows: whole
+// tokens x the g query heads of one key/value head) and per tile of 128 keys
+//   S = Q K^T               Q, K from shared memory, S in TMEM, float32
+//   P = 2^(c S - c m)       c = scale log2 e; one thread a row, P back to TMEM as bf16
+//   O += P V                P from TMEM, V from shared memory, O in TMEM, float32
+// with l the float32 sum of P before its rounding to bf16.  The rounding of P (relative 2^-9
+// each, as V's own storage) is what lets the second product run on the tensor cores; sums and
+// statistics stay in float32.  m is moved only when a row's maximum has grown by more than 2^8
+// in weight (O and l are then scaled): weights up to 2^8 keep bf16's relative precision, and the
+// rescaling of O, a round trip through TMEM, becomes rare.
+//
+// Width D <= 128: two row tiles a CTA share every key tile and alternate on the tensor cores, so
+// that one's softmax runs behind the other's products (TMEM: two S/P of 128 columns, two O of
+// D).  D <= 256: one row tile, two S buffers, the next tile's S computed behind this one's
+// softmax.  Warps: 4 softmax warps a row tile, then key/value loader, MMA issuer, query loader.
+//
+// Pages: a key tile is copied page by page, one box of rows per page and 64 columns (128-byte
+// swizzle).  A page that the tile does not need, or whose table entry is outside the cache,
+// is copied from outside the tensor map, which gives zeros: the byte count of a stage is
+// always the same, and nothing outside the cache is read.  Rows of V past the request's keys
+// (or before its window) are cleared in shared memory, so that stale or non-finite cache
+// contents cannot reach a product with a zero weight; scores of such keys are replaced.
+//
+// Work is divided over the CTAs by weight (paged.cuh): one CTA per SM, each with a list of
+// items of which the first and the last may be shared with its neighbours.
+#include <algorithm>
+
+#include "host_util.h"
+#include "paged.cuh"
+#include "tc.cuh"
+
+namespace rglru {
+
+namespace {
+
+constexpr int TA_BN = 128;                     // keys of a tile
+constexpr uint64_t TA_WAIT_NS = 2000000000ull;
+constexpr uint32_t TA_SLAB = 128 * 128;        // 64 columns of 128 rows
+
+template <int DP>
+struct Ta {
+  static constexpr int NT = DP == 256 ? 1 : 2;        // row tiles
+  static constexpr int SLABS = DP / 64;
+  static constexpr int UPT = DP == 256 ? 2 : 1;       // ring units of a key (or value) tile
+  static constexpr uint32_t UB = DP == 64 ? TA_SLAB : 2 * TA_SLAB;
+  static constexpr int STAGES = DP == 64 ? 10 : 5;
+  static constexpr int VROWS = TA_BN / UPT;           // rows of V in a unit
+  static constexpr uint32_t VSLAB = VROWS * 128;
+  static constexpr int SOFT = NT * 128;               // softmax threads
+  static constexpr int THREADS = SOFT + 128;
+  static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P buffers b at 128 b, O tiles
+  static constexpr size_t Q_BYTES = (size_t)NT * SLABS * TA_SLAB;
+  static constexpr size_t smem = 1024 + Q_BYTES + STAGES * UB + 512;
+};
+
+struct TaAbort {
+  uint32_t* flag;   // shared: set once a wait has run out
+  uint32_t* status; // global
+  // By a converged warp; the answer is the same in all its lanes.
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+    bool ok = tc::mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, ok || slow(bar, parity));
+    return ok;
+  }
+  __device__ bool slow(uint64_t* bar, uint32_t parity) const {
+    const uint64_t t0 = tc::global_ns();
+    while (!tc::mbar_try_wait_sleep(bar, parity, 20000u)) {
+      if (*reinterpret_cast<volatile uint32_t*>(flag)) return false;
+      if (tc::global_ns() - t0 > TA_WAIT_NS) {
+        *reinterpret_cast<volatile uint32_t*>(flag) = 1u;
+        *reinterpret_cast<volatile uint32_t*>(status) = 1u;
+        return false;
+      }
+    }
+    return true;
+  }
+};
+
+// Row tile t of an item and its key tiles within the CTA's part.
+struct TaTile {
+  int tok, rows, ja, jb;
+};
+__device__ __forceinline__ TaTile ta_tile(const PagedArgs& a, const PgItem& it, int t, int tb1, int j0, int j1) {
+  TaTile x;
+  x.tok = it.m * a.tb + t * tb1;
+  const int nt = min(tb1, it.r.q - x.tok);
+  x.rows = max(nt, 0) * a.g;
+  const int64_t base = (int64_t)it.r.kv - it.r.q + x.tok;
+  const int hi = (int)max(base + nt, (int64_t)0);
+  const int lo = a.window ? (int)max(base - a.window + 1, (int64_t)0) : 0;
+  x.ja = max(j0, lo / TA_BN);
+  x.jb = min(j1, (hi + TA_BN - 1) / TA_BN);
+  if (x.rows == 0 || x.jb < x.ja) x.jb = x.ja;
+  return x;
+}
+
+__device__ __forceinline__ float ta_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two float32 operations in one instruction
+__device__ __forceinline__ float2 ta_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 ta_add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ uint32_t ta_pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void ta_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// One row's results joined over the CTAs [c0, c1] of an item, by all softmax threads: a thread
+// takes one row and a run of columns.
+template <int DP>
+__device__ __noinline__ void ta_join(const PagedArgs& a, const PgItem& it, int tb1, int c0, int c1, int tid) {
+  using C = Ta<DP>;
+  const float2* ml = reinterpret_cast<const float2*>(a.ws + a.part_ml);
+  const float* po = reinterpret_cast<const float*>(a.ws + a.part_o);
+  const int R = C::NT * 128;
+  // rows in use: of tile 0, and past 128 of tile 1
+  const int n1 = min(it.r.q - it.m * a.tb, tb1) * a.g;
+  const int n2 = C::NT == 2 ? max(min(it.r.q - it.m * a.tb - tb1, tb1), 0) * a.g : 0;
+  const int used = n2 > 0 ? 128 + n2 : n1;
+  int rp = C::SOFT * 8 / DP;
+  while (rp < used) rp <<= 1;
+  const int groups = C::SOFT / rp, cols = DP / groups;
+  const int row = tid & (rp - 1), col0 = tid / rp * cols;
+  if (row >= used || (row < 128 && row >= n1)) return;
+  float m = -INFINITY;
+  for (int c = c0; c <= c1; ++c) {
+    const float2 x = __ldcg(ml + (size_t)PgWalk::slot(c, c0) * R + row);
+    if (x.y != 0.0f) m = fmaxf(m, x.x);
+  }
+  float l = 0.0f;
+  for (int c = c0; c <= c1; ++c) {
+    const float2 x = __ldcg(ml + (size_t)PgWalk::slot(c, c0) * R + row);
+    if (x.y != 0.0f) l += x.y * ta_ex2(x.x - m);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int t = row >> 7, r = row & 127;
+  const int64_t tok = it.r.first + it.m * a.tb + t * tb1 + r / a.g;
+  const int hq = it.h * a.g + r % a.g;
+  bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
+  for (int k = col0; k < col0 + cols && k < a.D; k += 8) {
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+#pragma unroll 2
+    for (int c = c0; c <= c1; ++c) {
+      const size_t s = (size_t)PgWalk::slot(c, c0);
+      const float2 x = __ldcg(ml + s * R + row);
+      if (x.y == 0.0f) continue;  // saw nothing: its sums were not written
+      const float f = ta_ex2(x.x - m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(__ldcg(po + (s * DP + k + e) * R + row), f, acc[e]);
+    }
+    uint4 u;
+    u.x = ta_pack(acc[0] * inv, acc[1] * inv);
+    u.y = ta_pack(acc[2] * inv, acc[3] * inv);
+    u.z = ta_pack(acc[4] * inv, acc[5] * inv);
+    u.w = ta_pack(acc[6] * inv, acc[7] * inv);
+    *reinterpret_cast<uint4*>(o + k) = u;
+  }
+  if (a.lse && col0 == 0)
+    a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
+    k_paged_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
+  using C = Ta<DP>;
+  constexpr int NT = C::NT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* s_q = smem;
+  uint8_t* s_ring = s_q + C::Q_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_ring + C::STAGES * C::UB);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* q_full = empty + C::STAGES;  // [NT]
+  uint64_t* q_empty = q_full + NT;       // [NT]
+  uint64_t* s_full = q_empty + NT;       // [2]  S of buffer b complete
+  uint64_t* p_full = s_full + 2;         // [2]  P of buffer b written (and O scaled)
+  uint64_t* pv_done = p_full + 2;        // [NT] a product P V of tile t complete
+  uint64_t* o_empty = pv_done + NT;      // [NT] O of tile t read
+  uint64_t* j_full = o_empty + NT;       // a part of an item is in the workspace
+  uint64_t* j_go = j_full + 1;           // s_last says whether this CTA joins the item
+  uint64_t* drain = j_go + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* s_flag = tmem_holder + 1;
+  uint32_t* s_last = tmem_holder + 2;
+  __shared__ int64_t scratch[33];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tb1 = max(1, 128 / a.g);  // tokens of a row tile
+  const TaAbort ctl{s_flag, reinterpret_cast<uint32_t*>(a.ws)};
+
+  // up to griddep_wait nothing touches global memory
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < NT; ++i) {
+      tc::mbar_init(&q_full[i], 1);
+      tc::mbar_init(&q_empty[i], 1);
+      tc::mbar_init(&pv_done[i], 1);
+      tc::mbar_init(&o_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&p_full[i], 4);
+    }
+    tc::mbar_init(j_full, C::SOFT / 32);
+    tc::mbar_init(j_go, 1);
+    tc::mbar_init(drain, 1);
+    *s_flag = 0u;
+    tc::fence_barrier_init();
+    tc::prefetch_tmap(&tm_q);
+    tc::prefetch_tmap(&tm_k);
+    tc::prefetch_tmap(&tm_v);
+  }
+  if (warp == C::SOFT / 32 + 1) {
+    tc::tmem_alloc(tmem_holder, 512);
+    tc::tmem_relinquish();
+  }
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  PgWalk w;
+  int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
+  pg_scan(a, prefix, scratch);
+  bool more = w.start(a, prefix);
+  tc::fence_proxy_async_smem();
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  const int role = warp - C::SOFT / 32;  // < 0: softmax; 0: keys and values, 1: MMA, 2: queries
+  if (role == 0) {
+    // ------------------------------------------------------------ key / value loader
+    const int ps = 1 << a.ps_log2;
+    uint32_t st = 0, ph = 1;  // stage, parity of its `empty` wait
+    uint32_t issued = 0;
+    bool ok = true;
+    while (more && ok) {
+      int j0, j1;
+      w.tiles(TA_BN, j0, j1);
+      const PgItem& it = w.it;
+      const int32_t* row = a.table + (int64_t)it.n * a.table_width;
+      // page of lane i in key tile j (lanes past the tile's pages: unused)
+      const int ppt = max(1, TA_BN >> a.ps_log2);
+      auto page_of = [&](int j) {
+        const int pos = j * TA_BN + (lane << a.ps_log2), pg = pos >> a.ps_log2;
+        if (j >= j1 || lane >= ppt || pos >= it.hi || pos + ps <= it.lo || pg >= a.table_width) return a.P;
+        const int id = row[pg];
+        return id >= 0 && id < a.P ? id : a.P;  // a.P: outside the map, zeros
+      };
+      // one ring unit: rows [r0, r0 + nr) of tile j, columns from slab s0
+      auto unit = [&](const CUtensorMap* tm, int j, int id, int r0, int nr, int s0, int ns, uint32_t slab_b) {
+        if (!ctl.wait(&empty[st], ph)) return false;
+        if (lane == 0) tc::mbar_expect_tx(&full[st], C::UB);
+        __syncwarp();
+        const int bx = min(ps, nr);  // rows of a box
+        const int first = r0 >> a.ps_log2, n = max(1, nr >> a.ps_log2);
+        const int i = lane - (ps >= TA_BN ? 0 : first);
+        if (i >= 0 && i < n) {
+          uint8_t* dst = s_ring + st * C::UB + i * bx * 128;
+          const int off = ps > nr ? (j * TA_BN + r0) & (ps - 1) : 0;
+          for (int s = 0; s < ns; ++s)
+            tc::tma_load_4d(dst + s * slab_b, tm, &full[st], (s0 + s) * 64, off, it.h, id);
+        }
+        __syncwarp();
+        ++issued;
+        if (++st == C::STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+        return true;
+      };
+      int id_prev = a.P, id = page_of(j0);
+      for (int j = j0; j <= j1 && ok; ++j) {
+        const int id_next = page_of(j + 1);
+        auto keys = [&] {
+          for (int u = 0; u < C::UPT && ok; ++u)
+            ok = unit(&tm_k, j, id, 0, TA_BN, 2 * u, C::SLABS / C::UPT, TA_SLAB);
+        };
+        auto values = [&] {
+          for (int u = 0; u < C::UPT && ok; ++u) {
+            // (a page of 128 rows or more is lane 0's for every unit)
+            ok = unit(&tm_v, j - 1, id_prev, u * C::VROWS, C::VROWS, 0, C::SLABS, C::VSLAB);
+          }
+        };
+        if (j1 > j0) {
+          if (NT == 1 && j < j1) keys();
+          if (j > j0) values();
+          if (NT == 2 && j < j1) keys();
+        }
+        id_prev = id;
+        id = id_next;
+      }
+      more = w.next(a);
+    }
+    if (!ok) {  // copies in flight land before the CTA leaves
+      for (uint32_t i = 0; i < min(issued, (uint32_t)C::STAGES); ++i) {
+        const uint32_t n = issued - 1 - i;
+        tc::mbar_wait(&full[n % C::STAGES], (n / C::STAGES) & 1, TA_WAIT_NS);
+      }
+    }
+  } else if (role == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = tc::elect_one();
+    constexpr uint32_t id_qk = tc::idesc_bf16(128, TA_BN, 0, 0);
+    constexpr uint32_t id_pv = tc::idesc_bf16(128, DP, 0, 1);
+    const uint32_t q_addr = tc::smem_u32(s_q), r_addr = tc::smem_u32(s_ring);
+    uint32_t st = 0, ph = 0;        // next ring unit, parity of its `full`
+    uint32_t nq[NT] = {}, no[NT] = {};  // items of tile t so far: queries taken, O begun
+    uint32_t cs[NT] = {}, cp[NT] = {};  // S of tile t issued, P taken
+    bool ok = true;
+    while (more && ok) {
+      int j0, j1;
+      w.tiles(TA_BN, j0, j1);
+      const PgItem& it = w.it;
+      TaTile tl[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) tl[t] = ta_tile(a, it, t, tb1, j0, j1);
+      // step j: the products P V of key tile j - 1 and Q K^T of key tile j (in the order in which
+      // the loader fills the ring)
+      for (int j = j0; j <= j1 && ok && j0 < j1; ++j) {
+        uint32_t v_st = 0, k_st = 0;
+        bool v_in = false, k_in = false;
+        auto take = [&](uint32_t& first) {
+          first = st;
+#pragma unroll
+          for (int u = 0; u < C::UPT; ++u) {
+            if (ok) ok = ctl.wait(&full[st], ph);
+            if (++st == C::STAGES) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+        };
+        auto take_k = [&] {
+          if (!k_in) take(k_st);
+          k_in = true;
+        };
+        auto take_v = [&] {
+          if (v_in) return;
+          take(v_st);
+          v_in = true;
+          const int p0 = (j - 1) * TA_BN;
+          if (ok && (p0 + TA_BN > it.hi || p0 < it.lo)) {
+            for (int i = lane; i < TA_BN * (DP / 8); i += 32) {
+              const int r = i / (DP / 8), c = i % (DP / 8);  // row, 16-byte piece of it
+              if (p0 + r >= it.hi || p0 + r < it.lo) {
+                const uint32_t u = (v_st + r / C::VROWS) % C::STAGES;
+                *reinterpret_cast<uint4*>(s_ring + u * C::UB + c / 8 * C::VSLAB + r % C::VROWS * 128 +
+                                          c % 8 * 16) = make_uint4(0, 0, 0, 0);
+              }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+          }
+        };
+        auto qk = [&](int t) {
+          take_k();
+          if (ok && j == tl[t].ja) ok = ctl.wait(&q_full[t], nq[t]++ & 1);
+          if (!ok) return;
+          const int b = NT == 2 ? t : cs[t] & 1;
+          ++cs[t];
+          tc::tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+              const uint32_t u = (k_st + k / 8) % C::STAGES;
+              const uint32_t off = (k % 8) / 4 * TA_SLAB + (k % 4) * 32;
+              tc::mma_bf16(tmem + C::S_COL + b * 128,
+                           tc::smem_desc(q_addr + (t * C::SLABS + k / 4) * TA_SLAB + (k % 4) * 32, 16, 1024,
+                                         tc::LAYOUT_SW128),
+                           tc::smem_desc(r_addr + u * C::UB + off, 16, 1024, tc::LAYOUT_SW128), id_qk, k > 0);
+            }
+            tc::mma_commit(&s_full[b]);
+            if (j == tl[t].jb - 1) tc::mma_commit(&q_empty[t]);
+          }
+          __syncwarp();
+        };
+        auto pv = [&](int t) {
+          take_v();
+          const int b = NT == 2 ? t : cp[t] & 1;
+          if (ok) ok = ctl.wait(&p_full[b], (NT == 2 ? cp[t] : cp[t] >> 1) & 1);
+          ++cp[t];
+          if (ok && j - 1 == tl[t].ja) ok = ctl.wait(&o_empty[t], (no[t]++ & 1) ^ 1);
+          if (!ok) return;
+          tc::tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < TA_BN / 16; ++k) {
+              const uint32_t u = (v_st + k * 16 / C::VROWS) % C::STAGES;
+              ta_mma_ts(tmem + C::O_COL + t * DP, tmem + C::S_COL + b * 128 + k * 8,
+                        tc::smem_desc(r_addr + u * C::UB + k * 16 % C::VROWS * 128, C::VSLAB, 1024,
+                                      tc::LAYOUT_SW128),
+                        id_pv, j - 1 > tl[t].ja || k > 0);
+            }
+            tc::mma_commit(&pv_done[t]);
+          }
+          __syncwarp();
+        };
+        if (NT == 1) {
+          if (j < j1) qk(0);
+          if (j > j0 && ok) pv(0);
+        } else {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (ok && j > tl[t].ja && j <= tl[t].jb) pv(t);
+            if (ok && j >= tl[t].ja && j < tl[t].jb) qk(t);
+          }
+        }
+        // what no tile used is passed over, so that the ring stays in step
+        if (ok && j > j0) take_v();
+        if (ok && j < j1) take_k();
+        if (leader && ok) {
+#pragma unroll
+          for (int u = 0; u < C::UPT; ++u) {
+            if (v_in) tc::mma_commit(&empty[(v_st + u) % C::STAGES]);
+            if (k_in) tc::mma_commit(&empty[(k_st + u) % C::STAGES]);
+          }
+        }
+        __syncwarp();
+      }
+      more = w.next(a);
+    }
+    if (!ok) {  // MMAs in flight end before TMEM is freed
+      if (leader) tc::mma_commit(drain);
+      __syncwarp();
+      tc::mbar_wait(drain, 0, TA_WAIT_NS);
+    }
+  } else if (role == 2) {
+    // ------------------------------------------------------------ query loader
+    uint32_t n[NT] = {};
+    const uint32_t bytes = C::SLABS * tb1 * a.g * 128;
+    bool ok = true;
+    while (more && ok) {
+      int j0, j1;
+      w.tiles(TA_BN, j0, j1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const TaTile x = ta_tile(a, w.it, t, tb1, j0, j1);
+        if (x.jb == x.ja || !ok) continue;
+        ok = ctl.wait(&q_empty[t], (n[t]++ & 1) ^ 1);
+        if (ok && lane == 0) {
+          tc::mbar_expect_tx(&q_full[t], bytes);
+          for (int s = 0; s < C::SLABS; ++s)
+            tc::tma_load_3d(s_q + (t * C::SLABS + s) * TA_SLAB, &tm_q, &q_full[t], s * 64, w.it.h * a.g,
+                            w.it.r.first + x.tok);
+        }
+        __syncwarp();
+      }
+      more = w.next(a);
+    }
+    if (!ok)
+      for (int t = 0; t < NT; ++t)
+        if (n[t]) tc::mbar_wait(&q_full[t], (n[t] - 1) & 1, TA_WAIT_NS);
+  } else if (role < 0) {
+    // ------------------------------------------------------------ softmax, one row a thread
+    const int t = NT == 2 ? warp >> 2 : 0, wq = warp & 3, r = wq * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t t_o = lanes + C::O_COL + t * DP;
+    const float sc = a.scale_log2;
+    uint32_t cs = 0, npv = 0, nj = 0;  // S taken, products P V of this tile, joins
+    bool ok = true;
+    while (more && ok) {
+      int j0, j1;
+      w.tiles(TA_BN, j0, j1);
+      const TaTile tl = ta_tile(a, w.it, t, tb1, j0, j1);
+      const bool live = wq * 32 < tl.rows;  // any row of the warp
+      const int base = w.it.r.kv - w.it.r.q + tl.tok;
+      const int pos = base + min(r, max(tl.rows - 1, 0)) / a.g;
+      // positions of the warp's first and last row: tiles between need no mask
+      const int p_first = base + wq * 32 / a.g, p_last = base + min(wq * 32 + 31, max(tl.rows - 1, 0)) / a.g;
+      float m = -INFINITY, l = 0.0f;  // in units of the scores; the sum at that maximum
+      for (int j = tl.ja; j < tl.jb; ++j) {
+        const int b = NT == 2 ? t : cs & 1;
+        ok = ctl.wait(&s_full[b], (NT == 2 ? cs : cs >> 1) & 1);
+        ++cs;
+        if (!ok) break;
+        tc::tc_fence_after();
+        bool waited = j == tl.ja;  // NT = 1: for the product before this one
+        if (live) {
+          float s[128];
+          const uint32_t t_s = lanes + C::S_COL + b * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) tc::tmem_ld16(t_s + 16 * c, *reinterpret_cast<float(*)[16]>(s + 16 * c));
+          tc::tmem_ld_wait();
+          tc::reg_fence(s);
+          const int k0 = j * TA_BN;
+          if (k0 + TA_BN - 1 > p_first || (a.window && k0 < p_last - a.window + 1)) {
+            const int hi = pos - k0, lo = a.window ? hi - a.window : -1;  // lo < column <= hi
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = c <= hi && c > lo ? s[c] : -INFINITY;
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < 128; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              mx[e] = fmaxf(mx[e], s[c + e]);
+              if (c + 4 + e < 128) mx[e] = fmaxf(mx[e], s[c + 4 + e]);
+            }
+          const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if (j == tl.ja) {
+            m = top;
+          } else if (__any_sync(0xffffffffu, (top - m) * sc > 8.0f)) {
+            const float f = top == m ? 1.0f : ta_ex2((top - m) * -sc);
+            l *= f;
+            m = top;
+            if (NT == 1) {
+              ok = ctl.wait(&pv_done[0], (npv + (j - tl.ja) - 1) & 1);
+              waited = true;
+              if (!ok) break;
+              tc::tc_fence_after();
+            }
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 16) {
+              float o[16];
+              tc::tmem_ld16(t_o + c, o);
+              tc::tmem_ld_wait();
+              tc::reg_fence(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tc::tmem_st16(t_o + c, o);
+            }
+          }
+          const float off = m == -INFINITY ? 0.0f : -m * sc;
+          float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            float pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 x = ta_fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), make_float2(sc, sc),
+                                       make_float2(off, off));
+              const float2 p = make_float2(ta_ex2(x.x), ta_ex2(x.y));
+              sum[e & 1] = ta_add2(sum[e & 1], p);
+              pk[e] = __uint_as_float(ta_pack(p.x, p.y));
+            }
+            tc::tmem_st16(t_s + c / 2, pk);
+          }
+          const float2 s2 = ta_add2(sum[0], sum[1]);
+          l += s2.x + s2.y;
+          tc::tmem_st_wait();
+        }
+        if (NT == 1 && !waited) {
+          ok = ctl.wait(&pv_done[0], (npv + (j - tl.ja) - 1) & 1);
+          if (!ok) break;
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[b]);
+      }
+      if (!ok) break;
+      const bool any = tl.jb > tl.ja;
+      if (any) {
+        npv += tl.jb - tl.ja;
+        ok = ctl.wait(&pv_done[t], (npv - 1) & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+      }
+      const bool mine = r < tl.rows;
+      const int row = t * 128 + r;
+      if (w.whole()) {
+        if (live) {
+          const int64_t tok = w.it.r.first + tl.tok + (mine ? r / a.g : 0);
+          const int hq = w.it.h * a.g + (mine ? r % a.g : 0);
+          bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+          for (int c = 0; c < DP && c < a.D; c += 16) {
+            float v[16];
+            if (any) {
+              tc::tmem_ld16(t_o + c, v);
+              tc::tmem_ld_wait();
+              tc::reg_fence(v);
+            }
+            uint32_t u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              u[e] = l == 0.0f ? 0u : ta_pack(v[2 * e] * inv, v[2 * e + 1] * inv);
+            if (mine) {
+              *reinterpret_cast<uint4*>(o + c) = make_uint4(u[0], u[1], u[2], u[3]);
+              if (c + 8 < a.D) *reinterpret_cast<uint4*>(o + c + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+            }
+          }
+          if (mine && a.lse)
+            a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m * sc + log2f(l)) * 0.69314718055994531f;
+        }
+        if (any) {
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&o_empty[t]);
+        }
+      } else {
+        // a part: maxima, sums and unscaled O to the workspace; the last CTA of the item joins them
+        int c0, c1;
+        w.owners(c0, c1);
+        const size_t slot = (size_t)PgWalk::slot(w.cta, c0);
+        const int R = NT * 128;
+        if (live) {
+          if (mine)
+            reinterpret_cast<float2*>(a.ws + a.part_ml)[slot * R + row] =
+                make_float2(m == -INFINITY ? m : m * sc, l);
+          if (any) {
+            float* po = reinterpret_cast<float*>(a.ws + a.part_o) + slot * DP * R + row;
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 16) {
+              float v[16];
+              tc::tmem_ld16(t_o + c, v);
+              tc::tmem_ld_wait();
+              tc::reg_fence(v);
+              if (mine)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) po[(size_t)(c + e) * R] = v[e];
+            }
+          }
+        }
+        if (any) tc::tc_fence_before();
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+          if (any) tc::mbar_arrive(&o_empty[t]);
+          tc::mbar_arrive(j_full);
+        }
+        if (warp == 0) {
+          ok = ctl.wait(j_full, nj & 1);
+          if (!ok) break;
+          if (lane == 0) {
+            __threadfence();
+            uint32_t* cnt = reinterpret_cast<uint32_t*>(a.ws + 256) + c0;
+            const bool last = atomicAdd(cnt, 1u) == (uint32_t)(c1 - c0);
+            if (last) *cnt = 0u;  // as it was found: zero between calls
+            *reinterpret_cast<volatile uint32_t*>(s_last) = last;
+            tc::mbar_arrive(j_go);
+          }
+          __syncwarp();
+        }
+        ok = ctl.wait(j_go, nj & 1);
+        if (!ok) break;
+        ++nj;
+        if (*reinterpret_cast<volatile uint32_t*>(s_last)) {
+          __threadfence();
+          ta_join<DP>(a, w.it, tb1, c0, c1, tid);
+        }
+      }
+      more = w.next(a);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == C::SOFT / 32 + 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DP>
+cudaError_t run(PagedArgs& a, int P, int ps, cudaStream_t s, int sms) {
+  using C = Ta<DP>;
+  const int tb1 = std::max(1, 128 / a.g);
+  CUtensorMap mq, mk, mv;
+  const uint64_t dq[3] = {(uint64_t)a.D, (uint64_t)a.Hq, (uint64_t)a.T};
+  const uint64_t sq[2] = {(uint64_t)a.q_head * 2, (uint64_t)a.q_token * 2};
+  const uint32_t bq[3] = {64, (uint32_t)a.g, (uint32_t)tb1};
+  cudaError_t e = encode_tmap(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dq, sq, bq,
+                              CU_TENSOR_MAP_SWIZZLE_128B);
+  const uint64_t dk[4] = {(uint64_t)a.D, (uint64_t)ps, (uint64_t)a.Hkv, (uint64_t)P};
+  const uint64_t sk[3] = {(uint64_t)a.kc_token * 2, (uint64_t)a.kc_head * 2, (uint64_t)a.kc_page * 2};
+  const uint64_t sv[3] = {(uint64_t)a.vc_token * 2, (uint64_t)a.vc_head * 2, (uint64_t)a.vc_page * 2};
+  const uint32_t bk[4] = {64, (uint32_t)std::min(ps, TA_BN), 1, 1};
+  const uint32_t bv[4] = {64, (uint32_t)std::min(ps, C::VROWS), 1, 1};
+  if (e == cudaSuccess)
+    e = encode_tmap(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.kc, dk, sk, bk, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e == cudaSuccess)
+    e = encode_tmap(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.vc, dk, sv, bv, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  const void* f = reinterpret_cast<const void*>(k_paged_attn<DP>);
+  e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem);
+  if (e != cudaSuccess) return e;
+  const PagedWs L = paged_ws(sms, C::NT * 128, DP);
+  a.part_ml = L.ml;
+  a.part_o = L.o;
+  a.rows = C::NT * 128;
+  a.tb = C::NT * tb1;
+  void* args[] = {&mq, &mk, &mv, &a};
+  return launch_pdl(f, dim3(sms), dim3(C::THREADS), C::smem, s, args, 1);
+}
+
+int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+}  // namespace
+
+cudaError_t launch_paged_attn_tc(PagedArgs a, int num_pages, int page_size, cudaStream_t s) {
+  const int sms = sm_count();
+  if (sms < 1 || sms > PG_MAX_CTAS) return cudaErrorNotSupported;
+  switch (dp_of(a.D)) {
+    case 64: return run<64>(a, num_pages, page_size, s, sms);
+    case 128: return run<128>(a, num_pages, page_size, s, sms);
+    default: return run<256>(a, num_pages, page_size, s, sms);
+  }
+}
+
+size_t paged_attn_tc_ws_bytes(const paged_shape* s) {
+  const int sms = sm_count(), dp = dp_of(s->D);
+  return paged_ws(sms > 0 ? sms : 256, dp == 256 ? 128 : 256, dp).total;
+}
+
+}  // namespace rglru
