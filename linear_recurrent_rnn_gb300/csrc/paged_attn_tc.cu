@@ -15,7 +15,8 @@
 // Width D <= 128: two row tiles a CTA share every key tile and alternate on the tensor cores, so
 // that one's softmax runs behind the other's products (TMEM: two S/P of 128 columns, two O of
 // D).  D <= 256: one row tile, two S buffers, the next tile's S computed behind this one's
-// softmax.  Warps: 4 softmax warps a row tile, then key/value loader, MMA issuer, query loader.
+// softmax.  Warps: 4 softmax warps a row tile, then key/value loader, MMA
+// issuer, query loader, and one that walks the CTA's items.
 //
 // Pages: a key tile is copied page by page, one box of rows per page and 64 columns (128-byte
 // swizzle).  A page that the tile does not need, or whose table entry is outside the cache,
@@ -27,6 +28,7 @@
 // Work is divided over the CTAs by weight (paged.cuh): one CTA per SM, each with a list of
 // items of which the first and the last may be shared with its neighbours.
 #include <algorithm>
+#include <atomic>
 
 #include "host_util.h"
 #include "paged.cuh"
@@ -79,20 +81,32 @@ struct TaAbort {
   }
 };
 
+// An item of the CTA's work as its warps read it: written by the walking warp into a ring in
+// shared memory, so that the walk's state costs the other warps no registers.
+struct TaItem {
+  int n, h;           // request (-1: no more items), key/value head
+  int first, q, kv;   // its first token row, new tokens, keys
+  int tok;            // the item's first token
+  int j0, j1;         // key tiles of the CTA's part
+  int lo, hi;         // keys that the item's rows see
+  int c0, c1, slot;   // CTAs that share the item, this one's partial-result slot
+};
+constexpr int TA_ITEMS = 4;
+
 // Row tile t of an item and its key tiles within the CTA's part.
 struct TaTile {
   int tok, rows, ja, jb;
 };
-__device__ __forceinline__ TaTile ta_tile(const PagedArgs& a, const PgItem& it, int t, int tb1, int j0, int j1) {
+__device__ __forceinline__ TaTile ta_tile(const PagedArgs& a, const TaItem& it, int t, int tb1) {
   TaTile x;
-  x.tok = it.m * a.tb + t * tb1;
-  const int nt = min(tb1, it.r.q - x.tok);
+  x.tok = it.tok + t * tb1;
+  const int nt = min(tb1, it.q - x.tok);
   x.rows = max(nt, 0) * a.g;
-  const int64_t base = (int64_t)it.r.kv - it.r.q + x.tok;
-  const int hi = (int)max(base + nt, (int64_t)0);
-  const int lo = a.window ? (int)max(base - a.window + 1, (int64_t)0) : 0;
-  x.ja = max(j0, lo / TA_BN);
-  x.jb = min(j1, (hi + TA_BN - 1) / TA_BN);
+  const int base = it.kv - it.q + x.tok;
+  const int hi = max(base + nt, 0);
+  const int lo = a.window && base >= a.window ? base - a.window + 1 : 0;
+  x.ja = max(it.j0, lo / TA_BN);
+  x.jb = min(it.j1, (hi + TA_BN - 1) / TA_BN);
   if (x.rows == 0 || x.jb < x.ja) x.jb = x.ja;
   return x;
 }
@@ -101,6 +115,11 @@ __device__ __forceinline__ float ta_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float ta_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // two float32 operations in one instruction
 __device__ __forceinline__ float2 ta_fma2(float2 a, float2 b, float2 c) {
@@ -136,14 +155,15 @@ __device__ __forceinline__ void ta_mma_ts(uint32_t d, uint32_t a, uint64_t b_des
 // One row's results joined over the CTAs [c0, c1] of an item, by all softmax threads: a thread
 // takes one row and a run of columns.
 template <int DP>
-__device__ __noinline__ void ta_join(const PagedArgs& a, const PgItem& it, int tb1, int c0, int c1, int tid) {
+__device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int tb1, int tid) {
+  const int c0 = it.c0, c1 = it.c1;
   using C = Ta<DP>;
   const float2* ml = reinterpret_cast<const float2*>(a.ws + a.part_ml);
   const float* po = reinterpret_cast<const float*>(a.ws + a.part_o);
   const int R = C::NT * 128;
   // rows in use: of tile 0, and past 128 of tile 1
-  const int n1 = min(it.r.q - it.m * a.tb, tb1) * a.g;
-  const int n2 = C::NT == 2 ? max(min(it.r.q - it.m * a.tb - tb1, tb1), 0) * a.g : 0;
+  const int n1 = min(it.q - it.tok, tb1) * a.g;
+  const int n2 = C::NT == 2 ? max(min(it.q - it.tok - tb1, tb1), 0) * a.g : 0;
   const int used = n2 > 0 ? 128 + n2 : n1;
   int rp = C::SOFT * 8 / DP;
   while (rp < used) rp <<= 1;
@@ -162,7 +182,7 @@ __device__ __noinline__ void ta_join(const PagedArgs& a, const PgItem& it, int t
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int t = row >> 7, r = row & 127;
-  const int64_t tok = it.r.first + it.m * a.tb + t * tb1 + r / a.g;
+  const int64_t tok = it.first + it.tok + t * tb1 + r / a.g;
   const int hq = it.h * a.g + r % a.g;
   bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
   for (int k = col0; k < col0 + cols && k < a.D; k += 8) {
@@ -209,11 +229,14 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   uint64_t* o_empty = pv_done + NT;      // [NT] O of tile t read
   uint64_t* j_full = o_empty + NT;       // a part of an item is in the workspace
   uint64_t* j_go = j_full + 1;           // s_last says whether this CTA joins the item
-  uint64_t* drain = j_go + 1;
+  uint64_t* i_full = j_go + 1;           // [TA_ITEMS] item records
+  uint64_t* i_empty = i_full + TA_ITEMS;
+  uint64_t* drain = i_empty + TA_ITEMS;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   uint32_t* s_flag = tmem_holder + 1;
   uint32_t* s_last = tmem_holder + 2;
   __shared__ int64_t scratch[33];
+  __shared__ TaItem s_item[TA_ITEMS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tb1 = max(1, 128 / a.g);  // tokens of a row tile
   const TaAbort ctl{s_flag, reinterpret_cast<uint32_t*>(a.ws)};
@@ -236,6 +259,10 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
     }
     tc::mbar_init(j_full, C::SOFT / 32);
     tc::mbar_init(j_go, 1);
+    for (int i = 0; i < TA_ITEMS; ++i) {
+      tc::mbar_init(&i_full[i], 1);
+      tc::mbar_init(&i_empty[i], C::SOFT / 32 + 3);
+    }
     tc::mbar_init(drain, 1);
     *s_flag = 0u;
     tc::fence_barrier_init();
@@ -249,241 +276,33 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   }
   tc::griddep_wait();
   tc::griddep_launch_dependents();
+  const int role = warp - C::SOFT / 32;  // < 0: softmax; 0: keys and values, 1: MMA, 2: queries, 3: walk
   PgWalk w;
   int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
   pg_scan(a, prefix, scratch);
-  bool more = w.start(a, prefix);
+  bool more = role == 3 && w.start(a, prefix);
   tc::fence_proxy_async_smem();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  const int role = warp - C::SOFT / 32;  // < 0: softmax; 0: keys and values, 1: MMA, 2: queries
-  if (role == 0) {
-    // ------------------------------------------------------------ key / value loader
-    const int ps = 1 << a.ps_log2;
-    uint32_t st = 0, ph = 1;  // stage, parity of its `empty` wait
-    uint32_t issued = 0;
-    bool ok = true;
-    while (more && ok) {
-      int j0, j1;
-      w.tiles(TA_BN, j0, j1);
-      const PgItem& it = w.it;
-      const int32_t* row = a.table + (int64_t)it.n * a.table_width;
-      // page of lane i in key tile j (lanes past the tile's pages: unused)
-      const int ppt = max(1, TA_BN >> a.ps_log2);
-      auto page_of = [&](int j) {
-        const int pos = j * TA_BN + (lane << a.ps_log2), pg = pos >> a.ps_log2;
-        if (j >= j1 || lane >= ppt || pos >= it.hi || pos + ps <= it.lo || pg >= a.table_width) return a.P;
-        const int id = row[pg];
-        return id >= 0 && id < a.P ? id : a.P;  // a.P: outside the map, zeros
-      };
-      // one ring unit: rows [r0, r0 + nr) of tile j, columns from slab s0
-      auto unit = [&](const CUtensorMap* tm, int j, int id, int r0, int nr, int s0, int ns, uint32_t slab_b) {
-        if (!ctl.wait(&empty[st], ph)) return false;
-        if (lane == 0) tc::mbar_expect_tx(&full[st], C::UB);
-        __syncwarp();
-        const int bx = min(ps, nr);  // rows of a box
-        const int first = r0 >> a.ps_log2, n = max(1, nr >> a.ps_log2);
-        const int i = lane - (ps >= TA_BN ? 0 : first);
-        if (i >= 0 && i < n) {
-          uint8_t* dst = s_ring + st * C::UB + i * bx * 128;
-          const int off = ps > nr ? (j * TA_BN + r0) & (ps - 1) : 0;
-          for (int s = 0; s < ns; ++s)
-            tc::tma_load_4d(dst + s * slab_b, tm, &full[st], (s0 + s) * 64, off, it.h, id);
-        }
-        __syncwarp();
-        ++issued;
-        if (++st == C::STAGES) {
-          st = 0;
-          ph ^= 1;
-        }
-        return true;
-      };
-      int id_prev = a.P, id = page_of(j0);
-      for (int j = j0; j <= j1 && ok; ++j) {
-        const int id_next = page_of(j + 1);
-        auto keys = [&] {
-          for (int u = 0; u < C::UPT && ok; ++u)
-            ok = unit(&tm_k, j, id, 0, TA_BN, 2 * u, C::SLABS / C::UPT, TA_SLAB);
-        };
-        auto values = [&] {
-          for (int u = 0; u < C::UPT && ok; ++u) {
-            // (a page of 128 rows or more is lane 0's for every unit)
-            ok = unit(&tm_v, j - 1, id_prev, u * C::VROWS, C::VROWS, 0, C::SLABS, C::VSLAB);
-          }
-        };
-        if (j1 > j0) {
-          if (NT == 1 && j < j1) keys();
-          if (j > j0) values();
-          if (NT == 2 && j < j1) keys();
-        }
-        id_prev = id;
-        id = id_next;
-      }
-      more = w.next(a);
-    }
-    if (!ok) {  // copies in flight land before the CTA leaves
-      for (uint32_t i = 0; i < min(issued, (uint32_t)C::STAGES); ++i) {
-        const uint32_t n = issued - 1 - i;
-        tc::mbar_wait(&full[n % C::STAGES], (n / C::STAGES) & 1, TA_WAIT_NS);
-      }
-    }
-  } else if (role == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    const bool leader = tc::elect_one();
-    constexpr uint32_t id_qk = tc::idesc_bf16(128, TA_BN, 0, 0);
-    constexpr uint32_t id_pv = tc::idesc_bf16(128, DP, 0, 1);
-    const uint32_t q_addr = tc::smem_u32(s_q), r_addr = tc::smem_u32(s_ring);
-    uint32_t st = 0, ph = 0;        // next ring unit, parity of its `full`
-    uint32_t nq[NT] = {}, no[NT] = {};  // items of tile t so far: queries taken, O begun
-    uint32_t cs[NT] = {}, cp[NT] = {};  // S of tile t issued, P taken
-    bool ok = true;
-    while (more && ok) {
-      int j0, j1;
-      w.tiles(TA_BN, j0, j1);
-      const PgItem& it = w.it;
-      TaTile tl[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) tl[t] = ta_tile(a, it, t, tb1, j0, j1);
-      // step j: the products P V of key tile j - 1 and Q K^T of key tile j (in the order in which
-      // the loader fills the ring)
-      for (int j = j0; j <= j1 && ok && j0 < j1; ++j) {
-        uint32_t v_st = 0, k_st = 0;
-        bool v_in = false, k_in = false;
-        auto take = [&](uint32_t& first) {
-          first = st;
-#pragma unroll
-          for (int u = 0; u < C::UPT; ++u) {
-            if (ok) ok = ctl.wait(&full[st], ph);
-            if (++st == C::STAGES) {
-              st = 0;
-              ph ^= 1;
-            }
-          }
-        };
-        auto take_k = [&] {
-          if (!k_in) take(k_st);
-          k_in = true;
-        };
-        auto take_v = [&] {
-          if (v_in) return;
-          take(v_st);
-          v_in = true;
-          const int p0 = (j - 1) * TA_BN;
-          if (ok && (p0 + TA_BN > it.hi || p0 < it.lo)) {
-            for (int i = lane; i < TA_BN * (DP / 8); i += 32) {
-              const int r = i / (DP / 8), c = i % (DP / 8);  // row, 16-byte piece of it
-              if (p0 + r >= it.hi || p0 + r < it.lo) {
-                const uint32_t u = (v_st + r / C::VROWS) % C::STAGES;
-                *reinterpret_cast<uint4*>(s_ring + u * C::UB + c / 8 * C::VSLAB + r % C::VROWS * 128 +
-                                          c % 8 * 16) = make_uint4(0, 0, 0, 0);
-              }
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-          }
-        };
-        auto qk = [&](int t) {
-          take_k();
-          if (ok && j == tl[t].ja) ok = ctl.wait(&q_full[t], nq[t]++ & 1);
-          if (!ok) return;
-          const int b = NT == 2 ? t : cs[t] & 1;
-          ++cs[t];
-          tc::tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-              const uint32_t u = (k_st + k / 8) % C::STAGES;
-              const uint32_t off = (k % 8) / 4 * TA_SLAB + (k % 4) * 32;
-              tc::mma_bf16(tmem + C::S_COL + b * 128,
-                           tc::smem_desc(q_addr + (t * C::SLABS + k / 4) * TA_SLAB + (k % 4) * 32, 16, 1024,
-                                         tc::LAYOUT_SW128),
-                           tc::smem_desc(r_addr + u * C::UB + off, 16, 1024, tc::LAYOUT_SW128), id_qk, k > 0);
-            }
-            tc::mma_commit(&s_full[b]);
-            if (j == tl[t].jb - 1) tc::mma_commit(&q_empty[t]);
-          }
-          __syncwarp();
-        };
-        auto pv = [&](int t) {
-          take_v();
-          const int b = NT == 2 ? t : cp[t] & 1;
-          if (ok) ok = ctl.wait(&p_full[b], (NT == 2 ? cp[t] : cp[t] >> 1) & 1);
-          ++cp[t];
-          if (ok && j - 1 == tl[t].ja) ok = ctl.wait(&o_empty[t], (no[t]++ & 1) ^ 1);
-          if (!ok) return;
-          tc::tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int k = 0; k < TA_BN / 16; ++k) {
-              const uint32_t u = (v_st + k * 16 / C::VROWS) % C::STAGES;
-              ta_mma_ts(tmem + C::O_COL + t * DP, tmem + C::S_COL + b * 128 + k * 8,
-                        tc::smem_desc(r_addr + u * C::UB + k * 16 % C::VROWS * 128, C::VSLAB, 1024,
-                                      tc::LAYOUT_SW128),
-                        id_pv, j - 1 > tl[t].ja || k > 0);
-            }
-            tc::mma_commit(&pv_done[t]);
-          }
-          __syncwarp();
-        };
-        if (NT == 1) {
-          if (j < j1) qk(0);
-          if (j > j0 && ok) pv(0);
-        } else {
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (ok && j > tl[t].ja && j <= tl[t].jb) pv(t);
-            if (ok && j >= tl[t].ja && j < tl[t].jb) qk(t);
-          }
-        }
-        // what no tile used is passed over, so that the ring stays in step
-        if (ok && j > j0) take_v();
-        if (ok && j < j1) take_k();
-        if (leader && ok) {
-#pragma unroll
-          for (int u = 0; u < C::UPT; ++u) {
-            if (v_in) tc::mma_commit(&empty[(v_st + u) % C::STAGES]);
-            if (k_in) tc::mma_commit(&empty[(k_st + u) % C::STAGES]);
-          }
-        }
-        __syncwarp();
-      }
-      more = w.next(a);
-    }
-    if (!ok) {  // MMAs in flight end before TMEM is freed
-      if (leader) tc::mma_commit(drain);
-      __syncwarp();
-      tc::mbar_wait(drain, 0, TA_WAIT_NS);
-    }
-  } else if (role == 2) {
-    // ------------------------------------------------------------ query loader
-    uint32_t n[NT] = {};
-    const uint32_t bytes = C::SLABS * tb1 * a.g * 128;
-    bool ok = true;
-    while (more && ok) {
-      int j0, j1;
-      w.tiles(TA_BN, j0, j1);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const TaTile x = ta_tile(a, w.it, t, tb1, j0, j1);
-        if (x.jb == x.ja || !ok) continue;
-        ok = ctl.wait(&q_empty[t], (n[t]++ & 1) ^ 1);
-        if (ok && lane == 0) {
-          tc::mbar_expect_tx(&q_full[t], bytes);
-          for (int s = 0; s < C::SLABS; ++s)
-            tc::tma_load_3d(s_q + (t * C::SLABS + s) * TA_SLAB, &tm_q, &q_full[t], s * 64, w.it.h * a.g,
-                            w.it.r.first + x.tok);
-        }
-        __syncwarp();
-      }
-      more = w.next(a);
-    }
-    if (!ok)
-      for (int t = 0; t < NT; ++t)
-        if (n[t]) tc::mbar_wait(&q_full[t], (n[t] - 1) & 1, TA_WAIT_NS);
-  } else if (role < 0) {
+  uint32_t ni = 0;  // items so far
+  // the next item, or null at the end of the work (or of a wait); done() hands its record back
+  auto next_item = [&]() -> const TaItem* {
+    if (!ctl.wait(&i_full[ni % TA_ITEMS], ni / TA_ITEMS & 1)) return nullptr;
+    const TaItem* it = &s_item[ni % TA_ITEMS];
+    return it->n < 0 ? nullptr : it;
+  };
+  auto done_item = [&] {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
+    ++ni;
+  };
+  // Registers: 384 threads x 168 at launch = 256 x 208 + 128 x 88 after the two warpgroups of
+  // softmax have taken what the other one gives up.
+  if (role < 0) {
+    if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax, one row a thread
     const int t = NT == 2 ? warp >> 2 : 0, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
@@ -491,12 +310,12 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
     const float sc = a.scale_log2;
     uint32_t cs = 0, npv = 0, nj = 0;  // S taken, products P V of this tile, joins
     bool ok = true;
-    while (more && ok) {
-      int j0, j1;
-      w.tiles(TA_BN, j0, j1);
-      const TaTile tl = ta_tile(a, w.it, t, tb1, j0, j1);
+    const TaItem* rec;
+    while (ok && (rec = next_item())) {
+      const TaItem& it = *rec;
+      const TaTile tl = ta_tile(a, it, t, tb1);
       const bool live = wq * 32 < tl.rows;  // any row of the warp
-      const int base = w.it.r.kv - w.it.r.q + tl.tok;
+      const int base = it.kv - it.q + tl.tok;
       const int pos = base + min(r, max(tl.rows - 1, 0)) / a.g;
       // positions of the warp's first and last row: tiles between need no mask
       const int p_first = base + wq * 32 / a.g, p_last = base + min(wq * 32 + 31, max(tl.rows - 1, 0)) / a.g;
@@ -521,15 +340,14 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < 128; ++c) s[c] = c <= hi && c > lo ? s[c] : -INFINITY;
           }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
+          float mx[4] = {m, s[1], s[2], s[3]};
+          mx[0] = fmaxf(m, s[0]);
 #pragma unroll
-          for (int c = 4; c < 128; c += 8)
+          for (int c = 4; c < 124; c += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              mx[e] = fmaxf(mx[e], s[c + e]);
-              if (c + 4 + e < 128) mx[e] = fmaxf(mx[e], s[c + 4 + e]);
-            }
-          const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+            for (int e = 0; e < 4; ++e) mx[e] = ta_max3(mx[e], s[c + e], s[c + 4 + e]);
+          const float top = ta_max3(ta_max3(mx[0], s[124], s[125]), ta_max3(mx[1], s[126], s[127]),
+                                    fmaxf(mx[2], mx[3]));
           if (j == tl.ja) {
             m = top;
           } else if (__any_sync(0xffffffffu, (top - m) * sc > 8.0f)) {
@@ -590,10 +408,10 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
       }
       const bool mine = r < tl.rows;
       const int row = t * 128 + r;
-      if (w.whole()) {
+      if (it.c0 == it.c1) {
         if (live) {
-          const int64_t tok = w.it.r.first + tl.tok + (mine ? r / a.g : 0);
-          const int hq = w.it.h * a.g + (mine ? r % a.g : 0);
+          const int64_t tok = it.first + tl.tok + (mine ? r / a.g : 0);
+          const int hq = it.h * a.g + (mine ? r % a.g : 0);
           bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
@@ -623,9 +441,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
         }
       } else {
         // a part: maxima, sums and unscaled O to the workspace; the last CTA of the item joins them
-        int c0, c1;
-        w.owners(c0, c1);
-        const size_t slot = (size_t)PgWalk::slot(w.cta, c0);
+        const size_t slot = it.slot;
         const int R = NT * 128;
         if (live) {
           if (mine)
@@ -657,8 +473,8 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
           if (!ok) break;
           if (lane == 0) {
             __threadfence();
-            uint32_t* cnt = reinterpret_cast<uint32_t*>(a.ws + 256) + c0;
-            const bool last = atomicAdd(cnt, 1u) == (uint32_t)(c1 - c0);
+            uint32_t* cnt = reinterpret_cast<uint32_t*>(a.ws + 256) + it.c0;
+            const bool last = atomicAdd(cnt, 1u) == (uint32_t)(it.c1 - it.c0);
             if (last) *cnt = 0u;  // as it was found: zero between calls
             *reinterpret_cast<volatile uint32_t*>(s_last) = last;
             tc::mbar_arrive(j_go);
@@ -670,10 +486,264 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
         ++nj;
         if (*reinterpret_cast<volatile uint32_t*>(s_last)) {
           __threadfence();
-          ta_join<DP>(a, w.it, tb1, c0, c1, tid);
+          ta_join<DP>(a, it, tb1, tid);
         }
       }
-      more = w.next(a);
+      done_item();
+    }
+  } else {
+    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (role == 3) {
+      // ------------------------------------------------------------ walk
+      for (bool ok = true; ok;) {
+        ok = ctl.wait(&i_empty[ni % TA_ITEMS], (ni / TA_ITEMS & 1) ^ 1);
+        if (ok && lane == 0) {
+          TaItem x;
+          x.n = -1;
+          if (more) {
+            x.n = w.it.n;
+            x.h = w.it.h;
+            x.first = w.it.r.first;
+            x.q = w.it.r.q;
+            x.kv = w.it.r.kv;
+            x.tok = w.it.m * a.tb;
+            w.tiles(TA_BN, x.j0, x.j1);
+            x.lo = w.it.lo;
+            x.hi = w.it.hi;
+            w.owners(x.c0, x.c1);
+            x.slot = PgWalk::slot(w.cta, x.c0);
+          }
+          s_item[ni % TA_ITEMS] = x;
+          tc::mbar_arrive(&i_full[ni % TA_ITEMS]);
+        }
+        __syncwarp();
+        ++ni;
+        if (!more) break;
+        more = w.next(a);
+      }
+    } else if (role == 0) {
+      // ------------------------------------------------------------ key / value loader
+      const int ps = 1 << a.ps_log2;
+      uint32_t st = 0, ph = 1;  // stage, parity of its `empty` wait
+      uint32_t issued = 0;
+      bool ok = true;
+      const TaItem* rec;
+      while (ok && (rec = next_item())) {
+        const TaItem it = *rec;
+        done_item();
+        const int j0 = it.j0, j1 = it.j1;
+        const int32_t* row = a.table + (int64_t)it.n * a.table_width;
+        // page of lane i in key tile j (lanes past the tile's pages: unused)
+        const int ppt = max(1, TA_BN >> a.ps_log2);
+        auto page_of = [&](int j) {
+          if (j >= j1 || lane >= ppt) return a.P;
+          const int pos = j * TA_BN + (lane << a.ps_log2), pg = pos >> a.ps_log2;
+          if (pos >= it.hi || pos + ps <= it.lo || pg >= a.table_width) return a.P;
+          const int id = row[pg];
+          return id >= 0 && id < a.P ? id : a.P;  // a.P: outside the map, zeros
+        };
+        // one ring unit: rows [r0, r0 + nr) of tile j, columns from slab s0
+        auto unit = [&](const CUtensorMap* tm, int j, int id, int r0, int nr, int s0, int ns, uint32_t slab_b) {
+          if (!ctl.wait(&empty[st], ph)) return false;
+          if (lane == 0) tc::mbar_expect_tx(&full[st], C::UB);
+          __syncwarp();
+          const int bx = min(ps, nr);  // rows of a box
+          const int first = r0 >> a.ps_log2, n = max(1, nr >> a.ps_log2);
+          const int i = lane - (ps >= TA_BN ? 0 : first);
+          if (i >= 0 && i < n) {
+            uint8_t* dst = s_ring + st * C::UB + i * bx * 128;
+            const int off = ps > nr ? (j * TA_BN + r0) & (ps - 1) : 0;
+            for (int s = 0; s < ns; ++s)
+              tc::tma_load_4d(dst + s * slab_b, tm, &full[st], (s0 + s) * 64, off, it.h, id);
+          }
+          __syncwarp();
+          ++issued;
+          if (++st == C::STAGES) {
+            st = 0;
+            ph ^= 1;
+          }
+          return true;
+        };
+        int id_prev = a.P, id = page_of(j0);
+        for (int j = j0; j <= j1 && ok; ++j) {
+          const int id_next = page_of(j + 1);
+          auto keys = [&] {
+            for (int u = 0; u < C::UPT && ok; ++u)
+              ok = unit(&tm_k, j, id, 0, TA_BN, 2 * u, C::SLABS / C::UPT, TA_SLAB);
+          };
+          auto values = [&] {
+            for (int u = 0; u < C::UPT && ok; ++u) {
+              // (a page of 128 rows or more is lane 0's for every unit)
+              ok = unit(&tm_v, j - 1, id_prev, u * C::VROWS, C::VROWS, 0, C::SLABS, C::VSLAB);
+            }
+          };
+          if (j1 > j0) {
+            if (NT == 1 && j < j1) keys();
+            if (j > j0) values();
+            if (NT == 2 && j < j1) keys();
+          }
+          id_prev = id;
+          id = id_next;
+        }
+      }
+      if (!ok) {  // copies in flight land before the CTA leaves
+        for (uint32_t i = 0; i < min(issued, (uint32_t)C::STAGES); ++i) {
+          const uint32_t n = issued - 1 - i;
+          tc::mbar_wait(&full[n % C::STAGES], (n / C::STAGES) & 1, TA_WAIT_NS);
+        }
+      }
+    } else if (role == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      const bool leader = tc::elect_one();
+      constexpr uint32_t id_qk = tc::idesc_bf16(128, TA_BN, 0, 0);
+      constexpr uint32_t id_pv = tc::idesc_bf16(128, DP, 0, 1);
+      const uint32_t q_addr = tc::smem_u32(s_q), r_addr = tc::smem_u32(s_ring);
+      uint32_t st = 0, ph = 0;        // next ring unit, parity of its `full`
+      uint32_t nq[NT] = {}, no[NT] = {};  // items of tile t so far: queries taken, O begun
+      uint32_t cs[NT] = {}, cp[NT] = {};  // S of tile t issued, P taken
+      bool ok = true;
+      const TaItem* rec;
+      while (ok && (rec = next_item())) {
+        const int j0 = rec->j0, j1 = rec->j1, k_lo = rec->lo, k_hi = rec->hi;
+        TaTile tl[NT];
+  #pragma unroll
+        for (int t = 0; t < NT; ++t) tl[t] = ta_tile(a, *rec, t, tb1);
+        done_item();
+        // step j: the products P V of key tile j - 1 and Q K^T of key tile j (in the order in which
+        // the loader fills the ring)
+        for (int j = j0; j <= j1 && ok && j0 < j1; ++j) {
+          uint32_t v_st = 0, k_st = 0;
+          bool v_in = false, k_in = false;
+          auto take = [&](uint32_t& first) {
+            first = st;
+  #pragma unroll
+            for (int u = 0; u < C::UPT; ++u) {
+              if (ok) ok = ctl.wait(&full[st], ph);
+              if (++st == C::STAGES) {
+                st = 0;
+                ph ^= 1;
+              }
+            }
+          };
+          auto take_k = [&] {
+            if (!k_in) take(k_st);
+            k_in = true;
+          };
+          auto take_v = [&] {
+            if (v_in) return;
+            take(v_st);
+            v_in = true;
+            const int p0 = (j - 1) * TA_BN;
+            if (ok && (p0 + TA_BN > k_hi || p0 < k_lo)) {
+              for (int i = lane; i < TA_BN * (DP / 8); i += 32) {
+                const int r = i / (DP / 8), c = i % (DP / 8);  // row, 16-byte piece of it
+                if (p0 + r >= k_hi || p0 + r < k_lo) {
+                  const uint32_t u = (v_st + r / C::VROWS) % C::STAGES;
+                  *reinterpret_cast<uint4*>(s_ring + u * C::UB + c / 8 * C::VSLAB + r % C::VROWS * 128 +
+                                            c % 8 * 16) = make_uint4(0, 0, 0, 0);
+                }
+              }
+              tc::fence_proxy_async_smem();
+              __syncwarp();
+            }
+          };
+          auto qk = [&](int t) {
+            take_k();
+            if (ok && j == tl[t].ja) ok = ctl.wait(&q_full[t], nq[t]++ & 1);
+            if (!ok) return;
+            const int b = NT == 2 ? t : cs[t] & 1;
+            ++cs[t];
+            tc::tc_fence_after();
+            if (leader) {
+  #pragma unroll
+              for (int k = 0; k < DP / 16; ++k) {
+                const uint32_t u = (k_st + k / 8) % C::STAGES;
+                const uint32_t off = (k % 8) / 4 * TA_SLAB + (k % 4) * 32;
+                tc::mma_bf16(tmem + C::S_COL + b * 128,
+                             tc::smem_desc(q_addr + (t * C::SLABS + k / 4) * TA_SLAB + (k % 4) * 32, 16, 1024,
+                                           tc::LAYOUT_SW128),
+                             tc::smem_desc(r_addr + u * C::UB + off, 16, 1024, tc::LAYOUT_SW128), id_qk, k > 0);
+              }
+              tc::mma_commit(&s_full[b]);
+              if (j == tl[t].jb - 1) tc::mma_commit(&q_empty[t]);
+            }
+            __syncwarp();
+          };
+          auto pv = [&](int t) {
+            take_v();
+            const int b = NT == 2 ? t : cp[t] & 1;
+            if (ok) ok = ctl.wait(&p_full[b], (NT == 2 ? cp[t] : cp[t] >> 1) & 1);
+            ++cp[t];
+            if (ok && j - 1 == tl[t].ja) ok = ctl.wait(&o_empty[t], (no[t]++ & 1) ^ 1);
+            if (!ok) return;
+            tc::tc_fence_after();
+            if (leader) {
+  #pragma unroll
+              for (int k = 0; k < TA_BN / 16; ++k) {
+                const uint32_t u = (v_st + k * 16 / C::VROWS) % C::STAGES;
+                ta_mma_ts(tmem + C::O_COL + t * DP, tmem + C::S_COL + b * 128 + k * 8,
+                          tc::smem_desc(r_addr + u * C::UB + k * 16 % C::VROWS * 128, C::VSLAB, 1024,
+                                        tc::LAYOUT_SW128),
+                          id_pv, j - 1 > tl[t].ja || k > 0);
+              }
+              tc::mma_commit(&pv_done[t]);
+            }
+            __syncwarp();
+          };
+          if (NT == 1) {
+            if (j < j1) qk(0);
+            if (j > j0 && ok) pv(0);
+          } else {
+  #pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if (ok && j > tl[t].ja && j <= tl[t].jb) pv(t);
+              if (ok && j >= tl[t].ja && j < tl[t].jb) qk(t);
+            }
+          }
+          // what no tile used is passed over, so that the ring stays in step
+          if (ok && j > j0) take_v();
+          if (ok && j < j1) take_k();
+          if (leader && ok) {
+  #pragma unroll
+            for (int u = 0; u < C::UPT; ++u) {
+              if (v_in) tc::mma_commit(&empty[(v_st + u) % C::STAGES]);
+              if (k_in) tc::mma_commit(&empty[(k_st + u) % C::STAGES]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {  // MMAs in flight end before TMEM is freed
+        if (leader) tc::mma_commit(drain);
+        __syncwarp();
+        tc::mbar_wait(drain, 0, TA_WAIT_NS);
+      }
+    } else if (role == 2) {
+      // ------------------------------------------------------------ query loader
+      uint32_t n[NT] = {};
+      const uint32_t bytes = C::SLABS * tb1 * a.g * 128;
+      bool ok = true;
+      const TaItem* rec;
+      while (ok && (rec = next_item())) {
+        const TaItem it = *rec;
+        done_item();
+  #pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const TaTile x = ta_tile(a, it, t, tb1);
+          if (x.jb == x.ja || !ok) continue;
+          ok = ctl.wait(&q_empty[t], (n[t]++ & 1) ^ 1);
+          if (ok && lane == 0) {
+            tc::mbar_expect_tx(&q_full[t], bytes);
+            for (int s = 0; s < C::SLABS; ++s)
+              tc::tma_load_3d(s_q + (t * C::SLABS + s) * TA_SLAB, &tm_q, &q_full[t], s * 64, it.h * a.g,
+                              it.first + x.tok);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok)
+        for (int t = 0; t < NT; ++t)
+          if (n[t]) tc::mbar_wait(&q_full[t], (n[t] - 1) & 1, TA_WAIT_NS);
     }
   }
   tc::tc_fence_before();
@@ -705,8 +775,20 @@ cudaError_t run(PagedArgs& a, int P, int ps, cudaStream_t s, int sms) {
     e = encode_tmap(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.vc, dk, sv, bv, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   const void* f = reinterpret_cast<const void*>(k_paged_attn<DP>);
-  e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem);
+  static std::atomic<uint64_t> ready{0};  // a bit a device
+  int dev = 0;
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, f);
+    if (e != cudaSuccess) return e;
+    // the register split draws on what the launch gives
+    if (C::NT == 2 && at.numRegs * C::THREADS < 256 * 208 + 128 * 88) return cudaErrorInvalidConfiguration;
+    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   const PagedWs L = paged_ws(sms, C::NT * 128, DP);
   a.part_ml = L.ml;
   a.part_o = L.o;
