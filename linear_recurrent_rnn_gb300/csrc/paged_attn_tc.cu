@@ -67,6 +67,10 @@ struct TaAbort {
     if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, ok || slow(bar, parity));
     return ok;
   }
+  // By one thread.
+  __device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity) const {
+    return tc::mbar_try_wait(bar, parity) || slow(bar, parity);
+  }
   __device__ bool slow(uint64_t* bar, uint32_t parity) const {
     const uint64_t t0 = tc::global_ns();
     while (!tc::mbar_try_wait_sleep(bar, parity, 20000u)) {
@@ -109,6 +113,11 @@ __device__ __forceinline__ TaTile ta_tile(const PagedArgs& a, const TaItem& it, 
   x.jb = min(it.j1, (hi + TA_BN - 1) / TA_BN);
   if (x.rows == 0 || x.jb < x.ja) x.jb = x.ja;
   return x;
+}
+
+// Key tile j has positions that no row of the item sees (keys [lo, hi)).
+__device__ __forceinline__ bool ta_cut(int j, int lo, int hi) {
+  return (j + 1) * TA_BN > hi || j * TA_BN < lo;
 }
 
 __device__ __forceinline__ float ta_ex2(float x) {
@@ -231,12 +240,15 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   uint64_t* j_go = j_full + 1;           // s_last says whether this CTA joins the item
   uint64_t* i_full = j_go + 1;           // [TA_ITEMS] item records
   uint64_t* i_empty = i_full + TA_ITEMS;
-  uint64_t* drain = i_empty + TA_ITEMS;
+  uint64_t* v_come = i_empty + TA_ITEMS;  // a value tile with rows that are not seen is there
+  uint64_t* v_clean = v_come + 1;         // those rows are cleared
+  uint64_t* drain = v_clean + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   uint32_t* s_flag = tmem_holder + 1;
   uint32_t* s_last = tmem_holder + 2;
   __shared__ int64_t scratch[33];
   __shared__ TaItem s_item[TA_ITEMS];
+  __shared__ uint32_t s_issued[NT + 1];  // loads issued: queries of each tile, ring units
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tb1 = max(1, 128 / a.g);  // tokens of a row tile
   const TaAbort ctl{s_flag, reinterpret_cast<uint32_t*>(a.ws)};
@@ -263,7 +275,10 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
       tc::mbar_init(&i_full[i], 1);
       tc::mbar_init(&i_empty[i], C::SOFT / 32 + 3);
     }
+    tc::mbar_init(v_come, 1);
+    tc::mbar_init(v_clean, 1);
     tc::mbar_init(drain, 1);
+    for (int i = 0; i <= NT; ++i) s_issued[i] = 0u;
     *s_flag = 0u;
     tc::fence_barrier_init();
     tc::prefetch_tmap(&tm_q);
@@ -586,148 +601,127 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
           id = id_next;
         }
       }
-      if (!ok) {  // copies in flight land before the CTA leaves
-        for (uint32_t i = 0; i < min(issued, (uint32_t)C::STAGES); ++i) {
-          const uint32_t n = issued - 1 - i;
-          tc::mbar_wait(&full[n % C::STAGES], (n / C::STAGES) & 1, TA_WAIT_NS);
-        }
-      }
+      if (lane == 0) s_issued[NT] = issued;
     } else if (role == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      const bool leader = tc::elect_one();
-      constexpr uint32_t id_qk = tc::idesc_bf16(128, TA_BN, 0, 0);
-      constexpr uint32_t id_pv = tc::idesc_bf16(128, DP, 0, 1);
-      const uint32_t q_addr = tc::smem_u32(s_q), r_addr = tc::smem_u32(s_ring);
-      uint32_t st = 0, ph = 0;        // next ring unit, parity of its `full`
-      uint32_t nq[NT] = {}, no[NT] = {};  // items of tile t so far: queries taken, O begun
-      uint32_t cs[NT] = {}, cp[NT] = {};  // S of tile t issued, P taken
-      bool ok = true;
-      const TaItem* rec;
-      while (ok && (rec = next_item())) {
-        const int j0 = rec->j0, j1 = rec->j1, k_lo = rec->lo, k_hi = rec->hi;
-        TaTile tl[NT];
-  #pragma unroll
-        for (int t = 0; t < NT; ++t) tl[t] = ta_tile(a, *rec, t, tb1);
-        done_item();
-        // step j: the products P V of key tile j - 1 and Q K^T of key tile j (in the order in which
-        // the loader fills the ring)
-        for (int j = j0; j <= j1 && ok && j0 < j1; ++j) {
-          uint32_t v_st = 0, k_st = 0;
-          bool v_in = false, k_in = false;
-          auto take = [&](uint32_t& first) {
-            first = st;
-  #pragma unroll
-            for (int u = 0; u < C::UPT; ++u) {
-              if (ok) ok = ctl.wait(&full[st], ph);
-              if (++st == C::STAGES) {
-                st = 0;
-                ph ^= 1;
-              }
-            }
-          };
-          auto take_k = [&] {
-            if (!k_in) take(k_st);
-            k_in = true;
-          };
-          auto take_v = [&] {
-            if (v_in) return;
-            take(v_st);
-            v_in = true;
-            const int p0 = (j - 1) * TA_BN;
-            if (ok && (p0 + TA_BN > k_hi || p0 < k_lo)) {
-              for (int i = lane; i < TA_BN * (DP / 8); i += 32) {
-                const int r = i / (DP / 8), c = i % (DP / 8);  // row, 16-byte piece of it
-                if (p0 + r >= k_hi || p0 + r < k_lo) {
-                  const uint32_t u = (v_st + r / C::VROWS) % C::STAGES;
-                  *reinterpret_cast<uint4*>(s_ring + u * C::UB + c / 8 * C::VSLAB + r % C::VROWS * 128 +
-                                            c % 8 * 16) = make_uint4(0, 0, 0, 0);
+      // ------------------------------------------------------------ MMA issuer: one thread
+      // Products are issued as their operands come; a product of 128 x 128 x 16 takes the tensor
+      // cores 64 cycles, so the thread must spend less than that on each: descriptors are one
+      // base and constant offsets, waits are its own.
+      if (tc::elect_one()) {
+        constexpr uint32_t id_qk = tc::idesc_bf16(128, TA_BN, 0, 0);
+        constexpr uint32_t id_pv = tc::idesc_bf16(128, DP, 0, 1);
+        const uint64_t d_q = tc::smem_desc(tc::smem_u32(s_q), 16, 1024, tc::LAYOUT_SW128);
+        const uint64_t d_k = tc::smem_desc(tc::smem_u32(s_ring), 16, 1024, tc::LAYOUT_SW128);
+        const uint64_t d_v = tc::smem_desc(tc::smem_u32(s_ring), C::VSLAB, 1024, tc::LAYOUT_SW128);
+        uint32_t st = 0, ph = 0;            // next ring unit, parity of its `full`
+        uint32_t nq[NT] = {}, no[NT] = {};  // items of tile t so far: queries taken, O begun
+        uint32_t cs[NT] = {}, cp[NT] = {};  // S of tile t issued, P taken
+        uint32_t nc = 0;                    // value tiles cleared
+        bool ok = true;
+        for (; ok; ++ni) {
+          if (!ctl.wait1(&i_full[ni % TA_ITEMS], ni / TA_ITEMS & 1)) break;
+          const TaItem& it = s_item[ni % TA_ITEMS];
+          if (it.n < 0) break;
+          const int j0 = it.j0, j1 = it.j1, k_lo = it.lo, k_hi = it.hi;
+          TaTile tl[NT];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) tl[t] = ta_tile(a, it, t, tb1);
+          tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
+          // step j: the products P V of key tile j - 1 and Q K^T of key tile j (in the order in
+          // which the loader fills the ring)
+          for (int j = j0; j <= j1 && ok && j0 < j1; ++j) {
+            uint32_t v_st[C::UPT], k_st[C::UPT];
+            bool v_in = false, k_in = false;
+            auto take = [&](uint32_t (&at)[C::UPT]) {
+#pragma unroll
+              for (int u = 0; u < C::UPT; ++u) {
+                at[u] = st;
+                ok = ok && ctl.wait1(&full[st], ph);
+                if (++st == C::STAGES) {
+                  st = 0;
+                  ph ^= 1;
                 }
               }
-              tc::fence_proxy_async_smem();
-              __syncwarp();
-            }
-          };
-          auto qk = [&](int t) {
-            take_k();
-            if (ok && j == tl[t].ja) ok = ctl.wait(&q_full[t], nq[t]++ & 1);
-            if (!ok) return;
-            const int b = NT == 2 ? t : cs[t] & 1;
-            ++cs[t];
-            tc::tc_fence_after();
-            if (leader) {
-  #pragma unroll
-              for (int k = 0; k < DP / 16; ++k) {
-                const uint32_t u = (k_st + k / 8) % C::STAGES;
-                const uint32_t off = (k % 8) / 4 * TA_SLAB + (k % 4) * 32;
-                tc::mma_bf16(tmem + C::S_COL + b * 128,
-                             tc::smem_desc(q_addr + (t * C::SLABS + k / 4) * TA_SLAB + (k % 4) * 32, 16, 1024,
-                                           tc::LAYOUT_SW128),
-                             tc::smem_desc(r_addr + u * C::UB + off, 16, 1024, tc::LAYOUT_SW128), id_qk, k > 0);
+            };
+            auto take_v = [&] {
+              if (v_in) return;
+              take(v_st);
+              v_in = true;
+              if (ok && ta_cut(j - 1, k_lo, k_hi)) {
+                tc::mbar_arrive(v_come);
+                ok = ctl.wait1(v_clean, nc++ & 1);
               }
+            };
+            auto take_k = [&] {
+              if (!k_in) take(k_st);
+              k_in = true;
+            };
+            auto qk = [&](int t) {
+              take_k();
+              if (j == tl[t].ja) ok = ok && ctl.wait1(&q_full[t], nq[t]++ & 1);
+              if (!ok) return;
+              const uint32_t b = NT == 2 ? t : cs[t] & 1;
+              ++cs[t];
+              tc::tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < DP / 16; ++k)
+                tc::mma_bf16(tmem + C::S_COL + b * 128,
+                             d_q + (((t * C::SLABS + k / 4) * TA_SLAB + k % 4 * 32) >> 4),
+                             d_k + (k_st[k / 8] * (C::UB >> 4) + ((k % 8 / 4 * TA_SLAB + k % 4 * 32) >> 4)),
+                             id_qk, k > 0);
               tc::mma_commit(&s_full[b]);
               if (j == tl[t].jb - 1) tc::mma_commit(&q_empty[t]);
-            }
-            __syncwarp();
-          };
-          auto pv = [&](int t) {
-            take_v();
-            const int b = NT == 2 ? t : cp[t] & 1;
-            if (ok) ok = ctl.wait(&p_full[b], (NT == 2 ? cp[t] : cp[t] >> 1) & 1);
-            ++cp[t];
-            if (ok && j - 1 == tl[t].ja) ok = ctl.wait(&o_empty[t], (no[t]++ & 1) ^ 1);
-            if (!ok) return;
-            tc::tc_fence_after();
-            if (leader) {
-  #pragma unroll
-              for (int k = 0; k < TA_BN / 16; ++k) {
-                const uint32_t u = (v_st + k * 16 / C::VROWS) % C::STAGES;
+            };
+            auto pv = [&](int t) {
+              take_v();
+              const uint32_t b = NT == 2 ? t : cp[t] & 1;
+              ok = ok && ctl.wait1(&p_full[b], (NT == 2 ? cp[t] : cp[t] >> 1) & 1);
+              ++cp[t];
+              if (j - 1 == tl[t].ja) ok = ok && ctl.wait1(&o_empty[t], (no[t]++ & 1) ^ 1);
+              if (!ok) return;
+              tc::tc_fence_after();
+              const uint32_t more = j - 1 > tl[t].ja;
+#pragma unroll
+              for (int k = 0; k < TA_BN / 16; ++k)
                 ta_mma_ts(tmem + C::O_COL + t * DP, tmem + C::S_COL + b * 128 + k * 8,
-                          tc::smem_desc(r_addr + u * C::UB + k * 16 % C::VROWS * 128, C::VSLAB, 1024,
-                                        tc::LAYOUT_SW128),
-                          id_pv, j - 1 > tl[t].ja || k > 0);
-              }
+                          d_v + (v_st[k * 16 / C::VROWS] * (C::UB >> 4) + (k * 16 % C::VROWS * 128 >> 4)), id_pv,
+                          k > 0 ? 1u : more);
               tc::mma_commit(&pv_done[t]);
+            };
+            if (NT == 1) {
+              if (j < j1) qk(0);
+              if (j > j0 && ok) pv(0);
+            } else {
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                if (ok && j > tl[t].ja && j <= tl[t].jb) pv(t);
+                if (ok && j >= tl[t].ja && j < tl[t].jb) qk(t);
+              }
             }
-            __syncwarp();
-          };
-          if (NT == 1) {
-            if (j < j1) qk(0);
-            if (j > j0 && ok) pv(0);
-          } else {
-  #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              if (ok && j > tl[t].ja && j <= tl[t].jb) pv(t);
-              if (ok && j >= tl[t].ja && j < tl[t].jb) qk(t);
-            }
-          }
-          // what no tile used is passed over, so that the ring stays in step
-          if (ok && j > j0) take_v();
-          if (ok && j < j1) take_k();
-          if (leader && ok) {
-  #pragma unroll
+            // what no tile used is passed over, so that the ring stays in step
+            if (ok && j > j0) take_v();
+            if (ok && j < j1) take_k();
+            if (!ok) break;
+#pragma unroll
             for (int u = 0; u < C::UPT; ++u) {
-              if (v_in) tc::mma_commit(&empty[(v_st + u) % C::STAGES]);
-              if (k_in) tc::mma_commit(&empty[(k_st + u) % C::STAGES]);
+              if (v_in) tc::mma_commit(&empty[v_st[u]]);
+              if (k_in) tc::mma_commit(&empty[k_st[u]]);
             }
           }
-          __syncwarp();
         }
-      }
-      if (!ok) {  // MMAs in flight end before TMEM is freed
-        if (leader) tc::mma_commit(drain);
-        __syncwarp();
-        tc::mbar_wait(drain, 0, TA_WAIT_NS);
+        tc::mma_commit(drain);  // arrives when all MMAs are done
       }
     } else if (role == 2) {
-      // ------------------------------------------------------------ query loader
+      // ------------------------------------------------------------ queries; rows of V to clear
       uint32_t n[NT] = {};
+      uint32_t units = 0, nc = 0;  // ring units of the items before; value tiles cleared
       const uint32_t bytes = C::SLABS * tb1 * a.g * 128;
       bool ok = true;
       const TaItem* rec;
       while (ok && (rec = next_item())) {
         const TaItem it = *rec;
         done_item();
-  #pragma unroll
+#pragma unroll
         for (int t = 0; t < NT; ++t) {
           const TaTile x = ta_tile(a, it, t, tb1);
           if (x.jb == x.ja || !ok) continue;
@@ -740,13 +734,45 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
           }
           __syncwarp();
         }
+        const int nj = it.j1 - it.j0;
+        for (int i = 0; i < nj && ok; i = i == 0 && nj > 1 ? nj - 1 : nj) {  // the first and the last tile
+          const int p0 = (it.j0 + i) * TA_BN;
+          if (!ta_cut(it.j0 + i, it.lo, it.hi)) continue;
+          // the tile's place in the ring, as the loader fills it
+          const uint32_t at = units + C::UPT * (NT == 2 || i == nj - 1 ? 2 * i + 1 : 2 * i + 2);
+          ok = ctl.wait(v_come, nc++ & 1);  // it is there, and stays until it is cleared
+          for (uint32_t u = 0; u < C::UPT && ok; ++u) {
+            const uint32_t st = (at + u) % C::STAGES;
+            for (int e = lane; e < C::VROWS * (DP / 8); e += 32) {
+              const int r = e / (DP / 8), c = e % (DP / 8);  // row, 16-byte piece of it
+              const int p = p0 + u * C::VROWS + r;
+              if (p >= it.hi || p < it.lo)
+                *reinterpret_cast<uint4*>(s_ring + st * C::UB + c / 8 * C::VSLAB + r * 128 + c % 8 * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(v_clean);
+        }
+        units += 2 * C::UPT * nj;
       }
-      if (!ok)
-        for (int t = 0; t < NT; ++t)
-          if (n[t]) tc::mbar_wait(&q_full[t], (n[t] - 1) & 1, TA_WAIT_NS);
+      if (lane == 0)
+        for (int t = 0; t < NT; ++t) s_issued[t] = n[t];
     }
   }
   tc::tc_fence_before();
+  __syncthreads();
+  if (*s_flag && tid < 32) {
+    // a wait ran out: copies and products in flight end (or run out too) before the CTA leaves
+    for (uint32_t i = lane; i < min(s_issued[NT], (uint32_t)C::STAGES); i += 32) {
+      const uint32_t n = s_issued[NT] - 1 - i;
+      tc::mbar_wait(&full[n % C::STAGES], n / C::STAGES & 1, TA_WAIT_NS);
+    }
+    for (int t = 0; t < NT; ++t)
+      if (s_issued[t]) tc::mbar_wait(&q_full[t], (s_issued[t] - 1) & 1, TA_WAIT_NS);
+    tc::mbar_wait(drain, 0, TA_WAIT_NS);
+  }
   __syncthreads();
   if (warp == C::SOFT / 32 + 1) {
     tc::tc_fence_after();
