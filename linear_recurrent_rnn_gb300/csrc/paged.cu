@@ -215,6 +215,12 @@ rglru_status check_queries(const paged_shape* s) {
   return RGLRU_OK;
 }
 
+// Rows (tokens x query heads of a key/value head) of a request in the mean, rounded up to whole
+// tokens: what the host knows of the lengths.  Either kernel is right for any lengths.
+int mean_rows(const paged_shape* s) {
+  return (int)std::min<int64_t>(((int64_t)s->tokens + s->num_seqs - 1) / s->num_seqs * (s->Hq / s->Hkv), 1 << 30);
+}
+
 bool aligned(const void* p, size_t n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 paged_strides strides_of(const paged_shape* s, const paged_strides* given) {
@@ -345,7 +351,9 @@ extern "C" rglru_status paged_kv_write(const paged_shape* s, const paged_strides
 extern "C" size_t paged_attention_workspace_bytes(const paged_shape* s) {
   if (check_cache(s) != RGLRU_OK || check_heads(s) != RGLRU_OK || check_queries(s) != RGLRU_OK)
     return 0;
-  return s->io == RGLRU_BF16 ? paged_attn_tc_ws_bytes(s) : paged_attn_simt_ws_bytes(s);
+  if (s->io == RGLRU_F32) return paged_attn_simt_ws_bytes(s);
+  const int rows = mean_rows(s);
+  return rows <= PG_FEW_ROWS ? paged_attn_few_ws_bytes(s, rows) : paged_attn_tc_ws_bytes(s);
 }
 
 extern "C" rglru_status paged_attention(const paged_shape* s, const paged_strides* strides,
@@ -398,7 +406,8 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
   a.vc_token = t.vc_token;
   a.vc_head = t.vc_head;
   a.ws = static_cast<uint8_t*>(workspace);
-  return cuda_status(s->io == RGLRU_BF16
-                         ? launch_paged_attn_tc(a, s->num_pages, s->page_size, stream)
-                         : launch_paged_attn_simt(a, stream));
+  if (s->io == RGLRU_F32) return cuda_status(launch_paged_attn_simt(a, stream));
+  const int rows = mean_rows(s);
+  return cuda_status(rows <= PG_FEW_ROWS ? launch_paged_attn_few(a, rows, stream)
+                                         : launch_paged_attn_tc(a, stream));
 }

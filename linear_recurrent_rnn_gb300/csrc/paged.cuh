@@ -4,14 +4,15 @@
 // Work division.  Rows of a request: its q new tokens x the g = Hq / Hkv query heads of one
 // key/value head, token-major; a row tile holds tb whole tokens.  An item is (request, key/value
 // head, row tile); its keys are [lo, hi): from the first key its first token sees to its last
-// token's own position.  Its weight is hi - lo + PG_OVERHEAD.  The items in order (requests,
-// then heads, then row tiles) lie end to end on a line of U = sum of weights, and CTA i of G
-// takes [U i / G, U (i + 1) / G): every CTA gets the same weight whatever the mix of lengths
+// token's own position.  Its weight is hi - lo + overhead.  The items in order (requests,
+// then heads, then row tiles) lie end to end on a line of U = sum of weights, and CTA i takes
+// [W i, W (i + 1)), W = U / CTAs rounded up: every CTA gets the same weight whatever the mix of lengths
 // (one long request, many short ones, prefill among decode), and no host knowledge of lengths
 // is needed.  An item cut by such a boundary is computed in parts, each over a range of whole
 // key tiles, and joined by the last of its CTAs to finish.  Prefix sums over the row tiles of
 // a request are sums of max(0, a + m tb) over m, so they have a closed form; only the sum over
-// requests is a scan.
+// requests is a scan.  All of it is done by every CTA for itself (no kernel before, no host
+// synchronisation), so it is in the way of the first load and kept short: no 64-bit division.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -25,15 +26,13 @@ namespace rglru {
 
 constexpr int PG_MAX_SEQS = 8192;
 constexpr int PG_MAX_CTAS = 1024;
-// Weight of an item beyond its keys (query load, epilogue): about one 128-key tile's time.
-constexpr int PG_OVERHEAD = 128;
-// Least weight of a CTA: one key tile and the overhead; below it splitting costs more than it
-// saves.
-constexpr int PG_MIN_WEIGHT = 128 + PG_OVERHEAD;
 
 struct PagedArgs {
   int N, T, Hq, Hkv, g, D, P, ps_log2, table_width, window;
-  int tb;      // tokens per row tile
+  int tb;          // tokens per row tile
+  int overhead;    // weight of an item beyond its keys: its switch, in keys' time
+  uint64_t grid_inv;
+  int min_weight;  // least weight of a CTA: below it splitting costs more than it saves
   float scale_log2;  // scale * log2(e): scores in units of log2
   const void* q;
   const void* kc;
@@ -64,6 +63,13 @@ inline PagedWs paged_ws(int ctas, int rows, int Dp) {
   return w;
 }
 
+// The division's constants: CTAs of the launch, an item's weight beyond its keys, a CTA's least.
+inline void pg_division(PagedArgs& a, int grid, int overhead, int min_weight) {
+  a.grid_inv = ~0ull / grid + 1;
+  a.overhead = overhead;
+  a.min_weight = min_weight;
+}
+
 struct PgReq {
   int first, q, kv;  // first token row, new tokens, keys
 };
@@ -79,7 +85,7 @@ __device__ __forceinline__ PgReq pg_request(const PagedArgs& a, int n) {
 
 // sum of max(0, x + m d) over 0 <= m < M (d > 0)
 __device__ __forceinline__ int64_t pg_ramp(int64_t x, int d, int64_t M) {
-  const int64_t m0 = x > 0 ? 0 : (-x) / d + 1;
+  const int64_t m0 = x > 0 ? 0 : (uint32_t)(-x) / (uint32_t)d + 1;  // (|x| < 2^32)
   if (m0 >= M) return 0;
   return (M - m0) * x + (int64_t)d * ((M * (M - 1) - m0 * (m0 - 1)) / 2);
 }
@@ -95,7 +101,7 @@ __device__ __forceinline__ void pg_range(const PagedArgs& a, const PgReq& r, int
 __device__ __forceinline__ int64_t pg_weight(const PagedArgs& a, const PgReq& r, int m) {
   int lo, hi;
   pg_range(a, r, m, lo, hi);
-  return hi - lo + PG_OVERHEAD;
+  return hi - lo + a.overhead;
 }
 __device__ __forceinline__ int pg_tiles(const PagedArgs& a, const PgReq& r) {
   return (r.q + a.tb - 1) / a.tb;
@@ -103,7 +109,7 @@ __device__ __forceinline__ int pg_tiles(const PagedArgs& a, const PgReq& r) {
 // Weight of the first M row tiles of one head, none of them the request's last.
 __device__ __forceinline__ int64_t pg_prefix(const PagedArgs& a, const PgReq& r, int64_t M) {
   const int64_t base = (int64_t)r.kv - r.q;
-  int64_t w = M * PG_OVERHEAD + pg_ramp(base + a.tb, a.tb, M);
+  int64_t w = M * a.overhead + pg_ramp(base + a.tb, a.tb, M);
   if (a.window) {
     // lo is at most hi: the keys before the window of a tile that ends past position 0
     const int64_t x = base - a.window + 1;
@@ -117,10 +123,12 @@ __device__ __forceinline__ int64_t pg_head_weight(const PagedArgs& a, const PgRe
   return pg_prefix(a, r, M - 1) + pg_weight(a, r, M - 1);
 }
 
-// CTA i's range of the line and the owner of a place on it.
-__device__ __forceinline__ int64_t pg_cut(int64_t U, int i, int G) { return U * i / G; }
-__device__ __forceinline__ int pg_owner(int64_t x, int64_t U, int G) {
-  return (int)(((x + 1) * G - 1) / U);
+// floor(x / y) for a quotient below 2^20, x < 2^62: the float32 quotient is at most one off.
+__device__ __forceinline__ int pg_div(int64_t x, int64_t y) {
+  int q = (int)__fdiv_rd((float)x, (float)y);
+  while (q * y > x) --q;
+  while ((q + 1) * y <= x) ++q;
+  return q;
 }
 
 // Sum over the requests by the whole CTA: prefix[n] = weight of the requests before n (n <= N).
@@ -165,18 +173,19 @@ struct PgItem {
 // Walks the items that meet [w0, w1).  All state is per thread; every thread that walks sees
 // the same items.
 struct PgWalk {
-  int64_t U, w0, w1;
-  int G, cta;
+  int64_t W, w0, w1;
+  int cta;
   PgItem it;
 
   // `prefix` as left by pg_scan.  Returns false if the CTA has no work.
   __device__ __forceinline__ bool start(const PagedArgs& a, const int64_t* prefix) {
-    U = prefix[a.N];
+    const int64_t U = prefix[a.N];
     cta = blockIdx.x;
-    G = (int)min((int64_t)gridDim.x, (U + PG_MIN_WEIGHT - 1) / PG_MIN_WEIGHT);
-    if (cta >= G) return false;
-    w0 = pg_cut(U, cta, G);
-    w1 = pg_cut(U, cta + 1, G);
+    // U / grid, rounded up: grid_inv is 2^64 / grid, rounded up (exact for U grid < 2^64)
+    W = max((int64_t)__umul64hi((uint64_t)U + gridDim.x - 1, a.grid_inv), (int64_t)a.min_weight);
+    w0 = W * cta;
+    w1 = min(w0 + W, U);
+    if (w0 >= U) return false;
     // the request, head and row tile that hold w0
     int l = 0, h = a.N - 1;
     while (l < h) {
@@ -188,7 +197,7 @@ struct PgWalk {
     it.r = pg_request(a, l);
     const int64_t hw = pg_head_weight(a, it.r);
     int64_t x = w0 - prefix[l];
-    it.h = (int)(x / hw);
+    it.h = pg_div(x, hw);
     x -= it.h * hw;
     int ml = 0, mh = pg_tiles(a, it.r) - 1;
     while (ml < mh) {
@@ -196,13 +205,13 @@ struct PgWalk {
       if (pg_prefix(a, it.r, mid) <= x) ml = mid; else mh = mid - 1;
     }
     it.m = ml;
-    it.at = prefix[l] + it.h * hw + pg_prefix(a, it.r, ml);
+    it.at = w0 - x + pg_prefix(a, it.r, ml);
     fill(a);
     return true;
   }
   __device__ __forceinline__ void fill(const PagedArgs& a) {
     pg_range(a, it.r, it.m, it.lo, it.hi);
-    it.w = it.hi - it.lo + PG_OVERHEAD;
+    it.w = it.hi - it.lo + a.overhead;
   }
   // The next item; false past the CTA's range.
   __device__ __forceinline__ bool next(const PagedArgs& a) {
@@ -221,26 +230,34 @@ struct PgWalk {
     return true;
   }
   // The CTA's key tiles [j0, j1) of the item, tiles of `bn` keys counted from position 0.
-  // A cut at x of the item's weight w gives the parts floor(tiles x / w) of its tiles.
+  // A cut at x of the item's weight w gives the parts about tiles x / w of its tiles, rounded in
+  // one way for the CTAs on both sides of the cut.
   __device__ __forceinline__ void tiles(int bn, int& j0, int& j1) const {
     const int t0 = it.lo / bn, nt = (it.hi + bn - 1) / bn - t0;
-    const int64_t x0 = max(w0, it.at) - it.at, x1 = min(w1, it.at + it.w) - it.at;
-    j0 = t0 + (int)(x0 * nt / it.w);
-    j1 = t0 + (int)(x1 * nt / it.w);
+    j0 = t0 + place(max(w0, it.at) - it.at, nt);
+    j1 = t0 + place(min(w1, it.at + it.w) - it.at, nt);
+  }
+  __device__ __forceinline__ int place(int64_t x, int nt) const {
+    if (x >= it.w) return nt;
+    return min((int)__fmul_rd(__fdiv_rd((float)x, (float)it.w), (float)nt), nt);
   }
   __device__ __forceinline__ bool whole() const { return w0 <= it.at && it.at + it.w <= w1; }
   // CTAs [first, last] that share the item.
   __device__ __forceinline__ void owners(int& first, int& last) const {
-    first = pg_owner(it.at, U, G);
-    last = pg_owner(it.at + it.w - 1, U, G);
+    first = it.at >= w0 ? cta : pg_div(it.at, W);
+    last = it.at + it.w <= w1 ? cta : pg_div(it.at + it.w - 1, W);
   }
   // Partial-result slot of CTA c for an item whose first CTA is `first`.
   __device__ __forceinline__ static int slot(int c, int first) { return 2 * c + (c == first); }
 };
 
-// Tensor-core attention (paged_attn_tc.cu, bf16 I/O).
-cudaError_t launch_paged_attn_tc(PagedArgs a, int num_pages, int page_size, cudaStream_t s);
+// Tensor-core attention (bf16 I/O): many rows a request (paged_attn_tc.cu), few rows a request,
+// `rows` in the mean (paged_attn_few.cu, up to PG_FEW_ROWS).
+cudaError_t launch_paged_attn_tc(PagedArgs a, cudaStream_t s);
 size_t paged_attn_tc_ws_bytes(const paged_shape* s);
+constexpr int PG_FEW_ROWS = 32;
+cudaError_t launch_paged_attn_few(PagedArgs a, int rows, cudaStream_t s);
+size_t paged_attn_few_ws_bytes(const paged_shape* s, int rows);
 // CUDA-core attention (paged_attn_simt.cu, float32 I/O).
 cudaError_t launch_paged_attn_simt(PagedArgs a, cudaStream_t s);
 size_t paged_attn_simt_ws_bytes(const paged_shape* s);

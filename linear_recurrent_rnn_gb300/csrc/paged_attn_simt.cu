@@ -269,6 +269,7 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   a.part_o = L.o;
   a.rows = BM;
   a.tb = std::max(1, BM / a.g);
+  pg_division(a, sms, 128, 256);
   void* args[] = {&a};
   return launch_pdl(f, dim3(sms), dim3(SA_THREADS), smem, s, args, 1);
 }

@@ -28,19 +28,13 @@
 // Work is divided over the CTAs by weight (paged.cuh): one CTA per SM, each with a list of
 // items of which the first and the last may be shared with its neighbours.
 #include <algorithm>
-#include <atomic>
 
 #include "host_util.h"
-#include "paged.cuh"
-#include "tc.cuh"
+#include "paged_tc.cuh"
 
 namespace rglru {
 
 namespace {
-
-constexpr int TA_BN = 128;                     // keys of a tile
-constexpr uint64_t TA_WAIT_NS = 2000000000ull;
-constexpr uint32_t TA_SLAB = 128 * 128;        // 64 columns of 128 rows
 
 template <int DP>
 struct Ta {
@@ -55,47 +49,8 @@ struct Ta {
   static constexpr int THREADS = SOFT + 128;
   static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P buffers b at 128 b, O tiles
   static constexpr size_t Q_BYTES = (size_t)NT * SLABS * TA_SLAB;
-  static constexpr size_t smem = 1024 + Q_BYTES + STAGES * UB + 512;
+  static constexpr size_t smem = 1024 + Q_BYTES + STAGES * UB + 768;
 };
-
-struct TaAbort {
-  uint32_t* flag;   // shared: set once a wait has run out
-  uint32_t* status; // global
-  // By a converged warp; the answer is the same in all its lanes.
-  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
-    bool ok = tc::mbar_try_wait(bar, parity);
-    if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, ok || slow(bar, parity));
-    return ok;
-  }
-  // By one thread.
-  __device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity) const {
-    return tc::mbar_try_wait(bar, parity) || slow(bar, parity);
-  }
-  __device__ bool slow(uint64_t* bar, uint32_t parity) const {
-    const uint64_t t0 = tc::global_ns();
-    while (!tc::mbar_try_wait_sleep(bar, parity, 20000u)) {
-      if (*reinterpret_cast<volatile uint32_t*>(flag)) return false;
-      if (tc::global_ns() - t0 > TA_WAIT_NS) {
-        *reinterpret_cast<volatile uint32_t*>(flag) = 1u;
-        *reinterpret_cast<volatile uint32_t*>(status) = 1u;
-        return false;
-      }
-    }
-    return true;
-  }
-};
-
-// An item of the CTA's work as its warps read it: written by the walking warp into a ring in
-// shared memory, so that the walk's state costs the other warps no registers.
-struct TaItem {
-  int n, h;           // request (-1: no more items), key/value head
-  int first, q, kv;   // its first token row, new tokens, keys
-  int tok;            // the item's first token
-  int j0, j1;         // key tiles of the CTA's part
-  int lo, hi;         // keys that the item's rows see
-  int c0, c1, slot;   // CTAs that share the item, this one's partial-result slot
-};
-constexpr int TA_ITEMS = 4;
 
 // Row tile t of an item and its key tiles within the CTA's part.
 struct TaTile {
@@ -113,42 +68,6 @@ __device__ __forceinline__ TaTile ta_tile(const PagedArgs& a, const TaItem& it, 
   x.jb = min(it.j1, (hi + TA_BN - 1) / TA_BN);
   if (x.rows == 0 || x.jb < x.ja) x.jb = x.ja;
   return x;
-}
-
-// Key tile j has positions that no row of the item sees (keys [lo, hi)).
-__device__ __forceinline__ bool ta_cut(int j, int lo, int hi) {
-  return (j + 1) * TA_BN > hi || j * TA_BN < lo;
-}
-
-__device__ __forceinline__ float ta_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float ta_max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// two float32 operations in one instruction
-__device__ __forceinline__ float2 ta_fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
-        "l"(reinterpret_cast<uint64_t&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 ta_add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return d;
-}
-__device__ __forceinline__ uint32_t ta_pack(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // D[tmem] (+)= A[tmem] B[smem]
@@ -240,14 +159,15 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   uint64_t* j_go = j_full + 1;           // s_last says whether this CTA joins the item
   uint64_t* i_full = j_go + 1;           // [TA_ITEMS] item records
   uint64_t* i_empty = i_full + TA_ITEMS;
-  uint64_t* v_come = i_empty + TA_ITEMS;  // a value tile with rows that are not seen is there
-  uint64_t* v_clean = v_come + 1;         // those rows are cleared
-  uint64_t* drain = v_clean + 1;
+  uint64_t* v_come = i_empty + TA_ITEMS;  // [TA_CLEARS] a value tile to clear is on its way
+  uint64_t* v_clean = v_come + TA_CLEARS; // [TA_CLEARS] it is cleared
+  uint64_t* drain = v_clean + TA_CLEARS;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   uint32_t* s_flag = tmem_holder + 1;
   uint32_t* s_last = tmem_holder + 2;
   __shared__ int64_t scratch[33];
   __shared__ TaItem s_item[TA_ITEMS];
+  __shared__ TaClear s_clear[TA_CLEARS];
   __shared__ uint32_t s_issued[NT + 1];  // loads issued: queries of each tile, ring units
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tb1 = max(1, 128 / a.g);  // tokens of a row tile
@@ -273,10 +193,12 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
     tc::mbar_init(j_go, 1);
     for (int i = 0; i < TA_ITEMS; ++i) {
       tc::mbar_init(&i_full[i], 1);
-      tc::mbar_init(&i_empty[i], C::SOFT / 32 + 3);
+      tc::mbar_init(&i_empty[i], C::SOFT / 32 + 2);
     }
-    tc::mbar_init(v_come, 1);
-    tc::mbar_init(v_clean, 1);
+    for (int i = 0; i < TA_CLEARS; ++i) {
+      tc::mbar_init(&v_come[i], 1);
+      tc::mbar_init(&v_clean[i], 1);
+    }
     tc::mbar_init(drain, 1);
     for (int i = 0; i <= NT; ++i) s_issued[i] = 0u;
     *s_flag = 0u;
@@ -291,7 +213,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   }
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  const int role = warp - C::SOFT / 32;  // < 0: softmax; 0: keys and values, 1: MMA, 2: queries, 3: walk
+  const int role = warp - C::SOFT / 32;  // < 0: softmax; 0: keys and values, 1: MMA, 2: clearing, 3: walk and queries and queries
   PgWalk w;
   int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
   pg_scan(a, prefix, scratch);
@@ -509,99 +431,75 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   } else {
     if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (role == 3) {
-      // ------------------------------------------------------------ walk
+      // ------------------------------------------------------------ walk, and queries
+      uint32_t n[NT] = {};  // query loads
+      const uint32_t bytes = C::SLABS * tb1 * a.g * 128;
       for (bool ok = true; ok;) {
         ok = ctl.wait(&i_empty[ni % TA_ITEMS], (ni / TA_ITEMS & 1) ^ 1);
-        if (ok && lane == 0) {
-          TaItem x;
-          x.n = -1;
-          if (more) {
-            x.n = w.it.n;
-            x.h = w.it.h;
-            x.first = w.it.r.first;
-            x.q = w.it.r.q;
-            x.kv = w.it.r.kv;
-            x.tok = w.it.m * a.tb;
-            w.tiles(TA_BN, x.j0, x.j1);
-            x.lo = w.it.lo;
-            x.hi = w.it.hi;
-            w.owners(x.c0, x.c1);
-            x.slot = PgWalk::slot(w.cta, x.c0);
-          }
+        if (!ok) break;
+        TaItem x;
+        x.n = -1;
+        if (more) {
+          x.n = w.it.n;
+          x.h = w.it.h;
+          x.first = w.it.r.first;
+          x.q = w.it.r.q;
+          x.kv = w.it.r.kv;
+          x.tok = w.it.m * a.tb;
+          w.tiles(TA_BN, x.j0, x.j1);
+          x.lo = w.it.lo;
+          x.hi = w.it.hi;
+          w.owners(x.c0, x.c1);
+          x.slot = PgWalk::slot(w.cta, x.c0);
+        }
+        if (lane == 0) {
           s_item[ni % TA_ITEMS] = x;
           tc::mbar_arrive(&i_full[ni % TA_ITEMS]);
         }
         __syncwarp();
         ++ni;
         if (!more) break;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const TaTile tl = ta_tile(a, x, t, tb1);
+          if (tl.jb == tl.ja || !ok) continue;
+          ok = ctl.wait(&q_empty[t], (n[t] & 1) ^ 1);
+          if (ok) {
+            if (lane == 0) {
+              tc::mbar_expect_tx(&q_full[t], bytes);
+              for (int s = 0; s < C::SLABS; ++s)
+                tc::tma_load_3d(s_q + (t * C::SLABS + s) * TA_SLAB, &tm_q, &q_full[t], s * 64, x.h * a.g,
+                                x.first + tl.tok);
+            }
+            ++n[t];
+          }
+          __syncwarp();
+        }
         more = w.next(a);
       }
+      if (lane == 0)
+        for (int t = 0; t < NT; ++t) s_issued[t] = n[t];
     } else if (role == 0) {
       // ------------------------------------------------------------ key / value loader
-      const int ps = 1 << a.ps_log2;
-      uint32_t st = 0, ph = 1;  // stage, parity of its `empty` wait
-      uint32_t issued = 0;
-      bool ok = true;
+      TaLoader<C> ld{a, ctl, s_ring, full, empty, s_clear, v_come};
       const TaItem* rec;
+      bool ok = true;
       while (ok && (rec = next_item())) {
         const TaItem it = *rec;
         done_item();
         const int j0 = it.j0, j1 = it.j1;
-        const int32_t* row = a.table + (int64_t)it.n * a.table_width;
-        // page of lane i in key tile j (lanes past the tile's pages: unused)
-        const int ppt = max(1, TA_BN >> a.ps_log2);
-        auto page_of = [&](int j) {
-          if (j >= j1 || lane >= ppt) return a.P;
-          const int pos = j * TA_BN + (lane << a.ps_log2), pg = pos >> a.ps_log2;
-          if (pos >= it.hi || pos + ps <= it.lo || pg >= a.table_width) return a.P;
-          const int id = row[pg];
-          return id >= 0 && id < a.P ? id : a.P;  // a.P: outside the map, zeros
-        };
-        // one ring unit: rows [r0, r0 + nr) of tile j, columns from slab s0
-        auto unit = [&](const CUtensorMap* tm, int j, int id, int r0, int nr, int s0, int ns, uint32_t slab_b) {
-          if (!ctl.wait(&empty[st], ph)) return false;
-          if (lane == 0) tc::mbar_expect_tx(&full[st], C::UB);
-          __syncwarp();
-          const int bx = min(ps, nr);  // rows of a box
-          const int first = r0 >> a.ps_log2, n = max(1, nr >> a.ps_log2);
-          const int i = lane - (ps >= TA_BN ? 0 : first);
-          if (i >= 0 && i < n) {
-            uint8_t* dst = s_ring + st * C::UB + i * bx * 128;
-            const int off = ps > nr ? (j * TA_BN + r0) & (ps - 1) : 0;
-            for (int s = 0; s < ns; ++s)
-              tc::tma_load_4d(dst + s * slab_b, tm, &full[st], (s0 + s) * 64, off, it.h, id);
-          }
-          __syncwarp();
-          ++issued;
-          if (++st == C::STAGES) {
-            st = 0;
-            ph ^= 1;
-          }
-          return true;
-        };
-        int id_prev = a.P, id = page_of(j0);
-        for (int j = j0; j <= j1 && ok; ++j) {
-          const int id_next = page_of(j + 1);
-          auto keys = [&] {
-            for (int u = 0; u < C::UPT && ok; ++u)
-              ok = unit(&tm_k, j, id, 0, TA_BN, 2 * u, C::SLABS / C::UPT, TA_SLAB);
-          };
-          auto values = [&] {
-            for (int u = 0; u < C::UPT && ok; ++u) {
-              // (a page of 128 rows or more is lane 0's for every unit)
-              ok = unit(&tm_v, j - 1, id_prev, u * C::VROWS, C::VROWS, 0, C::SLABS, C::VSLAB);
-            }
-          };
-          if (j1 > j0) {
-            if (NT == 1 && j < j1) keys();
-            if (j > j0) values();
-            if (NT == 2 && j < j1) keys();
-          }
+        int id_prev = a.P, id = ld.page_of(it, j0);
+        for (int j = j0; j <= j1 && ok && j0 < j1; ++j) {
+          const int id_next = ld.page_of(it, j + 1);
+          if (NT == 1 && j < j1) ok = ld.keys(&tm_k, j, id, it.h);
+          if (j > j0) ok = ok && ld.values(&tm_v, j - 1, id_prev, it.h, it.lo, it.hi);
+          if (NT == 2 && j < j1) ok = ok && ld.keys(&tm_k, j, id, it.h);
           id_prev = id;
           id = id_next;
         }
       }
-      if (lane == 0) s_issued[NT] = issued;
+      ld.end();
+      if (lane == 0) s_issued[NT] = ld.issued;
     } else if (role == 1) {
       // ------------------------------------------------------------ MMA issuer: one thread
       // Products are issued as their operands come; a product of 128 x 128 x 16 takes the tensor
@@ -647,9 +545,9 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
               if (v_in) return;
               take(v_st);
               v_in = true;
-              if (ok && ta_cut(j - 1, k_lo, k_hi)) {
-                tc::mbar_arrive(v_come);
-                ok = ctl.wait1(v_clean, nc++ & 1);
+              if (ta_cut(j - 1, k_lo, k_hi)) {
+                ok = ok && ctl.wait1(&v_clean[nc % TA_CLEARS], nc / TA_CLEARS & 1);
+                ++nc;
               }
             };
             auto take_k = [&] {
@@ -712,53 +610,8 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
         tc::mma_commit(drain);  // arrives when all MMAs are done
       }
     } else if (role == 2) {
-      // ------------------------------------------------------------ queries; rows of V to clear
-      uint32_t n[NT] = {};
-      uint32_t units = 0, nc = 0;  // ring units of the items before; value tiles cleared
-      const uint32_t bytes = C::SLABS * tb1 * a.g * 128;
-      bool ok = true;
-      const TaItem* rec;
-      while (ok && (rec = next_item())) {
-        const TaItem it = *rec;
-        done_item();
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const TaTile x = ta_tile(a, it, t, tb1);
-          if (x.jb == x.ja || !ok) continue;
-          ok = ctl.wait(&q_empty[t], (n[t]++ & 1) ^ 1);
-          if (ok && lane == 0) {
-            tc::mbar_expect_tx(&q_full[t], bytes);
-            for (int s = 0; s < C::SLABS; ++s)
-              tc::tma_load_3d(s_q + (t * C::SLABS + s) * TA_SLAB, &tm_q, &q_full[t], s * 64, it.h * a.g,
-                              it.first + x.tok);
-          }
-          __syncwarp();
-        }
-        const int nj = it.j1 - it.j0;
-        for (int i = 0; i < nj && ok; i = i == 0 && nj > 1 ? nj - 1 : nj) {  // the first and the last tile
-          const int p0 = (it.j0 + i) * TA_BN;
-          if (!ta_cut(it.j0 + i, it.lo, it.hi)) continue;
-          // the tile's place in the ring, as the loader fills it
-          const uint32_t at = units + C::UPT * (NT == 2 || i == nj - 1 ? 2 * i + 1 : 2 * i + 2);
-          ok = ctl.wait(v_come, nc++ & 1);  // it is there, and stays until it is cleared
-          for (uint32_t u = 0; u < C::UPT && ok; ++u) {
-            const uint32_t st = (at + u) % C::STAGES;
-            for (int e = lane; e < C::VROWS * (DP / 8); e += 32) {
-              const int r = e / (DP / 8), c = e % (DP / 8);  // row, 16-byte piece of it
-              const int p = p0 + u * C::VROWS + r;
-              if (p >= it.hi || p < it.lo)
-                *reinterpret_cast<uint4*>(s_ring + st * C::UB + c / 8 * C::VSLAB + r * 128 + c % 8 * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(v_clean);
-        }
-        units += 2 * C::UPT * nj;
-      }
-      if (lane == 0)
-        for (int t = 0; t < NT; ++t) s_issued[t] = n[t];
+      // ------------------------------------------------------------ rows of V that no row sees
+      ta_clear_rows<C>(ctl, s_clear, v_come, v_clean, full, s_ring);
     }
   }
   tc::tc_fence_before();
@@ -781,65 +634,41 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
 }
 
 template <int DP>
-cudaError_t run(PagedArgs& a, int P, int ps, cudaStream_t s, int sms) {
+cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   using C = Ta<DP>;
   const int tb1 = std::max(1, 128 / a.g);
   CUtensorMap mq, mk, mv;
-  const uint64_t dq[3] = {(uint64_t)a.D, (uint64_t)a.Hq, (uint64_t)a.T};
-  const uint64_t sq[2] = {(uint64_t)a.q_head * 2, (uint64_t)a.q_token * 2};
-  const uint32_t bq[3] = {64, (uint32_t)a.g, (uint32_t)tb1};
-  cudaError_t e = encode_tmap(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dq, sq, bq,
-                              CU_TENSOR_MAP_SWIZZLE_128B);
-  const uint64_t dk[4] = {(uint64_t)a.D, (uint64_t)ps, (uint64_t)a.Hkv, (uint64_t)P};
-  const uint64_t sk[3] = {(uint64_t)a.kc_token * 2, (uint64_t)a.kc_head * 2, (uint64_t)a.kc_page * 2};
-  const uint64_t sv[3] = {(uint64_t)a.vc_token * 2, (uint64_t)a.vc_head * 2, (uint64_t)a.vc_page * 2};
-  const uint32_t bk[4] = {64, (uint32_t)std::min(ps, TA_BN), 1, 1};
-  const uint32_t bv[4] = {64, (uint32_t)std::min(ps, C::VROWS), 1, 1};
-  if (e == cudaSuccess)
-    e = encode_tmap(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.kc, dk, sk, bk, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e == cudaSuccess)
-    e = encode_tmap(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.vc, dk, sv, bv, CU_TENSOR_MAP_SWIZZLE_128B);
+  cudaError_t e = ta_maps(a, tb1, C::VROWS, &mq, &mk, &mv);
   if (e != cudaSuccess) return e;
   const void* f = reinterpret_cast<const void*>(k_paged_attn<DP>);
-  static std::atomic<uint64_t> ready{0};  // a bit a device
-  int dev = 0;
-  e = cudaGetDevice(&dev);
+  static std::atomic<uint64_t> ready{0};
+  // the register split draws on what the launch gives
+  e = ta_prepare(f, C::smem, C::NT == 2 ? (256 * 208 + 128 * 88) / C::THREADS : 0, ready);
   if (e != cudaSuccess) return e;
-  if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem);
-    if (e != cudaSuccess) return e;
-    cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, f);
-    if (e != cudaSuccess) return e;
-    // the register split draws on what the launch gives
-    if (C::NT == 2 && at.numRegs * C::THREADS < 256 * 208 + 128 * 88) return cudaErrorInvalidConfiguration;
-    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
   const PagedWs L = paged_ws(sms, C::NT * 128, DP);
   a.part_ml = L.ml;
   a.part_o = L.o;
   a.rows = C::NT * 128;
   a.tb = C::NT * tb1;
+  pg_division(a, sms, 128, 256);
   void* args[] = {&mq, &mk, &mv, &a};
   return launch_pdl(f, dim3(sms), dim3(C::THREADS), C::smem, s, args, 1);
 }
 
-int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-
 }  // namespace
 
-cudaError_t launch_paged_attn_tc(PagedArgs a, int num_pages, int page_size, cudaStream_t s) {
+cudaError_t launch_paged_attn_tc(PagedArgs a, cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1 || sms > PG_MAX_CTAS) return cudaErrorNotSupported;
-  switch (dp_of(a.D)) {
-    case 64: return run<64>(a, num_pages, page_size, s, sms);
-    case 128: return run<128>(a, num_pages, page_size, s, sms);
-    default: return run<256>(a, num_pages, page_size, s, sms);
+  switch (ta_width(a.D)) {
+    case 64: return run<64>(a, s, sms);
+    case 128: return run<128>(a, s, sms);
+    default: return run<256>(a, s, sms);
   }
 }
 
 size_t paged_attn_tc_ws_bytes(const paged_shape* s) {
-  const int sms = sm_count(), dp = dp_of(s->D);
+  const int sms = sm_count(), dp = ta_width(s->D);
   return paged_ws(sms > 0 ? sms : 256, dp == 256 ? 128 : 256, dp).total;
 }
 
