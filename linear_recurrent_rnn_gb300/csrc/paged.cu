@@ -381,6 +381,7 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
   a.Hq = s->Hq;
   a.Hkv = s->Hkv;
   a.g = s->Hq / s->Hkv;
+  a.g_inv = (65536u + a.g - 1) / a.g;
   a.D = s->D;
   a.P = s->num_pages;
   a.ps_log2 = log2_exact(s->page_size);

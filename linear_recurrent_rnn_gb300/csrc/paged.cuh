@@ -30,6 +30,7 @@ constexpr int PG_MAX_CTAS = 1024;
 struct PagedArgs {
   int N, T, Hq, Hkv, g, D, P, ps_log2, table_width, window;
   int tb;          // tokens per row tile
+  uint32_t g_inv;  // 2^16 / g, rounded up
   int overhead;    // weight of an item beyond its keys: its switch, in keys' time
   uint64_t grid_inv;
   int min_weight;  // least weight of a CTA: below it splitting costs more than it saves
@@ -74,6 +75,9 @@ struct PgReq {
   int first, q, kv;  // first token row, new tokens, keys
 };
 
+// r / g for a row r < 2^16 / g
+__device__ __forceinline__ int pg_token(const PagedArgs& a, int r) { return (int)((uint32_t)r * a.g_inv >> 16); }
+
 __device__ __forceinline__ PgReq pg_request(const PagedArgs& a, int n) {
   PgReq r;
   const int s = min(max(a.cu[n], 0), a.T), e = min(max(a.cu[n + 1], s), a.T);
@@ -104,7 +108,7 @@ __device__ __forceinline__ int64_t pg_weight(const PagedArgs& a, const PgReq& r,
   return hi - lo + a.overhead;
 }
 __device__ __forceinline__ int pg_tiles(const PagedArgs& a, const PgReq& r) {
-  return (r.q + a.tb - 1) / a.tb;
+  return r.q <= a.tb ? (r.q > 0) : (r.q + a.tb - 1) / a.tb;
 }
 // Weight of the first M row tiles of one head, none of them the request's last.
 __device__ __forceinline__ int64_t pg_prefix(const PagedArgs& a, const PgReq& r, int64_t M) {
@@ -119,13 +123,18 @@ __device__ __forceinline__ int64_t pg_prefix(const PagedArgs& a, const PgReq& r,
 }
 __device__ __forceinline__ int64_t pg_head_weight(const PagedArgs& a, const PgReq& r) {
   const int M = pg_tiles(a, r);
-  if (M == 0) return 0;
+  if (M <= 1) return M == 0 ? 0 : pg_weight(a, r, 0);
   return pg_prefix(a, r, M - 1) + pg_weight(a, r, M - 1);
 }
 
+__device__ __forceinline__ float pg_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // floor(x / y) for a quotient below 2^20, x < 2^62: the float32 quotient is at most one off.
 __device__ __forceinline__ int pg_div(int64_t x, int64_t y) {
-  int q = (int)__fdiv_rd((float)x, (float)y);
+  int q = (int)__fmul_rn((float)x, pg_rcp((float)y));
   while (q * y > x) --q;
   while ((q + 1) * y <= x) ++q;
   return q;
@@ -199,13 +208,17 @@ struct PgWalk {
     int64_t x = w0 - prefix[l];
     it.h = pg_div(x, hw);
     x -= it.h * hw;
-    int ml = 0, mh = pg_tiles(a, it.r) - 1;
-    while (ml < mh) {
-      const int mid = (ml + mh + 1) >> 1;
-      if (pg_prefix(a, it.r, mid) <= x) ml = mid; else mh = mid - 1;
+    it.m = 0;
+    it.at = w0 - x;
+    if (it.r.q > a.tb) {
+      int ml = 0, mh = pg_tiles(a, it.r) - 1;
+      while (ml < mh) {
+        const int mid = (ml + mh + 1) >> 1;
+        if (pg_prefix(a, it.r, mid) <= x) ml = mid; else mh = mid - 1;
+      }
+      it.m = ml;
+      it.at += pg_prefix(a, it.r, ml);
     }
-    it.m = ml;
-    it.at = w0 - x + pg_prefix(a, it.r, ml);
     fill(a);
     return true;
   }
@@ -238,8 +251,9 @@ struct PgWalk {
     j1 = t0 + place(min(w1, it.at + it.w) - it.at, nt);
   }
   __device__ __forceinline__ int place(int64_t x, int nt) const {
+    if (x <= 0) return 0;
     if (x >= it.w) return nt;
-    return min((int)__fmul_rd(__fdiv_rd((float)x, (float)it.w), (float)nt), nt);
+    return min((int)__fmul_rn(__fmul_rn((float)x, pg_rcp((float)it.w)), (float)nt), nt);
   }
   __device__ __forceinline__ bool whole() const { return w0 <= it.at && it.at + it.w <= w1; }
   // CTAs [first, last] that share the item.

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
       if (it.n < 0) break;
       const int j0 = it.j0, j1 = it.j1;
       const int rows = min(a.tb, it.q - it.tok) * a.g;
-      const int p_first = it.kv - it.q + it.tok, p_last = p_first + rows / a.g - 1;
+      const int p_first = it.kv - it.q + it.tok, p_last = p_first + min(a.tb, it.q - it.tok) - 1;
       const uint32_t ob = no & 1, t_o = lanes + C::O_COL + ob * (C::MH * NR);
       float ref[NR], l[NR];  // the rows' references (scores in log2 units), this thread's sums
 #pragma unroll
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
         if (!whole)
           reinterpret_cast<float2*>(a.ws + a.part_ml)[(size_t)it.slot * NR + tid] = make_float2(s_ref[tid], sum);
         else if (a.lse)
-          a.lse[(int64_t)(tok0 + tid / a.g) * a.Hq + it.h * a.g + tid % a.g] = tf_lse(s_ref[tid], sum);
+          a.lse[(int64_t)(tok0 + pg_token(a, tid)) * a.Hq + it.h * a.g + tid - pg_token(a, tid) * a.g] =
+              tf_lse(s_ref[tid], sum);
       }
       {
         bf16* dst = static_cast<bf16*>(a.o) + tok0 * a.o_token + (int64_t)it.h * a.g * a.o_head + tid;
@@ -350,10 +351,9 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
       }
       if (any) tc::tc_fence_before();
       if (!whole) {
-        __threadfence();
         tf_any(false);
         if (tid == 0) {
-          __threadfence();
+          __threadfence();  // cumulative: the other threads' parts, ordered before by the barrier
           uint32_t* cnt = reinterpret_cast<uint32_t*>(a.ws + 256) + it.c0;
           const bool last = atomicAdd(cnt, 1u) == (uint32_t)(it.c1 - it.c0);
           if (last) *cnt = 0u;  // as it was found: zero between calls
@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
           __threadfence();
           float2* wt = reinterpret_cast<float2*>(s_p);  // [part][row]
           constexpr int PARTS = 2 * C::PB / (NR * 8), RP = 512 / DP, PASSES = NR / RP;
+          constexpr int BATCH = PASSES >= 16 ? 1 : 16 / PASSES;  // parts loaded at once
           const int col = tid % (DP / 4) * 4, r0 = tid / (DP / 4);
           float4 o[PASSES];
 #pragma unroll
@@ -374,7 +375,19 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
           float m = -INFINITY, sum = 0.0f;  // of row tid
           for (int q0 = it.c0; q0 <= it.c1; q0 += PARTS) {
             const int nq = min(PARTS, it.c1 - q0 + 1);
-#pragma unroll 4
+            // the first parts' sums are on their way while their weights are worked out
+            const float* po = reinterpret_cast<const float*>(a.ws + a.part_o) + r0 * DP + col;
+            float4 v[BATCH][PASSES];
+            auto load = [&](int qb) {
+#pragma unroll
+              for (int b = 0; b < BATCH; ++b) {
+                const float* pq = po + (size_t)PgWalk::slot(q0 + min(qb + b, nq - 1), it.c0) * NR * DP;
+#pragma unroll
+                for (int k = 0; k < PASSES; ++k) v[b][k] = __ldcg(reinterpret_cast<const float4*>(pq + k * RP * DP));
+              }
+            };
+            load(0);
+#pragma unroll 1
             for (int i = tid; i < nq * NR; i += TF_SOFT)
               wt[i] = i % NR < rows ? __ldcg(reinterpret_cast<const float2*>(a.ws + a.part_ml) +
                                              (size_t)PgWalk::slot(q0 + i / NR, it.c0) * NR + i % NR)
@@ -382,10 +395,11 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
             tf_any(false);
             if (tid < NR) {
               const float m0 = m;
-              for (int q = 0; q < nq; ++q)
-                if (wt[q * NR + tid].y != 0.0f) m = fmaxf(m, wt[q * NR + tid].x);
+#pragma unroll 4
+              for (int q = 0; q < nq; ++q) m = fmaxf(m, wt[q * NR + tid].y != 0.0f ? wt[q * NR + tid].x : -INFINITY);
               const float f = m0 == m ? 1.0f : ta_ex2(m0 - m);
               sum *= f;
+#pragma unroll 4
               for (int q = 0; q < nq; ++q) {
                 const float2 x = wt[q * NR + tid];  // a part that saw nothing did not write its sums
                 const float e = x.y != 0.0f ? ta_ex2(x.x - m) : 0.0f;
@@ -396,40 +410,38 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
               s_ref[tid] = sum;
             }
             tf_any(false);
-            const float* po = reinterpret_cast<const float*>(a.ws + a.part_o) + col;
             if (q0 > it.c0)
 #pragma unroll
               for (int k = 0; k < PASSES; ++k) {
                 const float f = s_scale[r0 + k * RP];
                 o[k] = make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f);
               }
-#pragma unroll 2
-            for (int q = 0; q < nq; ++q) {
-              const float* pq = po + (size_t)PgWalk::slot(q0 + q, it.c0) * NR * DP;
-              float4 v[PASSES];
-              float e[PASSES];
+#pragma unroll 1
+            for (int q = 0; q < nq; q += BATCH) {
+              if (q > 0) load(q);
 #pragma unroll
-              for (int k = 0; k < PASSES; ++k) {
-                e[k] = wt[q * NR + r0 + k * RP].x;
-                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (e[k] != 0.0f) v[k] = __ldcg(reinterpret_cast<const float4*>(pq + (r0 + k * RP) * DP));
-              }
+              for (int b = 0; b < BATCH; ++b)
 #pragma unroll
-              for (int k = 0; k < PASSES; ++k)
-                o[k] = make_float4(fmaf(e[k], v[k].x, o[k].x), fmaf(e[k], v[k].y, o[k].y),
-                                   fmaf(e[k], v[k].z, o[k].z), fmaf(e[k], v[k].w, o[k].w));
+                for (int k = 0; k < PASSES; ++k) {
+                  const float e = q + b < nq ? wt[(q + b) * NR + r0 + k * RP].x : 0.0f;
+                  if (e != 0.0f)
+                    o[k] = make_float4(fmaf(e, v[b][k].x, o[k].x), fmaf(e, v[b][k].y, o[k].y),
+                                       fmaf(e, v[b][k].z, o[k].z), fmaf(e, v[b][k].w, o[k].w));
+                }
             }
             tf_any(false);
           }
           if (tid < rows && a.lse)
-            a.lse[(int64_t)(tok0 + tid / a.g) * a.Hq + it.h * a.g + tid % a.g] = tf_lse(m, sum);
+            a.lse[(int64_t)(tok0 + pg_token(a, tid)) * a.Hq + it.h * a.g + tid - pg_token(a, tid) * a.g] =
+                tf_lse(m, sum);
 #pragma unroll
           for (int k = 0; k < PASSES; ++k) {
             const int r = r0 + k * RP;
             if (r >= rows || col >= a.D) continue;
             const float l = s_ref[r], inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-            bf16* dst = static_cast<bf16*>(a.o) + (int64_t)(tok0 + r / a.g) * a.o_token +
-                        (int64_t)(it.h * a.g + r % a.g) * a.o_head + col;
+            const int tok = pg_token(a, r);
+            bf16* dst = static_cast<bf16*>(a.o) + (int64_t)(tok0 + tok) * a.o_token +
+                        (int64_t)(it.h * a.g + r - tok * a.g) * a.o_head + col;
             *reinterpret_cast<uint2*>(dst) =
                 make_uint2(ta_pack(o[k].x * inv, o[k].y * inv), ta_pack(o[k].z * inv, o[k].w * inv));
           }

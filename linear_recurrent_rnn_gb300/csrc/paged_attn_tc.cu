@@ -110,8 +110,8 @@ __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int t
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int t = row >> 7, r = row & 127;
-  const int64_t tok = it.first + it.tok + t * tb1 + r / a.g;
-  const int hq = it.h * a.g + r % a.g;
+  const int64_t tok = it.first + it.tok + t * tb1 + pg_token(a, r);
+  const int hq = it.h * a.g + r - pg_token(a, r) * a.g;
   bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
   for (int k = col0; k < col0 + cols && k < a.D; k += 8) {
     float acc[8];
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
       const TaTile tl = ta_tile(a, it, t, tb1);
       const bool live = wq * 32 < tl.rows;  // any row of the warp
       const int base = it.kv - it.q + tl.tok;
-      const int pos = base + min(r, max(tl.rows - 1, 0)) / a.g;
+      const int my_tok = pg_token(a, min(r, max(tl.rows - 1, 0))), pos = base + my_tok;
       // positions of the warp's first and last row: tiles between need no mask
-      const int p_first = base + wq * 32 / a.g, p_last = base + min(wq * 32 + 31, max(tl.rows - 1, 0)) / a.g;
+      const int p_first = base + pg_token(a, wq * 32), p_last = base + pg_token(a, min(wq * 32 + 31, max(tl.rows - 1, 0)));
       float m = -INFINITY, l = 0.0f;  // in units of the scores; the sum at that maximum
       for (int j = tl.ja; j < tl.jb; ++j) {
         const int b = NT == 2 ? t : cs & 1;
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
       const int row = t * 128 + r;
       if (it.c0 == it.c1) {
         if (live) {
-          const int64_t tok = it.first + tl.tok + (mine ? r / a.g : 0);
-          const int hq = it.h * a.g + (mine ? r % a.g : 0);
+          const int64_t tok = it.first + tl.tok + my_tok;
+          const int hq = it.h * a.g + min(r, tl.rows - 1) - my_tok * a.g;
           bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
@@ -399,7 +399,6 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
           }
         }
         if (any) tc::tc_fence_before();
-        __threadfence();
         __syncwarp();
         if (lane == 0) {
           if (any) tc::mbar_arrive(&o_empty[t]);
@@ -409,7 +408,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
           ok = ctl.wait(j_full, nj & 1);
           if (!ok) break;
           if (lane == 0) {
-            __threadfence();
+            __threadfence();  // cumulative: the other threads' parts, ordered before by the barrier
             uint32_t* cnt = reinterpret_cast<uint32_t*>(a.ws + 256) + it.c0;
             const bool last = atomicAdd(cnt, 1u) == (uint32_t)(it.c1 - it.c0);
             if (last) *cnt = 0u;  // as it was found: zero between calls
