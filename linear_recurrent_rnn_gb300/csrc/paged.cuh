@@ -47,6 +47,7 @@ struct PagedArgs {
   uint8_t* ws;
   size_t part_ml, part_o;  // workspace offsets (below)
   int rows;                // rows of a partial result
+  int o_32;                // rows of o are multiples of 32 bytes on 32-byte boundaries
 };
 
 // Workspace: u32 status word, then at 256 one u32 counter per CTA (zero between calls), then the

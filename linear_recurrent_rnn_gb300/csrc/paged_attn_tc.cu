@@ -70,6 +70,12 @@ __device__ __forceinline__ TaTile ta_tile(const PagedArgs& a, const TaItem& it, 
   return x;
 }
 
+__device__ __forceinline__ void ta_store32(bf16* p, const uint32_t* u) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+               "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+
 // D[tmem] (+)= A[tmem] B[smem]
 __device__ __forceinline__ void ta_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -93,7 +99,7 @@ __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int t
   const int n1 = min(it.q - it.tok, tb1) * a.g;
   const int n2 = C::NT == 2 ? max(min(it.q - it.tok - tb1, tb1), 0) * a.g : 0;
   const int used = n2 > 0 ? 128 + n2 : n1;
-  int rp = C::SOFT * 8 / DP;
+  int rp = C::SOFT * 16 / DP;
   while (rp < used) rp <<= 1;
   const int groups = C::SOFT / rp, cols = DP / groups;
   const int row = tid & (rp - 1), col0 = tid / rp * cols;
@@ -113,25 +119,29 @@ __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int t
   const int64_t tok = it.first + it.tok + t * tb1 + pg_token(a, r);
   const int hq = it.h * a.g + r - pg_token(a, r) * a.g;
   bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
-  for (int k = col0; k < col0 + cols && k < a.D; k += 8) {
-    float acc[8];
+  constexpr int W = 16;  // columns at a time: with two parts, 32 loads in flight
+#pragma unroll 1
+  for (int k = col0; k < col0 + cols && k < a.D; k += W) {
+    float acc[W];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+    for (int e = 0; e < W; ++e) acc[e] = 0.0f;
 #pragma unroll 2
     for (int c = c0; c <= c1; ++c) {
       const size_t s = (size_t)PgWalk::slot(c, c0);
       const float2 x = __ldcg(ml + s * R + row);
-      if (x.y == 0.0f) continue;  // saw nothing: its sums were not written
-      const float f = ta_ex2(x.x - m);
+      float v[W];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(__ldcg(po + (s * DP + k + e) * R + row), f, acc[e]);
+      for (int e = 0; e < W; ++e) v[e] = __ldcg(po + (s * DP + k + e) * R + row);
+      const float f = x.y == 0.0f ? 0.0f : ta_ex2(x.x - m);  // a part that saw nothing did not write its sums
+#pragma unroll
+      for (int e = 0; e < W; ++e) acc[e] = f != 0.0f ? fmaf(v[e], f, acc[e]) : acc[e];
     }
-    uint4 u;
-    u.x = ta_pack(acc[0] * inv, acc[1] * inv);
-    u.y = ta_pack(acc[2] * inv, acc[3] * inv);
-    u.z = ta_pack(acc[4] * inv, acc[5] * inv);
-    u.w = ta_pack(acc[6] * inv, acc[7] * inv);
-    *reinterpret_cast<uint4*>(o + k) = u;
+#pragma unroll
+    for (int e = 0; e < W; e += 8)
+      if (k + e < a.D && k + e < col0 + cols)
+        *reinterpret_cast<uint4*>(o + k + e) =
+            make_uint4(ta_pack(acc[e] * inv, acc[e + 1] * inv), ta_pack(acc[e + 2] * inv, acc[e + 3] * inv),
+                       ta_pack(acc[e + 4] * inv, acc[e + 5] * inv), ta_pack(acc[e + 6] * inv, acc[e + 7] * inv));
   }
   if (a.lse && col0 == 0)
     a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   }
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  const int role = warp - C::SOFT / 32;  // < 0: softmax; 0: keys and values, 1: MMA, 2: clearing, 3: walk and queries and queries
+  const int role = warp - C::SOFT / 32;  // < 0: softmax; 0: keys and values, 1: MMA, 2: clearing, 3: walk and queries
   PgWalk w;
   int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
   pg_scan(a, prefix, scratch);
@@ -352,20 +362,29 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
           bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-          for (int c = 0; c < DP && c < a.D; c += 16) {
-            float v[16];
+          for (int c = 0; c < DP && c < a.D; c += 32) {
+            float v[32];
             if (any) {
-              tc::tmem_ld16(t_o + c, v);
+              tc::tmem_ld16(t_o + c, *reinterpret_cast<float(*)[16]>(v));
+              tc::tmem_ld16(t_o + c + 16, *reinterpret_cast<float(*)[16]>(v + 16));
               tc::tmem_ld_wait();
               tc::reg_fence(v);
             }
-            uint32_t u[8];
+            uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 16; ++e)
               u[e] = l == 0.0f ? 0u : ta_pack(v[2 * e] * inv, v[2 * e + 1] * inv);
             if (mine) {
-              *reinterpret_cast<uint4*>(o + c) = make_uint4(u[0], u[1], u[2], u[3]);
-              if (c + 8 < a.D) *reinterpret_cast<uint4*>(o + c + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+              if (a.o_32) {  // whole 32-byte sectors a store: half as many passes through L1
+                ta_store32(o + c, u);
+                if (c + 16 < a.D) ta_store32(o + c + 16, u + 8);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (c + 8 * e < a.D)
+                    *reinterpret_cast<uint4*>(o + c + 8 * e) =
+                        make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+              }
             }
           }
           if (mine && a.lse)
@@ -649,7 +668,9 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   a.part_o = L.o;
   a.rows = C::NT * 128;
   a.tb = C::NT * tb1;
-  pg_division(a, sms, 128, 256);
+  a.o_32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_token % 16 == 0 && a.o_head % 16 == 0 && a.D % 16 == 0;
+  // the switch of an item costs two row tiles about 9000 cycles, three key tiles' time
+  pg_division(a, sms, C::NT == 2 ? 384 : 256, 256);
   void* args[] = {&mq, &mk, &mv, &a};
   return launch_pdl(f, dim3(sms), dim3(C::THREADS), C::smem, s, args, 1);
 }
