@@ -13,15 +13,16 @@ namespace rglru {
 namespace {
 
 // ---------------------------------------------------------------- plan
-// One launch, one cluster.  Every CTA scans all requests (new tokens and pages wanted) into its
-// own shared memory, the cluster meets, and only then is anything written: so kv_lens and the
-// free state may be updated in place, and the CTAs share the new table entries and the token
-// rows between them without waiting for one another again.  A token finds its request by a
-// binary search over the offsets; the page of a token in a new page is read from the ring
-// itself, not from the table.  Latency-bound: the floor is a launch, two dependent reads
-// (lengths, then table or ring) and the writes.
+// One launch.  Every CTA scans all requests (new tokens and pages wanted) into its own shared
+// memory and then writes its share of the table entries and token rows: nothing waits for another
+// CTA's result, as the page of a token in a new page is read from the ring itself, not from the
+// table.  Updated in place (kv_lens = cached_lens or free_state_out = free_state) the CTAs must
+// all have read before one writes, so they are then one cluster, which meets in between.
+// Tokens: a warp takes 32 in a row and searches the offsets for the first; the others are mostly
+// in the same request.  Latency-bound: the floor is a launch, two dependent reads (lengths, then
+// table or ring) and the writes.
 struct PlanArgs {
-  int N, T, P, s, width;
+  int N, T, P, s, s_log2, width;
   const int32_t* cached;
   const int32_t* fresh;
   const int32_t* ring;
@@ -35,9 +36,10 @@ struct PlanArgs {
 };
 
 constexpr int PLAN_THREADS = 512;
-constexpr int PLAN_CLUSTER = 8;
+constexpr int PLAN_CLUSTER = 8;   // CTAs in place
+constexpr int PLAN_CTAS = 128;    // CTAs otherwise, at most
 
-__device__ __forceinline__ int plan_ceil(int64_t x, int s) { return (int)((x + s - 1) / s); }
+__device__ __forceinline__ int plan_ceil(int64_t x, const PlanArgs& a) { return (int)((x + a.s - 1) >> a.s_log2); }
 
 __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
   // per request: first row, first of its places in the ring's order, tokens cached
@@ -57,10 +59,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
     if (n < a.N) {
       c = max(a.cached[n], 0);
       q = max(a.fresh[n], 0);
-      const int held = min(plan_ceil(c, a.s), a.width);
-      const int want = plan_ceil((int64_t)c + q, a.s);
+      const int held = min(plan_ceil(c, a), a.width);
+      const int want = plan_ceil((int64_t)c + q, a);
       need = max(min(want, a.width) - held, 0);
-      over += max(want - max(plan_ceil(c, a.s), a.width), 0);
+      over += max(want - max(plan_ceil(c, a), a.width), 0);
     }
     int64_t sq = q, sp = need;
 #pragma unroll
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
   }
   for (int d = 16; d; d >>= 1) over += __shfl_xor_sync(0xffffffffu, over, d);
   if (lane == 0) s_warp[0][warp] = over;
-  // every CTA has read its inputs before any CTA writes
+  // in place: every CTA has read its inputs before any CTA writes
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   const int h0 = a.P > 0 ? ((head % a.P) + a.P) % a.P : 0;
@@ -121,7 +123,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
     }
     return l;
   };
-  auto ring = [&](int i) { return i < count ? a.ring[(int)(((int64_t)h0 + i) % a.P)] : -1; };
+  auto ring = [&](int i) { return i < count ?  // (count <= P: at most once around)
+                          a.ring[h0 + i < a.P ? h0 + i : h0 + i - a.P] : -1; };
   for (int n = first; n <= a.N; n += stride) {
     a.cu[n] = s_cu[n];
     if (n < a.N)
@@ -129,22 +132,34 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
   }
   for (int i = first; i < s_off[a.N]; i += stride) {
     const int n = owner(s_off, i);
-    a.table[(size_t)n * a.width + plan_ceil(s_c[n], a.s) + (i - s_off[n])] = ring(i);
+    a.table[(size_t)n * a.width + plan_ceil(s_c[n], a) + (i - s_off[n])] = ring(i);
   }
-  for (int t = first; t < a.T; t += stride) {
-    int pos = 0;
-    int64_t slot = -1;
-    if (t < s_cu[a.N]) {
-      const int n = owner(s_cu, t), c = s_c[n];
-      pos = (int)min((int64_t)c + (t - s_cu[n]), (int64_t)0x7fffffff);
-      const int pg = pos / a.s, held = plan_ceil(c, a.s);
-      if (pg < a.width) {
-        const int id = pg < held ? a.table[(size_t)n * a.width + pg] : ring(s_off[n] + pg - held);
-        if (id >= 0) slot = (int64_t)id * a.s + pos % a.s;
-      }
+  const int total = s_cu[a.N];
+  constexpr int BATCH = 4;  // rows of a thread whose pages are looked up at once
+  for (int64_t t0 = first; t0 - lane < a.T; t0 += (int64_t)BATCH * stride) {
+    int pos[BATCH], id[BATCH];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int64_t t = t0 + (int64_t)b * stride;
+      pos[b] = 0;
+      id[b] = -1;
+      const int64_t w = t - lane;  // the warp's first row
+      if (w >= a.T || w >= total) continue;
+      int n = owner(s_cu, (int)w);
+      if (s_cu[n + 1] < w + 32 && t < total) n = owner(s_cu, (int)t);
+      if (t >= total) continue;
+      const int c = s_c[n];
+      pos[b] = (int)min((int64_t)c + (t - s_cu[n]), (int64_t)0x7fffffff);
+      const int pg = pos[b] >> a.s_log2, held = plan_ceil(c, a);
+      if (pg < a.width) id[b] = pg < held ? a.table[(size_t)n * a.width + pg] : ring(s_off[n] + pg - held);
     }
-    a.positions[t] = pos;
-    a.slots[t] = slot;
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int64_t t = t0 + (int64_t)b * stride;
+      if (t >= a.T) continue;
+      a.positions[t] = pos[b];
+      a.slots[t] = id[b] >= 0 ? ((int64_t)id[b] << a.s_log2) + (pos[b] & (a.s - 1)) : -1;
+    }
   }
 }
 
@@ -285,6 +300,7 @@ extern "C" rglru_status paged_plan(const paged_shape* s, const int32_t* cached_l
   a.T = s->tokens;
   a.P = s->num_pages;
   a.s = s->page_size;
+  a.s_log2 = log2_exact(s->page_size);
   a.width = s->table_width;
   a.cached = cached_lens;
   a.fresh = new_lens;
@@ -297,14 +313,21 @@ extern "C" rglru_status paged_plan(const paged_shape* s, const int32_t* cached_l
   a.slots = slots;
   a.state_out = free_state_out;
   const size_t smem = (size_t)(3 * a.N + 2) * 4;
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_paged_plan),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return cuda_status(e);
-  // one CTA up to a row a thread, the whole cluster beyond
-  const int ctas = s->tokens > PLAN_THREADS ? PLAN_CLUSTER : 1;
+  if (smem > 48 << 10) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_paged_plan),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  // one CTA up to a row a thread; beyond, one to two rows a thread, or the cluster
+  const bool in_place = kv_lens == cached_lens || free_state_out == free_state;
+  int ctas = 1, cluster = 1;
+  if (s->tokens > PLAN_THREADS) {
+    ctas = in_place ? PLAN_CLUSTER : std::min(PLAN_CTAS, (s->tokens + PLAN_THREADS - 1) / PLAN_THREADS);
+    cluster = in_place ? PLAN_CLUSTER : 1;
+  }
   void* args[] = {&a};
   return cuda_status(launch_pdl(reinterpret_cast<const void*>(k_paged_plan), dim3(ctas),
-                                dim3(PLAN_THREADS), smem, stream, args, ctas));
+                                dim3(PLAN_THREADS), smem, stream, args, cluster));
 }
 
 extern "C" rglru_status paged_kv_write(const paged_shape* s, const paged_strides* strides,

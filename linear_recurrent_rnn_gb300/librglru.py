@@ -200,8 +200,14 @@ def _p(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without the Stream object around it (a tenth of its time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -373,63 +379,67 @@ def alloc_paged_workspace(shape: PagedShape, device="cuda") -> torch.Tensor:
 
 
 def _arg(t, name, dtype, shape):
-    """A contiguous CUDA tensor of this dtype and shape (the entry points read it through its
-    address alone)."""
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, want {tuple(shape)} {dtype}")
-    return _p(t)
+    """The address of a contiguous CUDA tensor of this dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: want a contiguous CUDA tensor, {tuple(shape)} {dtype}, not "
+                     f"{tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
 
 
 def _view(t, name, dtype, shape):
-    """A CUDA tensor of this dtype and shape whose last dimension is contiguous; the others may
-    have any stride."""
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, want {tuple(shape)} {dtype}")
-    if not t.is_cuda:
-        raise ValueError("librglru takes CUDA tensors")
-    if t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr()
+    """The address of a CUDA tensor of this dtype and shape whose last dimension is contiguous;
+    the others may have any stride."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.stride(-1) == 1:
+        return t.data_ptr()
+    raise ValueError(f"{name}: want a CUDA tensor with a contiguous last dimension, "
+                     f"{tuple(shape)} {dtype}, not {tuple(t.shape)} {t.dtype} on {t.device} "
+                     f"with strides {t.stride()}")
 
 
-def _steps(t):
-    """Strides of all dimensions but the last, in elements (a dimension of one element has the
-    stride that a contiguous tensor would have)."""
-    out, n = [], t.shape[-1]
-    for size, st in zip(t.shape[-2::-1], t.stride()[-2::-1]):
-        out.append(st if size > 1 else n)
-        n *= size
-    return out[::-1]
+def _row_steps(t, heads, width):
+    """Token and head strides of rows [tokens, heads, width], in elements (a dimension of one
+    element has the stride that a contiguous tensor would have)."""
+    s = t.stride()
+    return s[0] if t.shape[0] > 1 else heads * width, s[1] if heads > 1 else width
+
+
+def _cache_steps(t, heads, width):
+    """Page, token and head strides of a cache [pages, page_size, heads, width]."""
+    s, n = t.stride(), t.shape
+    return s[0] if n[0] > 1 else n[1] * heads * width, s[1], s[2] if heads > 1 else width
 
 
 def paged_plan(shape, cached_lens, new_lens, free_pages, free_state, block_table, cu_seqlens,
                kv_lens, positions, slots, free_state_out, stream=None):
     N, T, i32 = shape.num_seqs, shape.tokens, torch.int32
-    _check("paged_plan", lib().paged_plan(
-        ctypes.byref(shape), _arg(cached_lens, "cached_lens", i32, (N,)),
-        _arg(new_lens, "new_lens", i32, (N,)),
+    st = (_lib or lib()).paged_plan(
+        shape, _arg(cached_lens, "cached_lens", i32, (N,)), _arg(new_lens, "new_lens", i32, (N,)),
         _arg(free_pages, "free_pages", i32, (shape.num_pages,)),
         _arg(free_state, "free_state", i32, (3,)),
         _arg(block_table, "block_table", i32, (N, shape.table_width)),
         _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,)), _arg(kv_lens, "kv_lens", i32, (N,)),
         _arg(positions, "positions", i32, (T,)), _arg(slots, "slots", torch.int64, (T,)),
-        _arg(free_state_out, "free_state_out", i32, (3,)), _stream(stream)))
+        _arg(free_state_out, "free_state_out", i32, (3,)), _stream(stream))
+    if st:
+        _check("paged_plan", st)
 
 
 def paged_kv_write(shape, k, v, slots, k_cache, v_cache, stream=None):
     """k, v [tokens, Hkv, D] and the caches [num_pages, page_size, Hkv, D] may be strided views
     (slices of a fused projection, a cache stored head by head)."""
     dt, T, H, D = TORCH_DT[shape.io], shape.tokens, shape.Hkv, shape.D
-    cache = (shape.num_pages, shape.page_size, H, D)
-    kp, vp = _view(k, "k", dt, (T, H, D)), _view(v, "v", dt, (T, H, D))
-    kc, vc = _view(k_cache, "k_cache", dt, cache), _view(v_cache, "v_cache", dt, cache)
-    st = None
+    rows, cache = (T, H, D), (shape.num_pages, shape.page_size, H, D)
+    strides = None
     if not (k.is_contiguous() and v.is_contiguous() and k_cache.is_contiguous() and
             v_cache.is_contiguous()):
-        st = PagedStrides(0, 0, 0, 0, *_steps(k), *_steps(v), *_steps(k_cache), *_steps(v_cache))
-    _check("paged_kv_write", lib().paged_kv_write(
-        ctypes.byref(shape), st, kp, vp, _arg(slots, "slots", torch.int64, (T,)), kc, vc,
-        _stream(stream)))
+        strides = PagedStrides(0, 0, 0, 0, *_row_steps(k, H, D), *_row_steps(v, H, D),
+                               *_cache_steps(k_cache, H, D), *_cache_steps(v_cache, H, D))
+    st = (_lib or lib()).paged_kv_write(
+        shape, strides, _view(k, "k", dt, rows), _view(v, "v", dt, rows),
+        _arg(slots, "slots", torch.int64, (T,)), _view(k_cache, "k_cache", dt, cache),
+        _view(v_cache, "v_cache", dt, cache), _stream(stream))
+    if st:
+        _check("paged_kv_write", st)
 
 
 def paged_attention(shape, q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, scale, o, lse,
@@ -438,16 +448,20 @@ def paged_attention(shape, q, k_cache, v_cache, block_table, cu_seqlens, kv_lens
     lse float32 [tokens, Hq] or None; workspace from alloc_paged_workspace."""
     dt, T, D, i32 = TORCH_DT[shape.io], shape.tokens, shape.D, torch.int32
     N, Hq = shape.num_seqs, shape.Hq
-    cache = (shape.num_pages, shape.page_size, shape.Hkv, D)
-    qp, op = _view(q, "q", dt, (T, Hq, D)), _view(o, "o", dt, (T, Hq, D))
-    kc, vc = _view(k_cache, "k_cache", dt, cache), _view(v_cache, "v_cache", dt, cache)
-    st = None
+    rows, cache = (T, Hq, D), (shape.num_pages, shape.page_size, shape.Hkv, D)
+    strides = None
     if not (q.is_contiguous() and o.is_contiguous() and k_cache.is_contiguous() and
             v_cache.is_contiguous()):
-        st = PagedStrides(*_steps(q), *_steps(o), 0, 0, 0, 0, *_steps(k_cache), *_steps(v_cache))
-    _check("paged_attention", lib().paged_attention(
-        ctypes.byref(shape), st, qp, kc, vc,
+        strides = PagedStrides(*_row_steps(q, Hq, D), *_row_steps(o, Hq, D), 0, 0, 0, 0,
+                               *_cache_steps(k_cache, shape.Hkv, D),
+                               *_cache_steps(v_cache, shape.Hkv, D))
+    st = (_lib or lib()).paged_attention(
+        shape, strides, _view(q, "q", dt, rows), _view(k_cache, "k_cache", dt, cache),
+        _view(v_cache, "v_cache", dt, cache),
         _arg(block_table, "block_table", i32, (N, shape.table_width)),
         _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,)), _arg(kv_lens, "kv_lens", i32, (N,)),
-        float(scale), op, None if lse is None else _arg(lse, "lse", torch.float32, (T, Hq)),
-        _p(workspace), _stream(stream)))
+        scale, _view(o, "o", dt, rows),
+        None if lse is None else _arg(lse, "lse", torch.float32, (T, Hq)), _p(workspace),
+        _stream(stream))
+    if st:
+        _check("paged_attention", st)
