@@ -177,6 +177,7 @@ struct WriteArgs {
 };
 
 constexpr int WRITE_THREADS = 256;
+constexpr int WRITE_BATCH = 4;  // 16-byte pieces of a lane in flight
 
 __global__ void __launch_bounds__(WRITE_THREADS) k_paged_write(const WriteArgs a) {
   tc::griddep_wait();
@@ -187,13 +188,22 @@ __global__ void __launch_bounds__(WRITE_THREADS) k_paged_write(const WriteArgs a
     const int64_t slot = a.slots[t];
     if (slot < 0 || slot >= a.slots_end) continue;
     const int64_t page = slot >> a.s_log2, off = slot & ((1 << a.s_log2) - 1);
-#pragma unroll 4
-    for (int i = lane; i < 2 * a.pieces; i += 32) {
-      const int kv = i >= a.pieces, c = kv ? i - a.pieces : i;
-      const int h = c / a.head_pieces, b = (c - h * a.head_pieces) * 16;
-      const uint4 x = *reinterpret_cast<const uint4*>(a.src[kv] + t * a.src_token[kv] + h * a.src_head[kv] + b);
-      *reinterpret_cast<uint4*>(a.dst[kv] + page * a.dst_page[kv] + off * a.dst_token[kv] +
-                                h * a.dst_head[kv] + b) = x;
+    for (int i0 = lane; i0 < 2 * a.pieces; i0 += 32 * WRITE_BATCH) {
+      uint4 x[WRITE_BATCH];
+      uint8_t* to[WRITE_BATCH];
+#pragma unroll
+      for (int e = 0; e < WRITE_BATCH; ++e) {
+        const int i = i0 + 32 * e;
+        to[e] = nullptr;
+        if (i >= 2 * a.pieces) continue;
+        const int kv = i >= a.pieces, c = kv ? i - a.pieces : i;
+        const int h = c / a.head_pieces, b = (c - h * a.head_pieces) * 16;
+        x[e] = __ldg(reinterpret_cast<const uint4*>(a.src[kv] + t * a.src_token[kv] + h * a.src_head[kv] + b));
+        to[e] = a.dst[kv] + page * a.dst_page[kv] + off * a.dst_token[kv] + h * a.dst_head[kv] + b;
+      }
+#pragma unroll
+      for (int e = 0; e < WRITE_BATCH; ++e)
+        if (to[e]) *reinterpret_cast<uint4*>(to[e]) = x[e];
     }
   }
 }
