@@ -384,8 +384,8 @@ extern "C" rglru_status paged_kv_write(const paged_shape* s, const paged_strides
 extern "C" size_t paged_attention_workspace_bytes(const paged_shape* s) {
   if (check_cache(s) != RGLRU_OK || check_heads(s) != RGLRU_OK || check_queries(s) != RGLRU_OK)
     return 0;
-  if (s->io == RGLRU_F32) return paged_attn_simt_ws_bytes(s);
   const int rows = mean_rows(s);
+  if (s->io == RGLRU_F32) return paged_attn_simt_ws_bytes(s, rows);
   return rows <= PG_FEW_ROWS ? paged_attn_few_ws_bytes(s, rows) : paged_attn_tc_ws_bytes(s);
 }
 
@@ -440,8 +440,8 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
   a.vc_token = t.vc_token;
   a.vc_head = t.vc_head;
   a.ws = static_cast<uint8_t*>(workspace);
-  if (s->io == RGLRU_F32) return cuda_status(launch_paged_attn_simt(a, stream));
   const int rows = mean_rows(s);
+  if (s->io == RGLRU_F32) return cuda_status(launch_paged_attn_simt(a, rows, stream));
   return cuda_status(rows <= PG_FEW_ROWS ? launch_paged_attn_few(a, rows, stream)
                                          : launch_paged_attn_tc(a, stream));
 }

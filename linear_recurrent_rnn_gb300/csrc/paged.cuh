@@ -273,9 +273,9 @@ size_t paged_attn_tc_ws_bytes(const paged_shape* s);
 constexpr int PG_FEW_ROWS = 32;
 cudaError_t launch_paged_attn_few(PagedArgs a, int rows, cudaStream_t s);
 size_t paged_attn_few_ws_bytes(const paged_shape* s, int rows);
-// CUDA-core attention (paged_attn_simt.cu, float32 I/O).
-cudaError_t launch_paged_attn_simt(PagedArgs a, cudaStream_t s);
-size_t paged_attn_simt_ws_bytes(const paged_shape* s);
+// CUDA-core attention (paged_attn_simt.cu, float32 I/O), `rows` a request in the mean.
+cudaError_t launch_paged_attn_simt(PagedArgs a, int rows, cudaStream_t s);
+size_t paged_attn_simt_ws_bytes(const paged_shape* s, int rows);
 
 // One kernel on `s` with programmatic stream serialisation (and clusters of `cluster` CTAs).
 cudaError_t launch_pdl(const void* f, dim3 grid, dim3 block, size_t smem, cudaStream_t s,

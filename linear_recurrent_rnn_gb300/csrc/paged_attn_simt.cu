@@ -1,11 +1,22 @@
 // Attention over the paged cache on the CUDA cores (float32 I/O: its 1e-5 bound).
 //
-// One pass over the keys with a running maximum and sum: per tile of BN keys
+// One pass over the keys with a running maximum and sum: per tile of keys
 //   S = Q K^T (scores in units of log2), m' = max(m, max S), P = 2^(S - m'),
 //   l = l 2^(m - m') + sum P,  O = O 2^(m - m') + P V
-// and at the end o = O / l, lse = (m + log2 l) ln 2.  The row tile (BM rows: whole tokens x the
-// query heads of one key/value head) stays in shared memory, O in registers, and the key tile is
-// gathered page by page; work is divided over CTAs by weight (paged.cuh).
+// and at the end o = O / l, lse = (m + log2 l) ln 2.
+//
+// A row tile is BM rows (whole tokens x the query heads of one key/value head).  Half a warp
+// owns 4 rows: 16 lanes side by side along the keys for S and along the columns for O, so that
+// maxima, sums and the exchange of P stay within 16 lanes, and only the key and value tiles
+// are shared by the CTA.  With many rows (BM = 64) all warps work on one tile of keys and the
+// kernel is bound by the float32 pipe; two products an instruction (fma.f32x2) and 4 x 4 (S) or
+// 4 x DP / 16 (O) outputs a thread keep shared memory below it.  With few (BM = 16: decode) it is
+// bound by memory, and four pairs of warps take a quarter of the tile's keys each, with maxima
+// and sums of their own that are joined when the item ends.
+// Tiles are gathered by 16-byte asynchronous copies, row by row through the block table (whose
+// entries are looked up one tile ahead): values land behind the scores, the next keys behind P V.
+// Keys that no row of the item sees are not read, their rows are zero.  Work is divided over CTAs
+// by weight (paged.cuh).
 #include <algorithm>
 
 #include "host_util.h"
@@ -17,36 +28,53 @@ namespace rglru {
 namespace {
 
 constexpr int SA_THREADS = 256;
-constexpr int SA_BN = 64;
 
-__device__ __forceinline__ float4 sa_load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-// BM rows, DP columns (D rounded up).  Threads: TX along keys / columns, TY along rows, 4 rows a
-// thread.
 template <int BM, int DP>
 struct Sa {
-  static constexpr int TY = BM / 4, TX = SA_THREADS / TY;
-  static constexpr int KS = SA_BN / TX;        // keys a thread
-  static constexpr int CS = DP / TX;           // columns of O a thread
-  static constexpr int LD = DP + 4;            // row stride: 16-byte reads of 8 rows meet all banks
-  static constexpr int LS = SA_BN + 4;
-  static constexpr size_t smem = (size_t)((BM + 2 * SA_BN) * LD + BM * LS + 3 * BM) * 4;
+  static constexpr int SPLIT = BM == 64 ? 1 : 4;                    // key ranges of a tile
+  static constexpr int BN = BM == 64 || DP == 64 ? 64 : 4096 / DP;  // keys of a range
+  static constexpr int TILE = SPLIT * BN;
+  static constexpr int KS = BN / 16;     // keys a thread
+  static constexpr int C4 = DP / 64;     // times four columns of O a thread
+  static constexpr int LD = DP + 4;      // row stride: 16-byte reads of 8 rows meet all banks
+  static constexpr int CTAS = BM == 64 && DP == 64 ? 2 : 1;  // per SM
+  // shared memory, in floats: queries, keys, values, P^T of each warp; then row offsets
+  static constexpr int Q = 0, K = Q + BM * LD, V = K + TILE * LD, P = V + TILE * LD, OFF = P + 8 * BN * 8;
+  static constexpr size_t smem = (size_t)OFF * 4 + (size_t)4 * TILE * 8;
 };
 
+__device__ __forceinline__ void sa_copy16(float* dst, const float* src, bool read) {
+  const int n = read ? 16 : 0;  // 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void sa_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void sa_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ float2 sa_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+
 template <int BM, int DP>
-__global__ void __launch_bounds__(SA_THREADS) k_paged_attn_simt(const PagedArgs a) {
+__global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_simt(const PagedArgs a) {
   using C = Sa<BM, DP>;
-  extern __shared__ float sa_sm[];
-  float* s_q = sa_sm;
-  float* s_k = s_q + BM * C::LD;
-  float* s_v = s_k + SA_BN * C::LD;
-  float* s_p = s_v + SA_BN * C::LD;
-  float* s_m = s_p + BM * C::LS;
-  float* s_l = s_m + BM;
-  float* s_a = s_l + BM;
+  extern __shared__ __align__(16) float sa_sm[];
+  float* s_q = sa_sm + C::Q;
+  float* s_k = sa_sm + C::K;
+  float* s_v = sa_sm + C::V;
+  int64_t* s_off = reinterpret_cast<int64_t*>(sa_sm + C::OFF);  // [2 tiles][keys, values][TILE]
   __shared__ int64_t scratch[33];
+  __shared__ float2 s_ml[C::SPLIT][BM];  // maxima and sums of the key ranges
+  __shared__ float s_f[BM], s_sum[BM];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tx = tid % C::TX, ty = tid / C::TX;
+  const int sp = warp / (BM / 8), tx = lane & 15;
+  const int r0 = warp % (BM / 8) * 8 + (lane >> 4) * 4;  // first of this thread's rows
+  float* s_p = sa_sm + C::P + warp * (C::BN * 8) + (lane >> 4) * 4;
 
   tc::griddep_wait();
   tc::griddep_launch_dependents();
@@ -58,220 +86,304 @@ __global__ void __launch_bounds__(SA_THREADS) k_paged_attn_simt(const PagedArgs 
     __syncthreads();
     if (!any) return;
   }
-  const int dv = a.D / 4;
   do {
     const PgItem& it = w.it;
     int j0, j1;
-    w.tiles(SA_BN, j0, j1);
+    w.tiles(C::TILE, j0, j1);
     const int t0 = it.m * a.tb, rows = min(a.tb, it.r.q - t0) * a.g;
-    const int64_t base = (int64_t)it.r.kv - it.r.q;
-    for (int i = tid; i < BM * (DP / 4); i += SA_THREADS) {
-      const int r = i / (DP / 4), c = i % (DP / 4);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rows && c < dv)
-        x = sa_load4(static_cast<const float*>(a.q) + (int64_t)(it.r.first + t0 + r / a.g) * a.q_token +
-                     (int64_t)(it.h * a.g + r % a.g) * a.q_head + 4 * c);
-      *reinterpret_cast<float4*>(s_q + r * C::LD + 4 * c) = x;
-    }
-    for (int r = tid; r < BM; r += SA_THREADS) {
-      s_m[r] = -INFINITY;
-      s_l[r] = 0.0f;
-    }
-    float acc[4][C::CS];
+    const int base = it.r.kv - it.r.q + t0;  // position of row 0
+    int pos[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < C::CS; ++c) acc[i][c] = 0.0f;
+    for (int i = 0; i < 4; ++i) pos[i] = base + pg_token(a, min(r0 + i, rows - 1));
 
-    for (int j = j0; j < j1; ++j) {
-      __syncthreads();
-      for (int i = tid; i < SA_BN * (DP / 4); i += SA_THREADS) {
-        const int r = i / (DP / 4), c = i % (DP / 4);
-        const int64_t pos = (int64_t)j * SA_BN + r;
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-        if (pos >= it.lo && pos < it.hi && c < dv) {
-          const int64_t pg = pos >> a.ps_log2, off = pos & ((1 << a.ps_log2) - 1);
-          const int id = pg < a.table_width ? a.table[(int64_t)it.n * a.table_width + pg] : -1;
-          if (id >= 0 && id < a.P) {
-            k = sa_load4(static_cast<const float*>(a.kc) + id * a.kc_page + off * a.kc_token + it.h * a.kc_head + 4 * c);
-            v = sa_load4(static_cast<const float*>(a.vc) + id * a.vc_page + off * a.vc_token + it.h * a.vc_head + 4 * c);
-          }
+    // offsets of tile j's rows (negative: not seen, or no page)
+    auto look_up = [&](int j) {
+      if (j >= j1 || tid >= C::TILE) return;
+      const int p = j * C::TILE + tid;
+      int64_t ko = -1, vo = -1;
+      if (p >= it.lo && p < it.hi) {
+        const int pg = p >> a.ps_log2, off = p & ((1 << a.ps_log2) - 1);
+        const int id = pg < a.table_width ? __ldg(a.table + (int64_t)it.n * a.table_width + pg) : -1;
+        if (id >= 0 && id < a.P) {
+          ko = id * a.kc_page + off * a.kc_token;
+          vo = id * a.vc_page + off * a.vc_token;
         }
-        *reinterpret_cast<float4*>(s_k + r * C::LD + 4 * c) = k;
-        *reinterpret_cast<float4*>(s_v + r * C::LD + 4 * c) = v;
       }
-      __syncthreads();
-      // S: rows ty * 4 + i, keys tx + TX * k
-      float s[4][C::KS];
+      s_off[(j & 1) * 2 * C::TILE + tid] = ko;
+      s_off[((j & 1) * 2 + 1) * C::TILE + tid] = vo;
+    };
+    auto load = [&](int j, int kv) {
+      const int64_t* off = s_off + ((j & 1) * 2 + kv) * C::TILE;
+      float* dst = kv ? s_v : s_k;
+      const float* src = static_cast<const float*>(kv ? a.vc : a.kc) + it.h * (kv ? a.vc_head : a.kc_head);
+#pragma unroll 4
+      for (int i = tid; i < C::TILE * (DP / 4); i += SA_THREADS) {
+        const int r = i / (DP / 4), c = i % (DP / 4) * 4;
+        const int64_t o = off[r];
+        const bool read = o >= 0 && c < a.D;
+        sa_copy16(dst + r * C::LD + c, read ? src + o + c : src, read);
+      }
+      sa_commit();
+    };
+
+    look_up(j0);
+    for (int i = tid; i < BM * (DP / 4); i += SA_THREADS) {
+      const int r = i / (DP / 4), c = i % (DP / 4) * 4, t = pg_token(a, r);
+      const bool read = r < rows && c < a.D;
+      const float* src = static_cast<const float*>(a.q);
+      if (read)
+        src += (int64_t)(it.r.first + t0 + t) * a.q_token + (int64_t)(it.h * a.g + r - t * a.g) * a.q_head + c;
+      sa_copy16(s_q + r * C::LD + c, src, read);
+    }
+    sa_commit();
+    __syncthreads();
+    if (j0 < j1) load(j0, 0);
+
+    float m[4], l[4];
+    float2 acc[4][2 * C::C4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 2 * C::C4; ++c) acc[i][c] = make_float2(0.0f, 0.0f);
+    }
+    for (int j = j0; j < j1; ++j) {
+      sa_wait();        // the keys are there,
+      __syncthreads();  // for everyone, and the values before are used
+      load(j, 1);
+      look_up(j + 1);
+      float2 s2[4][C::KS];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int k = 0; k < C::KS; ++k) s[i][k] = 0.0f;
+        for (int k = 0; k < C::KS; ++k) s2[i][k] = make_float2(0.0f, 0.0f);
+      const float* kp = s_k + (sp * C::BN + tx) * C::LD;
+      const float* qp = s_q + r0 * C::LD;
+#pragma unroll 4
       for (int d = 0; d < DP; d += 4) {
-        float4 qv[4], kv[C::KS];
+        float4 q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(s_q + (ty * 4 + i) * C::LD + d);
-#pragma unroll
-        for (int k = 0; k < C::KS; ++k) kv[k] = *reinterpret_cast<const float4*>(s_k + (tx + C::TX * k) * C::LD + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int k = 0; k < C::KS; ++k) {
-            s[i][k] = fmaf(qv[i].x, kv[k].x, s[i][k]);
-            s[i][k] = fmaf(qv[i].y, kv[k].y, s[i][k]);
-            s[i][k] = fmaf(qv[i].z, kv[k].z, s[i][k]);
-            s[i][k] = fmaf(qv[i].w, kv[k].w, s[i][k]);
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
-        const int64_t p = base + t0 + r / a.g;
+        for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(qp + i * C::LD + d);
 #pragma unroll
         for (int k = 0; k < C::KS; ++k) {
-          const int64_t pos = (int64_t)j * SA_BN + tx + C::TX * k;
-          const bool seen = r < rows && pos <= p && (!a.window || pos > p - a.window);
-          s_p[r * C::LS + tx + C::TX * k] = seen ? s[i][k] * a.scale_log2 : -INFINITY;
+          const float4 x = *reinterpret_cast<const float4*>(kp + k * 16 * C::LD + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s2[i][k] = sa_fma2(make_float2(q[i].x, q[i].y), make_float2(x.x, x.y), s2[i][k]);
+            s2[i][k] = sa_fma2(make_float2(q[i].z, q[i].w), make_float2(x.z, x.w), s2[i][k]);
+          }
         }
       }
-      __syncthreads();
-      // a warp takes BM / 8 rows, a lane two keys
+      float p[4][C::KS];
 #pragma unroll
-      for (int rr = 0; rr < BM / 8; ++rr) {
-        const int r = warp * (BM / 8) + rr;
-        const float2 x = *reinterpret_cast<const float2*>(s_p + r * C::LS + 2 * lane);
-        float mx = fmaxf(x.x, x.y);
+      for (int i = 0; i < 4; ++i) {
+        float top = -INFINITY;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float m0 = s_m[r], m1 = fmaxf(m0, mx);
+        for (int k = 0; k < C::KS; ++k) {
+          const int key = j * C::TILE + sp * C::BN + tx + 16 * k;
+          const bool seen = key <= pos[i] && (!a.window || key > pos[i] - a.window);
+          p[i][k] = seen ? (s2[i][k].x + s2[i][k].y) * a.scale_log2 : -INFINITY;
+          top = fmaxf(top, p[i][k]);
+        }
+#pragma unroll
+        for (int b = 8; b; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
+        const float m1 = fmaxf(m[i], top);
         // a row that has seen nothing yet keeps m = -inf; its weights are zero
-        const float sub = m1 == -INFINITY ? 0.0f : m1;
-        const float2 p = make_float2(exp2f(x.x - sub), exp2f(x.y - sub));
-        float sum = p.x + p.y;
+        const float sub = m1 == -INFINITY ? 0.0f : m1, f = exp2f(m[i] - sub);
+        float sum = 0.0f;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        *reinterpret_cast<float2*>(s_p + r * C::LS + 2 * lane) = p;
-        __syncwarp();
-        if (lane == 0) {
-          const float al = exp2f(m0 - sub);
-          s_a[r] = al;
-          s_m[r] = m1;
-          s_l[r] = s_l[r] * al + sum;
+        for (int k = 0; k < C::KS; ++k) {
+          p[i][k] = exp2f(p[i][k] - sub);
+          sum += p[i][k];
         }
+        m[i] = m1;
+        l[i] = l[i] * f + sum;  // over this lane's keys; over the lanes when the item ends
+#pragma unroll
+        for (int c = 0; c < 2 * C::C4; ++c) acc[i][c] = make_float2(acc[i][c].x * f, acc[i][c].y * f);
       }
-      __syncthreads();
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float al = s_a[ty * 4 + i];
+      for (int k = 0; k < C::KS; ++k)
+        *reinterpret_cast<float4*>(s_p + (tx + 16 * k) * 8) = make_float4(p[0][k], p[1][k], p[2][k], p[3][k]);
+      sa_wait();        // the values are there,
+      __syncthreads();  // for everyone, and the keys are used
+      if (j + 1 < j1) load(j + 1, 0);
+      const float* vp = s_v + sp * C::BN * C::LD + tx * 4;
+#pragma unroll 4
+      for (int k = 0; k < C::BN; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(s_p + k * 8);
+        const float pr[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int c = 0; c < C::CS; ++c) acc[i][c] *= al;
-      }
-      for (int k = 0; k < SA_BN; ++k) {
-        float p[4], v[C::CS];
+        for (int c = 0; c < C::C4; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(vp + k * C::LD + 64 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = s_p[(ty * 4 + i) * C::LS + k];
-#pragma unroll
-        for (int c = 0; c < C::CS; ++c) v[c] = s_v[k * C::LD + tx + C::TX * c];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int c = 0; c < C::CS; ++c) acc[i][c] = fmaf(p[i], v[c], acc[i][c]);
-      }
-    }
-    __syncthreads();
-    float m[4], l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = s_m[ty * 4 + i];
-      l[i] = s_l[ty * 4 + i];
-    }
-    bool last = true;
-    if (!w.whole()) {
-      int c0, c1;
-      w.owners(c0, c1);
-      float2* ml = reinterpret_cast<float2*>(a.ws + a.part_ml);
-      float* po = reinterpret_cast<float*>(a.ws + a.part_o);
-      const int slot = PgWalk::slot(w.cta, c0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
-        if (r >= rows) continue;
-        if (tx == 0) ml[(size_t)slot * a.rows + r] = make_float2(m[i], l[i]);
-#pragma unroll
-        for (int c = 0; c < C::CS; ++c)
-          po[((size_t)slot * a.rows + r) * DP + tx + C::TX * c] = acc[i][c];
-      }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t* cnt = reinterpret_cast<uint32_t*>(a.ws + 256) + c0;
-        const uint32_t had = atomicAdd(cnt, 1u);
-        s_last = had == (uint32_t)(c1 - c0);
-        if (s_last) *cnt = 0u;  // as it was found: zero between calls
-      }
-      __syncthreads();
-      last = s_last;
-      if (last) {
-        __threadfence();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          m[i] = -INFINITY;
-          l[i] = 0.0f;
-#pragma unroll
-          for (int c = 0; c < C::CS; ++c) acc[i][c] = 0.0f;
-          const int r = ty * 4 + i;
-          if (r >= rows) continue;
-          for (int q = c0; q <= c1; ++q) {
-            const size_t at = (size_t)PgWalk::slot(q, c0) * a.rows + r;
-            const float2 x = __ldcg(ml + at);
-            if (x.y == 0.0f) continue;  // saw nothing
-            const float m1 = fmaxf(m[i], x.x), f0 = exp2f(m[i] - m1), f1 = exp2f(x.x - m1);
-            m[i] = m1;
-            l[i] = l[i] * f0 + x.y * f1;
-#pragma unroll
-            for (int c = 0; c < C::CS; ++c)
-              acc[i][c] = acc[i][c] * f0 + __ldcg(po + at * DP + tx + C::TX * c) * f1;
+          for (int i = 0; i < 4; ++i) {
+            const float2 pp = make_float2(pr[i], pr[i]);
+            acc[i][2 * c] = sa_fma2(pp, make_float2(v.x, v.y), acc[i][2 * c]);
+            acc[i][2 * c + 1] = sa_fma2(pp, make_float2(v.z, v.w), acc[i][2 * c + 1]);
           }
         }
       }
     }
-    if (last) {
+    sa_wait();
+    __syncthreads();  // the tiles' memory is free
+    // the rows' parts over the key ranges to shared memory
+    float* s_o = s_k;  // [SPLIT][BM][DP]
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
-        if (r >= rows) continue;
-        const int64_t t = it.r.first + t0 + r / a.g;
-        const int hq = it.h * a.g + r % a.g;
-        const float inv = l[i] > 0.0f ? 1.0f / l[i] : l[i] == 0.0f ? 0.0f : l[i];
-        float* o = static_cast<float*>(a.o) + t * a.o_token + hq * a.o_head;
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int c = 0; c < C::CS; ++c) {
-          const int col = tx + C::TX * c;
-          if (col < a.D) o[col] = acc[i][c] * inv;
-        }
-        if (a.lse && tx == 0)
-          a.lse[t * a.Hq + hq] = l[i] == 0.0f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
-      }
+      for (int b = 8; b; b >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], b);
+      if (tx == 0) s_ml[sp][r0 + i] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int c = 0; c < C::C4; ++c)
+        *reinterpret_cast<float4*>(s_o + ((sp * BM + r0 + i) * DP + tx * 4 + 64 * c)) =
+            make_float4(acc[i][2 * c].x, acc[i][2 * c].y, acc[i][2 * c + 1].x, acc[i][2 * c + 1].y);
     }
     __syncthreads();
+    const bool whole = w.whole();
+    int c0 = w.cta, c1 = w.cta;
+    if (!whole) w.owners(c0, c1);
+    float2* g_ml = reinterpret_cast<float2*>(a.ws + a.part_ml);
+    float* g_o = reinterpret_cast<float*>(a.ws + a.part_o);
+    // one weight a range and row: 2^(m - top)
+    if (tid < BM) {
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int q = 0; q < C::SPLIT; ++q)
+        if (s_ml[q][tid].y != 0.0f) top = fmaxf(top, s_ml[q][tid].x);
+#pragma unroll
+      for (int q = 0; q < C::SPLIT; ++q) {
+        const float f = s_ml[q][tid].y != 0.0f ? exp2f(s_ml[q][tid].x - top) : 0.0f;
+        sum += s_ml[q][tid].y * f;
+        s_ml[q][tid].x = f;
+      }
+      if (tid < rows) {
+        if (!whole)
+          g_ml[(size_t)PgWalk::slot(w.cta, c0) * BM + tid] = make_float2(top, sum);
+        else if (a.lse)
+          a.lse[(int64_t)(it.r.first + t0 + pg_token(a, tid)) * a.Hq + it.h * a.g + tid - pg_token(a, tid) * a.g] =
+              sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+      }
+      s_f[tid] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+    }
+    __syncthreads();
+    auto write = [&](int r, int c, float4 x) {
+      const int t = pg_token(a, r);
+      *reinterpret_cast<float4*>(static_cast<float*>(a.o) + (int64_t)(it.r.first + t0 + t) * a.o_token +
+                                 (int64_t)(it.h * a.g + r - t * a.g) * a.o_head + c) = x;
+    };
+    for (int i = tid; i < rows * (DP / 4); i += SA_THREADS) {
+      const int r = i / (DP / 4), c = i % (DP / 4) * 4;
+      if (c >= a.D) continue;
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < C::SPLIT; ++q) {
+        const float4 o = *reinterpret_cast<const float4*>(s_o + (q * BM + r) * DP + c);
+        const float f = s_ml[q][r].x * s_f[r];
+        if (f != 0.0f) {
+          x.x = fmaf(o.x, f, x.x);
+          x.y = fmaf(o.y, f, x.y);
+          x.z = fmaf(o.z, f, x.z);
+          x.w = fmaf(o.w, f, x.w);
+        }
+      }
+      if (whole)
+        write(r, c, x);
+      else
+        *reinterpret_cast<float4*>(g_o + ((size_t)PgWalk::slot(w.cta, c0) * BM + r) * DP + c) = x;
+    }
+    __syncthreads();
+    if (!whole) {
+      if (tid == 0) {
+        __threadfence();  // cumulative: the other threads' parts, ordered before by the barrier
+        uint32_t* cnt = reinterpret_cast<uint32_t*>(a.ws + 256) + c0;
+        const bool last = atomicAdd(cnt, 1u) == (uint32_t)(c1 - c0);
+        if (last) *cnt = 0u;  // as it was found: zero between calls
+        s_last = last;
+      }
+      __syncthreads();
+      if (s_last) {
+        // the item's last CTA joins its parts, up to PARTS at a time: their weights, then the sums
+        __threadfence();
+        float2* wt = reinterpret_cast<float2*>(s_k);  // [part][row]
+        constexpr int PARTS = C::TILE * C::LD / (BM * 2), RP = SA_THREADS * 4 / DP, PASSES = (BM + RP - 1) / RP;
+        const int c = tid % (DP / 4) * 4, rr = tid / (DP / 4);
+        float4 o[PASSES];
+#pragma unroll
+        for (int k = 0; k < PASSES; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top = -INFINITY, sum = 0.0f;  // of row tid
+        for (int q0 = c0; q0 <= c1; q0 += PARTS) {
+          const int nq = min(PARTS, c1 - q0 + 1);
+          for (int i = tid; i < nq * BM; i += SA_THREADS)
+            wt[i] = i % BM < rows ? __ldcg(g_ml + (size_t)PgWalk::slot(q0 + i / BM, c0) * BM + i % BM)
+                                  : make_float2(0.0f, 0.0f);
+          __syncthreads();
+          if (tid < BM) {
+            const float m0 = top;
+            for (int q = 0; q < nq; ++q) top = fmaxf(top, wt[q * BM + tid].y != 0.0f ? wt[q * BM + tid].x : -INFINITY);
+            const float f = m0 == top ? 1.0f : exp2f(m0 - top);
+            sum *= f;
+            for (int q = 0; q < nq; ++q) {
+              const float2 x = wt[q * BM + tid];
+              const float e = x.y != 0.0f ? exp2f(x.x - top) : 0.0f;
+              sum += x.y * e;
+              wt[q * BM + tid].x = e;
+            }
+            s_f[tid] = f;
+            s_sum[tid] = sum;
+          }
+          __syncthreads();
+#pragma unroll
+          for (int k = 0; k < PASSES; ++k) {
+            const int r = rr + k * RP;
+            if (r >= rows) break;
+            const float f = s_f[r];
+            float4 x = make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f);
+#pragma unroll 4
+            for (int q = 0; q < nq; ++q) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                  g_o + ((size_t)PgWalk::slot(q0 + q, c0) * BM + r) * DP + c));
+              const float e = wt[q * BM + r].x;
+              if (e != 0.0f) x = make_float4(fmaf(e, v.x, x.x), fmaf(e, v.y, x.y), fmaf(e, v.z, x.z), fmaf(e, v.w, x.w));
+            }
+            o[k] = x;
+          }
+          __syncthreads();
+        }
+        if (tid < rows && a.lse)
+          a.lse[(int64_t)(it.r.first + t0 + pg_token(a, tid)) * a.Hq + it.h * a.g + tid - pg_token(a, tid) * a.g] =
+              sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+#pragma unroll
+        for (int k = 0; k < PASSES; ++k) {
+          const int r = rr + k * RP;
+          if (r >= rows || c >= a.D) break;
+          const float inv = s_sum[r] == 0.0f ? 0.0f : 1.0f / s_sum[r];
+          write(r, c, make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
+        }
+        __syncthreads();
+      }
+    }
   } while (w.next(a));
 }
 
 template <int BM, int DP>
 cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   using C = Sa<BM, DP>;
+  static_assert(C::SPLIT * BM * DP <= C::TILE * C::LD, "the parts of the key ranges fit the key tile");
   const size_t smem = std::max(C::smem, (size_t)(a.N + 1) * 8);
   const void* f = reinterpret_cast<const void*>(k_paged_attn_simt<BM, DP>);
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const PagedWs L = paged_ws(sms, BM, DP);
+  const int ctas = std::min(sms * C::CTAS, PG_MAX_CTAS);
+  const PagedWs L = paged_ws(ctas, BM, DP);
   a.part_ml = L.ml;
   a.part_o = L.o;
   a.rows = BM;
-  a.tb = std::max(1, BM / a.g);
-  pg_division(a, sms, 128, 256);
+  a.tb = BM / a.g;
+  pg_division(a, ctas, 128, 128);
   void* args[] = {&a};
-  return launch_pdl(f, dim3(sms), dim3(SA_THREADS), smem, s, args, 1);
+  return launch_pdl(f, dim3(ctas), dim3(SA_THREADS), smem, s, args, 1);
 }
 
 template <int BM>
@@ -283,15 +395,16 @@ cudaError_t run_d(PagedArgs& a, cudaStream_t s, int sms) {
 
 }  // namespace
 
-cudaError_t launch_paged_attn_simt(PagedArgs a, cudaStream_t s) {
+cudaError_t launch_paged_attn_simt(PagedArgs a, int rows, cudaStream_t s) {
   const int sms = sm_count();
-  if (sms < 1 || sms > PG_MAX_CTAS) return cudaErrorNotSupported;
-  return run_d<64>(a, s, sms);
+  if (sms < 1) return cudaErrorNotSupported;
+  return rows <= 16 ? run_d<16>(a, s, sms) : run_d<64>(a, s, sms);
 }
 
-size_t paged_attn_simt_ws_bytes(const paged_shape* s) {
+size_t paged_attn_simt_ws_bytes(const paged_shape* s, int rows) {
   const int sms = sm_count();
-  return paged_ws(sms > 0 ? sms : 256, 64, s->D <= 64 ? 64 : s->D <= 128 ? 128 : 256).total;
+  return paged_ws(std::min(2 * (sms > 0 ? sms : 256), PG_MAX_CTAS), rows <= 16 ? 16 : 64,
+                  s->D <= 64 ? 64 : s->D <= 128 ? 128 : 256).total;
 }
 
 }  // namespace rglru
