@@ -31,8 +31,9 @@ constexpr int SA_THREADS = 256;
 
 template <int BM, int DP>
 struct Sa {
-  static constexpr int SPLIT = BM == 64 ? 1 : 4;                    // key ranges of a tile
-  static constexpr int BN = BM == 64 || DP == 64 ? 64 : 4096 / DP;  // keys of a range
+  static constexpr int SPLIT = 64 / BM;  // key ranges of a tile
+  // keys of a range: 64, or what lets a tile of all ranges fit
+  static constexpr int BN = SPLIT == 1 ? 64 : SPLIT == 4 ? (DP == 64 ? 64 : 4096 / DP) : 2048 / DP;
   static constexpr int TILE = SPLIT * BN;
   static constexpr int KS = BN / 16;     // keys a thread
   static constexpr int C4 = DP / 64;     // times four columns of O a thread
@@ -308,6 +309,7 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
         __threadfence();
         float2* wt = reinterpret_cast<float2*>(s_k);  // [part][row]
         constexpr int PARTS = C::TILE * C::LD / (BM * 2), RP = SA_THREADS * 4 / DP, PASSES = (BM + RP - 1) / RP;
+        constexpr int BATCH = PASSES >= 16 ? 1 : 16 / PASSES;  // parts loaded at once
         const int c = tid % (DP / 4) * 4, rr = tid / (DP / 4);
         float4 o[PASSES];
 #pragma unroll
@@ -334,20 +336,30 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
             s_sum[tid] = sum;
           }
           __syncthreads();
+          if (q0 > c0)
 #pragma unroll
-          for (int k = 0; k < PASSES; ++k) {
-            const int r = rr + k * RP;
-            if (r >= rows) break;
-            const float f = s_f[r];
-            float4 x = make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f);
-#pragma unroll 4
-            for (int q = 0; q < nq; ++q) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                  g_o + ((size_t)PgWalk::slot(q0 + q, c0) * BM + r) * DP + c));
-              const float e = wt[q * BM + r].x;
-              if (e != 0.0f) x = make_float4(fmaf(e, v.x, x.x), fmaf(e, v.y, x.y), fmaf(e, v.z, x.z), fmaf(e, v.w, x.w));
+            for (int k = 0; k < PASSES; ++k) {
+              const float f = s_f[min(rr + k * RP, BM - 1)];
+              o[k] = make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f);
             }
-            o[k] = x;
+#pragma unroll 1
+          for (int q = 0; q < nq; q += BATCH) {
+            float4 v[BATCH][PASSES];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+              for (int k = 0; k < PASSES; ++k)
+                v[b][k] = __ldcg(reinterpret_cast<const float4*>(
+                    g_o + ((size_t)PgWalk::slot(q0 + min(q + b, nq - 1), c0) * BM + min(rr + k * RP, BM - 1)) * DP + c));
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b)
+#pragma unroll
+              for (int k = 0; k < PASSES; ++k) {
+                const float e = q + b < nq ? wt[(q + b) * BM + min(rr + k * RP, BM - 1)].x : 0.0f;
+                if (e != 0.0f)  // (a part that saw nothing did not write its sums)
+                  o[k] = make_float4(fmaf(e, v[b][k].x, o[k].x), fmaf(e, v[b][k].y, o[k].y),
+                                     fmaf(e, v[b][k].z, o[k].z), fmaf(e, v[b][k].w, o[k].w));
+              }
           }
           __syncthreads();
         }
@@ -398,6 +410,8 @@ cudaError_t run_d(PagedArgs& a, cudaStream_t s, int sms) {
 cudaError_t launch_paged_attn_simt(PagedArgs a, int rows, cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorNotSupported;
+  // (rows of 256 columns leave room for ranges of 16 rows only)
+  if (rows <= 8 && a.D <= 128) return a.D <= 64 ? run<8, 64>(a, s, sms) : run<8, 128>(a, s, sms);
   return rows <= 16 ? run_d<16>(a, s, sms) : run_d<64>(a, s, sms);
 }
 
