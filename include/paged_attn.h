@@ -118,7 +118,9 @@ size_t paged_attention_workspace_bytes(const paged_shape *shape);
  * in float32; with bf16 the weights exp(s_j - max) are rounded to bf16 before they meet v.
  * strides NULL: everything contiguous.  The result does not depend on timing (sums in a fixed
  * order).  A device wait that runs out marks the workspace (rglru_sync_status gives
- * RGLRU_ERR_TIMEOUT); zero it before using it again. */
+ * RGLRU_ERR_TIMEOUT); zero it before using it again.  Tests bring that about with
+ * rglru_debug_lookback(polls, cta): that CTA of a tensor-core call gets no work and its waits
+ * are limited to polls x 100 ns. */
 rglru_status paged_attention(const paged_shape *shape, const paged_strides *strides,
                              const void *q, const void *k_cache, const void *v_cache,
                              const int32_t *block_table, const int32_t *cu_seqlens,

@@ -5,8 +5,7 @@
 #include <algorithm>
 
 #include "host_util.h"
-#include "paged.cuh"
-#include "tc.cuh"
+#include "paged_tc.cuh"
 
 namespace rglru {
 
@@ -440,6 +439,9 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
   a.vc_token = t.vc_token;
   a.vc_head = t.vc_head;
   a.ws = static_cast<uint8_t*>(workspace);
+  // rglru_debug_lookback: the limit in polls, taken as 100 ns each, and the CTA without work
+  a.drop_cta = debug_drop_tile();
+  a.wait_ns = a.drop_cta >= 0 ? (uint64_t)debug_spin_limit() * 100 : TA_WAIT_NS;
   const int rows = mean_rows(s);
   if (s->io == RGLRU_F32) return cuda_status(launch_paged_attn_simt(a, rows, stream));
   return cuda_status(rows <= PG_FEW_ROWS ? launch_paged_attn_few(a, rows, stream)

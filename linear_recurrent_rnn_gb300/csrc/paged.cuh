@@ -47,6 +47,8 @@ struct PagedArgs {
   uint8_t* ws;
   size_t part_ml, part_o;  // workspace offsets (below)
   int rows;                // rows of a partial result
+  uint64_t wait_ns;        // limit of a device wait; CTA that hands out no work (tests; -1: none)
+  int drop_cta;
   int o_32;                // rows of o are multiples of 32 bytes on 32-byte boundaries
 };
 

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
   __shared__ __align__(16) float s_ref[NR], s_scale[NR];  // the rows' references; factors of a change
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int role = warp - TF_SOFT / 32;  // < 0: softmax; 0: loader, 1: MMA, 2: clearing, 3: walk and queries
-  const TaAbort ctl{&s_flag, reinterpret_cast<uint32_t*>(a.ws)};
+  const TaAbort ctl{&s_flag, reinterpret_cast<uint32_t*>(a.ws), a.wait_ns};
 
   // up to griddep_wait nothing touches global memory
   if (tid == 0) {
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
       }
       if (lane == 0) {
         s_item[ni % TA_ITEMS] = x;
-        tc::mbar_arrive(&i_full[ni % TA_ITEMS]);
+        if (a.drop_cta != (int)blockIdx.x) tc::mbar_arrive(&i_full[ni % TA_ITEMS]);
       }
       __syncwarp();
       if (!more) break;
@@ -625,13 +625,13 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
     // a wait ran out: copies and products in flight end (or run out too) before the CTA leaves
     for (uint32_t i = lane; i < min(s_issued[1], (uint32_t)C::STAGES); i += 32) {
       const uint32_t n = s_issued[1] - 1 - i;
-      tc::mbar_wait(&full[n % C::STAGES], n / C::STAGES & 1, TA_WAIT_NS);
+      tc::mbar_wait(&full[n % C::STAGES], n / C::STAGES & 1, a.wait_ns);
     }
     for (uint32_t i = lane; i < min(s_issued[0], (uint32_t)C::QBUF); i += 32) {
       const uint32_t n = s_issued[0] - 1 - i;
-      tc::mbar_wait(&q_full[n % C::QBUF], n / C::QBUF & 1, TA_WAIT_NS);
+      tc::mbar_wait(&q_full[n % C::QBUF], n / C::QBUF & 1, a.wait_ns);
     }
-    tc::mbar_wait(drain, 0, TA_WAIT_NS);
+    tc::mbar_wait(drain, 0, a.wait_ns);
   }
   __syncthreads();
   if (role == 1) {

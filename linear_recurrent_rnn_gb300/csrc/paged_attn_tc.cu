@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   __shared__ uint32_t s_issued[NT + 1];  // loads issued: queries of each tile, ring units
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tb1 = max(1, 128 / a.g);  // tokens of a row tile
-  const TaAbort ctl{s_flag, reinterpret_cast<uint32_t*>(a.ws)};
+  const TaAbort ctl{s_flag, reinterpret_cast<uint32_t*>(a.ws), a.wait_ns};
 
   // up to griddep_wait nothing touches global memory
   if (tid == 0) {
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
         }
         if (lane == 0) {
           s_item[ni % TA_ITEMS] = x;
-          tc::mbar_arrive(&i_full[ni % TA_ITEMS]);
+          if (a.drop_cta != (int)blockIdx.x) tc::mbar_arrive(&i_full[ni % TA_ITEMS]);
         }
         __syncwarp();
         ++ni;
@@ -638,11 +638,11 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
     // a wait ran out: copies and products in flight end (or run out too) before the CTA leaves
     for (uint32_t i = lane; i < min(s_issued[NT], (uint32_t)C::STAGES); i += 32) {
       const uint32_t n = s_issued[NT] - 1 - i;
-      tc::mbar_wait(&full[n % C::STAGES], n / C::STAGES & 1, TA_WAIT_NS);
+      tc::mbar_wait(&full[n % C::STAGES], n / C::STAGES & 1, a.wait_ns);
     }
     for (int t = 0; t < NT; ++t)
-      if (s_issued[t]) tc::mbar_wait(&q_full[t], (s_issued[t] - 1) & 1, TA_WAIT_NS);
-    tc::mbar_wait(drain, 0, TA_WAIT_NS);
+      if (s_issued[t]) tc::mbar_wait(&q_full[t], (s_issued[t] - 1) & 1, a.wait_ns);
+    tc::mbar_wait(drain, 0, a.wait_ns);
   }
   __syncthreads();
   if (warp == C::SOFT / 32 + 1) {

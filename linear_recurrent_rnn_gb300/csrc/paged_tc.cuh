@@ -11,12 +11,13 @@
 namespace rglru {
 
 constexpr int TA_BN = 128;                     // keys of a tile
-constexpr uint64_t TA_WAIT_NS = 2000000000ull;
+constexpr uint64_t TA_WAIT_NS = 2000000000ull;  // a wait's limit: far above any time it can take
 constexpr uint32_t TA_SLAB = 128 * 128;        // 64 columns of 128 rows
 
 struct TaAbort {
-  uint32_t* flag;   // shared: set once a wait has run out
-  uint32_t* status; // global
+  uint32_t* flag;     // shared: set once a wait has run out
+  uint32_t* status;   // global
+  uint64_t limit_ns;  // of a wait
   // By a converged warp; the answer is the same in all its lanes.
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
     bool ok = tc::mbar_try_wait(bar, parity);
@@ -31,7 +32,7 @@ struct TaAbort {
     const uint64_t t0 = tc::global_ns();
     while (!tc::mbar_try_wait_sleep(bar, parity, 20000u)) {
       if (*reinterpret_cast<volatile uint32_t*>(flag)) return false;
-      if (tc::global_ns() - t0 > TA_WAIT_NS) {
+      if (tc::global_ns() - t0 > limit_ns) {
         *reinterpret_cast<volatile uint32_t*>(flag) = 1u;
         *reinterpret_cast<volatile uint32_t*>(status) = 1u;
         return false;
