@@ -9,7 +9,8 @@
 // [W i, W (i + 1)), W = U / CTAs rounded up: every CTA gets the same weight whatever the mix of lengths
 // (one long request, many short ones, prefill among decode), and no host knowledge of lengths
 // is needed.  An item cut by such a boundary is computed in parts, each over a range of whole
-// key tiles, and joined by the last of its CTAs to finish.  Prefix sums over the row tiles of
+// key tiles, and joined by the last of its CTAs to finish; a cut that would leave a part of less
+// than `snap` moves to the item's end, as parts cost more than a small difference of weight.  Prefix sums over the row tiles of
 // a request are sums of max(0, a + m tb) over m, so they have a closed form; only the sum over
 // requests is a scan.  All of it is done by every CTA for itself (no kernel before, no host
 // synchronisation), so it is in the way of the first load and kept short: no 64-bit division.
@@ -26,6 +27,7 @@ namespace rglru {
 
 constexpr int PG_MAX_SEQS = 8192;
 constexpr int PG_MAX_CTAS = 1024;
+constexpr int PG_WARP_SEQS = 32;  // requests that one warp scans alone
 
 struct PagedArgs {
   int N, T, Hq, Hkv, g, D, P, ps_log2, table_width, window;
@@ -34,6 +36,7 @@ struct PagedArgs {
   int overhead;    // weight of an item beyond its keys: its switch, in keys' time
   uint64_t grid_inv;
   int min_weight;  // least weight of a CTA: below it splitting costs more than it saves
+  int snap;        // least weight of a part (at most a quarter of a CTA's)
   float scale_log2;  // scale * log2(e): scores in units of log2
   const void* q;
   const void* kc;
@@ -67,11 +70,13 @@ inline PagedWs paged_ws(int ctas, int rows, int Dp) {
   return w;
 }
 
-// The division's constants: CTAs of the launch, an item's weight beyond its keys, a CTA's least.
-inline void pg_division(PagedArgs& a, int grid, int overhead, int min_weight) {
+// The division's constants: CTAs of the launch, an item's weight beyond its keys, a CTA's and a
+// part's least.
+inline void pg_division(PagedArgs& a, int grid, int overhead, int min_weight, int snap) {
   a.grid_inv = ~0ull / grid + 1;
   a.overhead = overhead;
   a.min_weight = min_weight;
+  a.snap = snap;
 }
 
 struct PgReq {
@@ -186,48 +191,94 @@ struct PgItem {
 // the same items.
 struct PgWalk {
   int64_t W, w0, w1;
-  int cta;
+  int cta, snap;
   PgItem it;
 
-  // `prefix` as left by pg_scan.  Returns false if the CTA has no work.
-  __device__ __forceinline__ bool start(const PagedArgs& a, const int64_t* prefix) {
-    const int64_t U = prefix[a.N];
+  // The CTA's range of a line of weight U; false if there is none.
+  __device__ __forceinline__ bool range(const PagedArgs& a, int64_t U) {
     cta = blockIdx.x;
     // U / grid, rounded up: grid_inv is 2^64 / grid, rounded up (exact for U grid < 2^64)
     W = max((int64_t)__umul64hi((uint64_t)U + gridDim.x - 1, a.grid_inv), (int64_t)a.min_weight);
+    snap = (int)min((int64_t)a.snap, W >> 2);
     w0 = W * cta;
     w1 = min(w0 + W, U);
-    if (w0 >= U) return false;
-    // the request, head and row tile that hold w0
+    return w0 < U;
+  }
+  // Begins at w0, in a request whose heads weigh hw each and which begins at `at`.
+  __device__ __forceinline__ bool enter(const PagedArgs& a, int n, const PgReq& r, int64_t at, int64_t hw) {
+    it.n = n;
+    it.r = r;
+    int64_t x = w0 - at;
+    it.h = pg_div(x, hw);
+    x -= it.h * hw;
+    it.m = 0;
+    it.at = w0 - x;
+    if (r.q > a.tb) {
+      int ml = 0, mh = pg_tiles(a, r) - 1;
+      while (ml < mh) {
+        const int mid = (ml + mh + 1) >> 1;
+        if (pg_prefix(a, r, mid) <= x) ml = mid; else mh = mid - 1;
+      }
+      it.m = ml;
+      it.at += pg_prefix(a, r, ml);
+    }
+    fill(a);
+    const int64_t d = w0 - it.at;
+    if (d > 0) {  // the cut is inside the item
+      if (d < snap)
+        w0 = it.at;
+      else if (it.w - d < snap) {
+        w0 = it.at + it.w;
+        return next(a);
+      }
+    }
+    return it.at < w1;
+  }
+  // `prefix` as left by pg_scan.  Returns false if the CTA has no work.
+  __device__ __forceinline__ bool start(const PagedArgs& a, const int64_t* prefix) {
+    if (!range(a, prefix[a.N])) return false;
     int l = 0, h = a.N - 1;
     while (l < h) {
       const int mid = (l + h + 1) >> 1;
       if (prefix[mid] <= w0) l = mid; else h = mid - 1;
     }
     // (requests without rows have no weight: l is the last one that starts at or before w0)
-    it.n = l;
-    it.r = pg_request(a, l);
-    const int64_t hw = pg_head_weight(a, it.r);
-    int64_t x = w0 - prefix[l];
-    it.h = pg_div(x, hw);
-    x -= it.h * hw;
-    it.m = 0;
-    it.at = w0 - x;
-    if (it.r.q > a.tb) {
-      int ml = 0, mh = pg_tiles(a, it.r) - 1;
-      while (ml < mh) {
-        const int mid = (ml + mh + 1) >> 1;
-        if (pg_prefix(a, it.r, mid) <= x) ml = mid; else mh = mid - 1;
-      }
-      it.m = ml;
-      it.at += pg_prefix(a, it.r, ml);
+    const PgReq r = pg_request(a, l);
+    return enter(a, l, r, prefix[l], pg_head_weight(a, r));
+  }
+  // The same for up to 32 requests, one a lane, by a whole warp without shared memory.
+  __device__ __forceinline__ bool start_warp(const PagedArgs& a) {
+    const int lane = threadIdx.x & 31;
+    PgReq r = {0, 0, 0};
+    int64_t hw = 0;
+    if (lane < a.N) {
+      r = pg_request(a, lane);
+      hw = pg_head_weight(a, r);
     }
-    fill(a);
-    return true;
+    const int64_t w = hw * a.Hkv;
+    int64_t s = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += u;
+    }
+    if (!range(a, __shfl_sync(0xffffffffu, s, 31))) return false;
+    const int l = 31 - __clz(__ballot_sync(0xffffffffu, w > 0 && s - w <= w0));
+    r.first = __shfl_sync(0xffffffffu, r.first, l);
+    r.q = __shfl_sync(0xffffffffu, r.q, l);
+    r.kv = __shfl_sync(0xffffffffu, r.kv, l);
+    return enter(a, l, r, __shfl_sync(0xffffffffu, s - w, l), __shfl_sync(0xffffffffu, hw, l));
   }
   __device__ __forceinline__ void fill(const PagedArgs& a) {
     pg_range(a, it.r, it.m, it.lo, it.hi);
     it.w = it.hi - it.lo + a.overhead;
+    const int64_t d = w1 - it.at;
+    if (d > 0 && d < it.w) {  // the CTA's other cut
+      if (d < snap)
+        w1 = it.at;
+      else if (it.w - d < snap)
+        w1 = it.at + it.w;
+    }
   }
   // The next item; false past the CTA's range.
   __device__ __forceinline__ bool next(const PagedArgs& a) {
@@ -243,7 +294,7 @@ struct PgWalk {
       }
     }
     fill(a);
-    return true;
+    return it.at < w1;
   }
   // The CTA's key tiles [j0, j1) of the item, tiles of `bn` keys counted from position 0.
   // A cut at x of the item's weight w gives the parts about tiles x / w of its tiles, rounded in
@@ -259,10 +310,18 @@ struct PgWalk {
     return min((int)__fmul_rn(__fmul_rn((float)x, pg_rcp((float)it.w)), (float)nt), nt);
   }
   __device__ __forceinline__ bool whole() const { return w0 <= it.at && it.at + it.w <= w1; }
-  // CTAs [first, last] that share the item.
+  // CTAs [first, last] that share the item: where it begins and ends on the line, but for a cut
+  // that has moved to its end.
   __device__ __forceinline__ void owners(int& first, int& last) const {
-    first = it.at >= w0 ? cta : pg_div(it.at, W);
-    last = it.at + it.w <= w1 ? cta : pg_div(it.at + it.w - 1, W);
+    first = last = cta;
+    if (it.at < w0) {
+      first = pg_div(it.at, W);
+      if ((first + 1) * W - it.at < snap) ++first;
+    }
+    if (it.at + it.w > w1) {
+      last = pg_div(it.at + it.w - 1, W);
+      if (it.at + it.w - last * W < snap) --last;
+    }
   }
   // Partial-result slot of CTA c for an item whose first CTA is `first`.
   __device__ __forceinline__ static int slot(int c, int first) { return 2 * c + (c == first); }

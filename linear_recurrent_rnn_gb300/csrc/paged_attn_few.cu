@@ -171,16 +171,23 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
   // rows of the query buffers that no copy fills stay zero
   for (uint32_t i = tid; i < C::QBUF * C::QB / 16; i += TF_THREADS)
     reinterpret_cast<uint4*>(s_q)[i] = make_uint4(0, 0, 0, 0);
-  tc::griddep_wait();
-  tc::griddep_launch_dependents();
-  PgWalk w;
-  int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
-  pg_scan(a, prefix, scratch);
-  bool more = role == 3 && w.start(a, prefix);
   tc::fence_proxy_async_smem();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  PgWalk w;
+  bool more = false;
+  if (a.N <= PG_WARP_SEQS) {
+    if (role == 3) more = w.start_warp(a);
+  } else {
+    int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
+    pg_scan(a, prefix, scratch);
+    if (role == 3) more = w.start(a, prefix);
+    tc::fence_proxy_async_smem();
+    __syncthreads();
+  }
   const uint32_t tmem = tmem_holder;
 
   if (role < 0) {
@@ -656,7 +663,7 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   a.part_o = L.o;
   a.rows = NR;
   // an item's switch costs about a key tile's time
-  pg_division(a, sms, 128, 128);
+  pg_division(a, sms, 128, 128, 128);
   void* args[] = {&mq, &mk, &mv, &a};
   return launch_pdl(f, dim3(sms), dim3(TF_THREADS), C::smem, s, args, 1);
 }

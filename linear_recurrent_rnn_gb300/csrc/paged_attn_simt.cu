@@ -80,7 +80,9 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
   tc::griddep_wait();
   tc::griddep_launch_dependents();
   PgWalk w;
-  {
+  if (a.N <= PG_WARP_SEQS) {
+    if (!w.start_warp(a)) return;
+  } else {
     int64_t* prefix = reinterpret_cast<int64_t*>(sa_sm);  // before the tiles are in use
     pg_scan(a, prefix, scratch);
     const bool any = w.start(a, prefix);
@@ -393,7 +395,7 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   a.part_o = L.o;
   a.rows = BM;
   a.tb = BM / a.g;
-  pg_division(a, ctas, 128, 128);
+  pg_division(a, ctas, 128, 128, 128);
   void* args[] = {&a};
   return launch_pdl(f, dim3(ctas), dim3(SA_THREADS), smem, s, args, 1);
 }

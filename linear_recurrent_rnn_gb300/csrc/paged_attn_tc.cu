@@ -221,17 +221,23 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
     tc::tmem_alloc(tmem_holder, 512);
     tc::tmem_relinquish();
   }
-  tc::griddep_wait();
-  tc::griddep_launch_dependents();
   const int role = warp - C::SOFT / 32;  // < 0: softmax; 0: keys and values, 1: MMA, 2: clearing, 3: walk and queries
-  PgWalk w;
-  int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
-  pg_scan(a, prefix, scratch);
-  bool more = role == 3 && w.start(a, prefix);
-  tc::fence_proxy_async_smem();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  PgWalk w;
+  bool more = false;
+  if (a.N <= PG_WARP_SEQS) {
+    if (role == 3) more = w.start_warp(a);
+  } else {
+    int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
+    pg_scan(a, prefix, scratch);
+    if (role == 3) more = w.start(a, prefix);
+    tc::fence_proxy_async_smem();
+    __syncthreads();
+  }
   const uint32_t tmem = *tmem_holder;
 
   uint32_t ni = 0;  // items so far
@@ -670,7 +676,7 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   a.tb = C::NT * tb1;
   a.o_32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_token % 16 == 0 && a.o_head % 16 == 0 && a.D % 16 == 0;
   // the switch of an item costs two row tiles about 9000 cycles, three key tiles' time
-  pg_division(a, sms, C::NT == 2 ? 384 : 256, 256);
+  pg_division(a, sms, C::NT == 2 ? 384 : 256, 256, C::NT == 2 ? 768 : 384);
   void* args[] = {&mq, &mk, &mv, &a};
   return launch_pdl(f, dim3(sms), dim3(C::THREADS), C::smem, s, args, 1);
 }
