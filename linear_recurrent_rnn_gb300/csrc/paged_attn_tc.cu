@@ -52,6 +52,8 @@ struct Ta {
   static constexpr size_t smem = 1024 + Q_BYTES + STAGES * UB + 768;
 };
 
+constexpr int TA_HERE = 4;  // parts that are joined without handing over the last one
+
 // Row tile t of an item and its key tiles within the CTA's part.
 struct TaTile {
   int tok, rows, ja, jb;
@@ -167,7 +169,8 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   uint64_t* o_empty = pv_done + NT;      // [NT] O of tile t read
   uint64_t* j_full = o_empty + NT;       // a part of an item is in the workspace
   uint64_t* j_go = j_full + 1;           // s_last says whether this CTA joins the item
-  uint64_t* i_full = j_go + 1;           // [TA_ITEMS] item records
+  uint64_t* j_here = j_go + 1;           // [TA_ITEMS] s_here says whether this CTA has the last part
+  uint64_t* i_full = j_here + TA_ITEMS;           // [TA_ITEMS] item records
   uint64_t* i_empty = i_full + TA_ITEMS;
   uint64_t* v_come = i_empty + TA_ITEMS;  // [TA_CLEARS] a value tile to clear is on its way
   uint64_t* v_clean = v_come + TA_CLEARS; // [TA_CLEARS] it is cleared
@@ -178,6 +181,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   __shared__ int64_t scratch[33];
   __shared__ TaItem s_item[TA_ITEMS];
   __shared__ TaClear s_clear[TA_CLEARS];
+  __shared__ uint32_t s_here[TA_ITEMS];
   __shared__ uint32_t s_issued[NT + 1];  // loads issued: queries of each tile, ring units
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tb1 = max(1, 128 / a.g);  // tokens of a row tile
@@ -202,6 +206,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
     tc::mbar_init(j_full, C::SOFT / 32);
     tc::mbar_init(j_go, 1);
     for (int i = 0; i < TA_ITEMS; ++i) {
+      tc::mbar_init(&j_here[i], 1);
       tc::mbar_init(&i_full[i], 1);
       tc::mbar_init(&i_empty[i], C::SOFT / 32 + 2);
     }
@@ -261,7 +266,8 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t t_o = lanes + C::O_COL + t * DP;
     const float sc = a.scale_log2;
-    uint32_t cs = 0, npv = 0, nj = 0;  // S taken, products P V of this tile, joins
+    uint32_t cs = 0, npv = 0, nj = 0;  // S taken, products P V of this tile, parts handed over
+    uint32_t here_par = 0;             // parities of j_here
     bool ok = true;
     const TaItem* rec;
     while (ok && (rec = next_item())) {
@@ -353,6 +359,26 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
       }
       if (!ok) break;
       const bool any = tl.jb > tl.ja;
+      // If all other parts of an item are there by now, this CTA joins them to its own in TMEM.
+      const int parts = it.c1 - it.c0 + 1;
+      bool here = parts == 1;
+      if (parts > 1 && parts <= TA_HERE) {
+        const uint32_t k = ni % TA_ITEMS;
+        if (tid == 0) {
+          uint32_t* cnt = reinterpret_cast<uint32_t*>(a.ws + 256) + it.c0;
+          uint32_t had;
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(had) : "l"(cnt) : "memory");
+          const bool all = had == (uint32_t)(parts - 1);
+          if (all) *cnt = 0u;  // as it was found: zero between calls
+          *reinterpret_cast<volatile uint32_t*>(&s_here[k]) = all;
+          tc::mbar_arrive(&j_here[k]);
+        }
+        __syncwarp();
+        ok = ctl.wait(&j_here[k], here_par >> k & 1);
+        if (!ok) break;
+        here_par ^= 1u << k;
+        here = *reinterpret_cast<volatile uint32_t*>(&s_here[k]);
+      }
       if (any) {
         npv += tl.jb - tl.ja;
         ok = ctl.wait(&pv_done[t], (npv - 1) & 1);
@@ -361,12 +387,26 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
       }
       const bool mine = r < tl.rows;
       const int row = t * 128 + r;
-      if (it.c0 == it.c1) {
+      constexpr int R = NT * 128;
+      const float2* g_ml = reinterpret_cast<const float2*>(a.ws + a.part_ml);
+      const float* g_o = reinterpret_cast<const float*>(a.ws + a.part_o);
+      const float2 own = make_float2(m == -INFINITY ? m : m * sc, l);
+      if (here) {
         if (live) {
           const int64_t tok = it.first + tl.tok + my_tok;
           const int hq = it.h * a.g + min(r, tl.rows - 1) - my_tok * a.g;
           bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          float top = own.x, sum = l;
+          auto part = [&](int q) { return q == (int)blockIdx.x ? own : __ldcg(g_ml + (size_t)PgWalk::slot(q, it.c0) * R + row); };
+          if (parts > 1) {
+            top = -INFINITY;
+            for (int q = it.c0; q <= it.c1; ++q)
+              if (part(q).y != 0.0f) top = fmaxf(top, part(q).x);
+            sum = 0.0f;
+            for (int q = it.c0; q <= it.c1; ++q)
+              if (part(q).y != 0.0f) sum += part(q).y * ta_ex2(part(q).x - top);
+          }
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll 1
           for (int c = 0; c < DP && c < a.D; c += 32) {
             float v[32];
@@ -376,10 +416,34 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
               tc::tmem_ld_wait();
               tc::reg_fence(v);
             }
+            if (parts > 1) {
+              float acc[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) acc[e] = 0.0f;
+#pragma unroll 1
+              for (int q = it.c0; q <= it.c1; ++q) {
+                const float2 x = part(q);
+                if (x.y == 0.0f) continue;  // saw nothing: its sums were not written
+                const float f = ta_ex2(x.x - top);
+                if (q == (int)blockIdx.x) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) acc[e] = fmaf(v[e], f, acc[e]);
+                } else {
+                  const float* po = g_o + ((size_t)PgWalk::slot(q, it.c0) * DP + c) * R + row;
+                  float u[32];
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) u[e] = __ldcg(po + e * R);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) acc[e] = fmaf(u[e], f, acc[e]);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = acc[e];
+            }
             uint32_t u[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              u[e] = l == 0.0f ? 0u : ta_pack(v[2 * e] * inv, v[2 * e + 1] * inv);
+              u[e] = sum == 0.0f ? 0u : ta_pack(v[2 * e] * inv, v[2 * e + 1] * inv);
             if (mine) {
               if (a.o_32) {  // whole 32-byte sectors a store: half as many passes through L1
                 ta_store32(o + c, u);
@@ -394,7 +458,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
             }
           }
           if (mine && a.lse)
-            a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m * sc + log2f(l)) * 0.69314718055994531f;
+            a.lse[tok * a.Hq + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
         }
         if (any) {
           tc::tc_fence_before();
@@ -403,23 +467,20 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
         }
       } else {
         // a part: maxima, sums and unscaled O to the workspace; the last CTA of the item joins them
-        const size_t slot = it.slot;
-        const int R = NT * 128;
         if (live) {
-          if (mine)
-            reinterpret_cast<float2*>(a.ws + a.part_ml)[slot * R + row] =
-                make_float2(m == -INFINITY ? m : m * sc, l);
+          if (mine) const_cast<float2*>(g_ml)[(size_t)it.slot * R + row] = own;
           if (any) {
-            float* po = reinterpret_cast<float*>(a.ws + a.part_o) + slot * DP * R + row;
+            float* po = const_cast<float*>(g_o) + (size_t)it.slot * DP * R + row;
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
-              float v[16];
-              tc::tmem_ld16(t_o + c, v);
+            for (int c = 0; c < DP; c += 32) {
+              float v[32];
+              tc::tmem_ld16(t_o + c, *reinterpret_cast<float(*)[16]>(v));
+              tc::tmem_ld16(t_o + c + 16, *reinterpret_cast<float(*)[16]>(v + 16));
               tc::tmem_ld_wait();
               tc::reg_fence(v);
               if (mine)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) po[(size_t)(c + e) * R] = v[e];
+                for (int e = 0; e < 32; ++e) po[(size_t)(c + e) * R] = v[e];
             }
           }
         }
