@@ -148,6 +148,21 @@ __device__ __forceinline__ int pg_div(int64_t x, int64_t y) {
   return q;
 }
 
+// The last n < count with f(n) true, f true up to there and f(0) true; by a converged warp, 32
+// places at a time.
+template <class F>
+__device__ __forceinline__ int pg_last(int count, F f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = count;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, at = lane * step;
+    const int k = __popc(__ballot_sync(0xffffffffu, at < n && f(lo + at))) - 1;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
 // Sum over the requests by the whole CTA: prefix[n] = weight of the requests before n (n <= N).
 // `prefix` and the 33-entry `scratch` in shared memory; ends with a CTA barrier.
 __device__ __forceinline__ void pg_scan(const PagedArgs& a, int64_t* prefix, int64_t* scratch) {
@@ -204,70 +219,73 @@ struct PgWalk {
     w1 = min(w0 + W, U);
     return w0 < U;
   }
-  // Begins at w0, in a request whose heads weigh hw each and which begins at `at`.
-  __device__ __forceinline__ bool enter(const PagedArgs& a, int n, const PgReq& r, int64_t at, int64_t hw) {
-    it.n = n;
-    it.r = r;
-    int64_t x = w0 - at;
-    it.h = pg_div(x, hw);
-    x -= it.h * hw;
-    it.m = 0;
-    it.at = w0 - x;
-    if (r.q > a.tb) {
-      int ml = 0, mh = pg_tiles(a, r) - 1;
-      while (ml < mh) {
-        const int mid = (ml + mh + 1) >> 1;
-        if (pg_prefix(a, r, mid) <= x) ml = mid; else mh = mid - 1;
-      }
-      it.m = ml;
-      it.at += pg_prefix(a, r, ml);
-    }
-    fill(a);
-    const int64_t d = w0 - it.at;
-    if (d > 0) {  // the cut is inside the item
-      if (d < snap)
-        w0 = it.at;
-      else if (it.w - d < snap) {
-        w0 = it.at + it.w;
-        return next(a);
-      }
-    }
-    return it.at < w1;
-  }
-  // `prefix` as left by pg_scan.  Returns false if the CTA has no work.
-  __device__ __forceinline__ bool start(const PagedArgs& a, const int64_t* prefix) {
-    if (!range(a, prefix[a.N])) return false;
-    int l = 0, h = a.N - 1;
-    while (l < h) {
-      const int mid = (l + h + 1) >> 1;
-      if (prefix[mid] <= w0) l = mid; else h = mid - 1;
-    }
+  // The request that holds w0 (r.q = 0: the CTA has no work), its place and one head's weight;
+  // `prefix` as left by pg_scan.
+  struct Found {
+    int n;
+    PgReq r;
+    int64_t at, hw;
+  };
+  __device__ __forceinline__ Found find(const PagedArgs& a, const int64_t* prefix) {
+    Found f = {0, {0, 0, 0}, 0, 0};
+    if (!range(a, prefix[a.N])) return f;
+    const int l = pg_last(a.N, [&](int n) { return prefix[n] <= w0; });
     // (requests without rows have no weight: l is the last one that starts at or before w0)
-    const PgReq r = pg_request(a, l);
-    return enter(a, l, r, prefix[l], pg_head_weight(a, r));
+    f.n = l;
+    f.r = pg_request(a, l);
+    f.at = prefix[l];
+    f.hw = pg_head_weight(a, f.r);
+    return f;
   }
   // The same for up to 32 requests, one a lane, by a whole warp without shared memory.
-  __device__ __forceinline__ bool start_warp(const PagedArgs& a) {
+  __device__ __forceinline__ Found find_warp(const PagedArgs& a) {
     const int lane = threadIdx.x & 31;
-    PgReq r = {0, 0, 0};
-    int64_t hw = 0;
+    Found f = {0, {0, 0, 0}, 0, 0};
     if (lane < a.N) {
-      r = pg_request(a, lane);
-      hw = pg_head_weight(a, r);
+      f.r = pg_request(a, lane);
+      f.hw = pg_head_weight(a, f.r);
     }
-    const int64_t w = hw * a.Hkv;
+    const int64_t w = f.hw * a.Hkv;
     int64_t s = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t u = __shfl_up_sync(0xffffffffu, s, d);
       if (lane >= d) s += u;
     }
-    if (!range(a, __shfl_sync(0xffffffffu, s, 31))) return false;
-    const int l = 31 - __clz(__ballot_sync(0xffffffffu, w > 0 && s - w <= w0));
-    r.first = __shfl_sync(0xffffffffu, r.first, l);
-    r.q = __shfl_sync(0xffffffffu, r.q, l);
-    r.kv = __shfl_sync(0xffffffffu, r.kv, l);
-    return enter(a, l, r, __shfl_sync(0xffffffffu, s - w, l), __shfl_sync(0xffffffffu, hw, l));
+    const bool any = range(a, __shfl_sync(0xffffffffu, s, 31));
+    const uint32_t before = __ballot_sync(0xffffffffu, w > 0 && s - w <= w0);
+    f.n = before ? 31 - __clz(before) : 0;
+    f.at = __shfl_sync(0xffffffffu, s - w, f.n);
+    f.hw = __shfl_sync(0xffffffffu, f.hw, f.n);
+    f.r.first = __shfl_sync(0xffffffffu, f.r.first, f.n);
+    f.r.kv = __shfl_sync(0xffffffffu, f.r.kv, f.n);
+    f.r.q = __shfl_sync(0xffffffffu, f.r.q, f.n);
+    if (!any) f.r.q = 0;
+    return f;
+  }
+  // Begins at w0.  False if the CTA has no work.
+  __device__ __forceinline__ bool enter(const PagedArgs& a, const Found& f) {
+    if (f.r.q == 0) return false;
+    it.n = f.n;
+    it.r = f.r;
+    int64_t x = w0 - f.at;
+    it.h = pg_div(x, f.hw);
+    x -= it.h * f.hw;
+    it.m = 0;
+    it.at = w0 - x;
+    if (it.r.q > a.tb) {
+      it.m = pg_last(pg_tiles(a, it.r), [&](int m) { return pg_prefix(a, it.r, m) <= x; });
+      it.at += pg_prefix(a, it.r, it.m);
+    }
+    fill(a);
+    const int64_t d = w0 - it.at;
+    if (d > 0) {  // the cut is inside the item
+      if (d < snap)
+        w0 = it.at;
+      else if (it.w - d < snap)
+        w0 = it.at + it.w;  // the item is the neighbour's
+    }
+    return it.at + it.w > w0 ? it.at < w1 : next(a);
   }
   __device__ __forceinline__ void fill(const PagedArgs& a) {
     pg_range(a, it.r, it.m, it.lo, it.hi);

@@ -171,23 +171,21 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
   // rows of the query buffers that no copy fills stay zero
   for (uint32_t i = tid; i < C::QBUF * C::QB / 16; i += TF_THREADS)
     reinterpret_cast<uint4*>(s_q)[i] = make_uint4(0, 0, 0, 0);
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  PgWalk w;
+  PgWalk::Found start;
+  if (a.N <= PG_WARP_SEQS) {
+    if (role == 3) start = w.find_warp(a);
+  } else {
+    int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
+    pg_scan(a, prefix, scratch);
+    if (role == 3) start = w.find(a, prefix);
+  }
   tc::fence_proxy_async_smem();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  tc::griddep_wait();
-  tc::griddep_launch_dependents();
-  PgWalk w;
-  bool more = false;
-  if (a.N <= PG_WARP_SEQS) {
-    if (role == 3) more = w.start_warp(a);
-  } else {
-    int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
-    pg_scan(a, prefix, scratch);
-    if (role == 3) more = w.start(a, prefix);
-    tc::fence_proxy_async_smem();
-    __syncthreads();
-  }
   const uint32_t tmem = tmem_holder;
 
   if (role < 0) {
@@ -583,6 +581,7 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
   } else {
     // ------------------------------------------------------------ walk, and queries
     uint32_t n = 0;  // query loads
+    bool more = w.enter(a, start);
     const uint32_t bytes = C::SLABS * a.tb * a.g * 128;
     bool ok = true;
     for (uint32_t ni = 0; ok; ++ni) {

@@ -80,15 +80,16 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
   tc::griddep_wait();
   tc::griddep_launch_dependents();
   PgWalk w;
+  PgWalk::Found start;
   if (a.N <= PG_WARP_SEQS) {
-    if (!w.start_warp(a)) return;
+    start = w.find_warp(a);
   } else {
     int64_t* prefix = reinterpret_cast<int64_t*>(sa_sm);  // before the tiles are in use
     pg_scan(a, prefix, scratch);
-    const bool any = w.start(a, prefix);
+    start = w.find(a, prefix);
     __syncthreads();
-    if (!any) return;
   }
+  if (!w.enter(a, start)) return;
   do {
     const PgItem& it = w.it;
     int j0, j1;

@@ -233,13 +233,13 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   tc::griddep_wait();
   tc::griddep_launch_dependents();
   PgWalk w;
-  bool more = false;
+  PgWalk::Found start;
   if (a.N <= PG_WARP_SEQS) {
-    if (role == 3) more = w.start_warp(a);
+    if (role == 3) start = w.find_warp(a);
   } else {
     int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
     pg_scan(a, prefix, scratch);
-    if (role == 3) more = w.start(a, prefix);
+    if (role == 3) start = w.find(a, prefix);
     tc::fence_proxy_async_smem();
     __syncthreads();
   }
@@ -518,6 +518,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
     if (role == 3) {
       // ------------------------------------------------------------ walk, and queries
       uint32_t n[NT] = {};  // query loads
+      bool more = w.enter(a, start);
       const uint32_t bytes = C::SLABS * tb1 * a.g * 128;
       for (bool ok = true; ok;) {
         ok = ctl.wait(&i_empty[ni % TA_ITEMS], (ni / TA_ITEMS & 1) ^ 1);
