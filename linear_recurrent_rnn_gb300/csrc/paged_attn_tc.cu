@@ -614,13 +614,15 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
           // step j: the products P V of key tile j - 1 and Q K^T of key tile j (in the order in
           // which the loader fills the ring)
           for (int j = j0; j <= j1 && ok && j0 < j1; ++j) {
-            uint32_t v_st[C::UPT], k_st[C::UPT];
+            uint32_t v_st[C::UPT], k_st[C::UPT], v_par[C::UPT], k_par[C::UPT];
             bool v_in = false, k_in = false;
-            auto take = [&](uint32_t (&at)[C::UPT]) {
+            // (NT = 1: the units' arrival is waited for where they are used, one by one)
+            auto take = [&](uint32_t (&at)[C::UPT], uint32_t (&par)[C::UPT]) {
 #pragma unroll
               for (int u = 0; u < C::UPT; ++u) {
                 at[u] = st;
-                ok = ok && ctl.wait1(&full[st], ph);
+                par[u] = ph;
+                if (NT == 2) ok = ok && ctl.wait1(&full[st], ph);
                 if (++st == C::STAGES) {
                   st = 0;
                   ph ^= 1;
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
             };
             auto take_v = [&] {
               if (v_in) return;
-              take(v_st);
+              take(v_st, v_par);
               v_in = true;
               if (ta_cut(j - 1, k_lo, k_hi)) {
                 ok = ok && ctl.wait1(&v_clean[nc % TA_CLEARS], nc / TA_CLEARS & 1);
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
               }
             };
             auto take_k = [&] {
-              if (!k_in) take(k_st);
+              if (!k_in) take(k_st, k_par);
               k_in = true;
             };
             auto qk = [&](int t) {
@@ -648,11 +650,18 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
               ++cs[t];
               tc::tc_fence_after();
 #pragma unroll
-              for (int k = 0; k < DP / 16; ++k)
+              for (int k = 0; k < DP / 16; ++k) {
+                if (NT == 1 && k % 8 == 0) {
+                  ok = ctl.wait1(&full[k_st[k / 8]], k_par[k / 8]);
+                  if (!ok) return;
+                  tc::tc_fence_after();
+                }
                 tc::mma_bf16(tmem + C::S_COL + b * 128,
                              d_q + (((t * C::SLABS + k / 4) * TA_SLAB + k % 4 * 32) >> 4),
                              d_k + (k_st[k / 8] * (C::UB >> 4) + ((k % 8 / 4 * TA_SLAB + k % 4 * 32) >> 4)),
                              id_qk, k > 0);
+                if (NT == 1 && k % 8 == 7) tc::mma_commit(&empty[k_st[k / 8]]);  // a unit is free once read
+              }
               tc::mma_commit(&s_full[b]);
               if (j == tl[t].jb - 1) tc::mma_commit(&q_empty[t]);
             };
@@ -666,10 +675,17 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
               tc::tc_fence_after();
               const uint32_t more = j - 1 > tl[t].ja;
 #pragma unroll
-              for (int k = 0; k < TA_BN / 16; ++k)
+              for (int k = 0; k < TA_BN / 16; ++k) {
+                if (NT == 1 && k * 16 % C::VROWS == 0) {
+                  ok = ctl.wait1(&full[v_st[k * 16 / C::VROWS]], v_par[k * 16 / C::VROWS]);
+                  if (!ok) return;
+                  tc::tc_fence_after();
+                }
                 ta_mma_ts(tmem + C::O_COL + t * DP, tmem + C::S_COL + b * 128 + k * 8,
                           d_v + (v_st[k * 16 / C::VROWS] * (C::UB >> 4) + (k * 16 % C::VROWS * 128 >> 4)), id_pv,
                           k > 0 ? 1u : more);
+                if (NT == 1 && (k + 1) * 16 % C::VROWS == 0) tc::mma_commit(&empty[v_st[k * 16 / C::VROWS]]);
+              }
               tc::mma_commit(&pv_done[t]);
             };
             if (NT == 1) {
@@ -679,17 +695,18 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
                 if (ok && j > tl[t].ja && j <= tl[t].jb) pv(t);
+                if (ok && t == NT - 1 && v_in) tc::mma_commit(&empty[v_st[0]]);  // the values' last use
                 if (ok && j >= tl[t].ja && j < tl[t].jb) qk(t);
               }
             }
-            // what no tile used is passed over, so that the ring stays in step
-            if (ok && j > j0) take_v();
-            if (ok && j < j1) take_k();
-            if (!ok) break;
-#pragma unroll
-            for (int u = 0; u < C::UPT; ++u) {
-              if (v_in) tc::mma_commit(&empty[v_st[u]]);
-              if (k_in) tc::mma_commit(&empty[k_st[u]]);
+            // two row tiles: what neither used is passed over, so that the ring stays in step
+            if (NT == 2 && ok && j > j0 && !v_in) {
+              take_v();
+              if (ok) tc::mma_commit(&empty[v_st[0]]);
+            }
+            if (NT == 2 && ok && j < j1) {
+              take_k();
+              if (ok) tc::mma_commit(&empty[k_st[0]]);
             }
           }
         }
