@@ -504,11 +504,12 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
         uint32_t step, item;
         bool first, cut;
       } pv = {};
-      auto take = [&](uint32_t (&at)[C::UPT]) {
+      // (a unit's arrival is waited for where it is used)
+      auto take = [&](uint32_t (&at)[C::UPT], uint32_t (&arr)[C::UPT]) {
 #pragma unroll
         for (int u = 0; u < C::UPT; ++u) {
           at[u] = st;
-          ok = ok && ctl.wait1(&full[st], par);
+          arr[u] = par;
           if (++st == C::STAGES) {
             st = 0;
             par ^= 1;
@@ -516,8 +517,8 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
         }
       };
       auto product = [&] {  // O^T += V^T P^T of the step before
-        uint32_t at[C::UPT];
-        take(at);
+        uint32_t at[C::UPT], arr[C::UPT];
+        take(at, arr);
         if (pv.cut) {
           ok = ok && ctl.wait1(&v_clean[nc % TA_CLEARS], nc / TA_CLEARS & 1);
           ++nc;
@@ -528,16 +529,21 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
         if (!ok) return;
         tc::tc_fence_after();
 #pragma unroll
-        for (int hm = 0; hm < C::MH; ++hm)
+        for (int k = 0; k < TA_BN / 16; ++k) {
+          if (k * 16 % C::VROWS == 0) {
+            ok = ctl.wait1(&full[at[k * 16 / C::VROWS]], arr[k * 16 / C::VROWS]);
+            if (!ok) return;
+            tc::tc_fence_after();
+          }
 #pragma unroll
-          for (int k = 0; k < TA_BN / 16; ++k)
+          for (int hm = 0; hm < C::MH; ++hm)
             tc::mma_bf16(tmem + C::O_COL + (ob * C::MH + hm) * NR,
                          d_v + (at[k * 16 / C::VROWS] * (C::UB >> 4) +
                                 ((2 * hm * C::VSLAB + k * 16 % C::VROWS * 128) >> 4)),
                          d_p + ((b * C::PB + k * 16 * C::PROW) >> 4), id_o, k > 0 ? 1u : (uint32_t)!pv.first);
+          if ((k + 1) * 16 % C::VROWS == 0) tc::mma_commit(&empty[at[k * 16 / C::VROWS]]);
+        }
         tc::mma_commit(&pv_done[b]);
-#pragma unroll
-        for (int u = 0; u < C::UPT; ++u) tc::mma_commit(&empty[at[u]]);
       };
       for (uint32_t ni = 0; ok; ++ni) {
         ok = ctl.wait1(&i_full[ni % TA_ITEMS], ni / TA_ITEMS & 1);
@@ -548,21 +554,27 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
         tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
         const uint32_t qb = nq % C::QBUF;
         for (int j = j0; j < j1 && ok; ++j, ++step) {
-          uint32_t at[C::UPT];
-          take(at);
+          uint32_t at[C::UPT], arr[C::UPT];
+          take(at, arr);
           if (j == j0) ok = ok && ctl.wait1(&q_full[qb], nq / C::QBUF & 1);
           if (!ok) break;
           tc::tc_fence_after();
           const uint32_t b = step & 1;
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k)
+          for (int k = 0; k < DP / 16; ++k) {
+            if (k % 8 == 0) {
+              ok = ctl.wait1(&full[at[k / 8]], arr[k / 8]);
+              if (!ok) break;
+              tc::tc_fence_after();
+            }
             tc::mma_bf16(tmem + C::S_COL + b * NR,
                          d_k + (at[k / 8] * (C::UB >> 4) + ((k % 8 / 4 * TA_SLAB + k % 4 * 32) >> 4)),
                          d_q + ((qb * C::QB + k / 4 * C::QSLAB + k % 4 * 32) >> 4), id_s, k > 0);
+            if (k % 8 == 7 || k == DP / 16 - 1) tc::mma_commit(&empty[at[k / 8]]);
+          }
+          if (!ok) break;
           tc::mma_commit(&s_full[b]);
           if (j == j1 - 1) tc::mma_commit(&q_empty[qb]);
-#pragma unroll
-          for (int u = 0; u < C::UPT; ++u) tc::mma_commit(&empty[at[u]]);
           if (pend) product();
           pend = true;
           pv.step = step;
