@@ -19,7 +19,8 @@ namespace {
 // all have read before one writes, so they are then one cluster, which meets in between.
 // Tokens: a warp takes 32 in a row and searches the offsets for the first; the others are mostly
 // in the same request.  Latency-bound: the floor is a launch, two dependent reads (lengths, then
-// table or ring) and the writes.
+// table or ring) and the writes.  Measured (GB300): 4.0 us for 8 requests, 5.0 for 512, 7.2 for 1024
+// requests with 130 000 new tokens.
 struct PlanArgs {
   int N, T, P, s, s_log2, width;
   const int32_t* cached;
@@ -165,7 +166,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
 // ---------------------------------------------------------------- write
 // A copy whose destination rows are chosen by the slots: a warp takes a token, its lanes the
 // 16-byte pieces of the token's keys and then its values, so that a warp has all of a token's
-// loads in flight at once.  Bound by memory bandwidth (and by latency for few tokens).
+// loads in flight at once (as many as its registers hold: stores may not be passed by later loads).
+// Bound by memory bandwidth (and by latency for few tokens).  Measured (GB300): 16384 tokens of 8
+// heads of 128, slices of a fused projection: 22.0 us, 6.1 TB/s read and written (one piece at a
+// time: 23.9); 64 tokens: 2.0 us.
 struct WriteArgs {
   int T, pieces, head_pieces, s_log2;  // 16-byte pieces of a token's keys, of one head
   int64_t slots_end;                   // num_pages * page_size

@@ -17,6 +17,12 @@
 // entries are looked up one tile ahead): values land behind the scores, the next keys behind P V.
 // Keys that no row of the item sees are not read, their rows are zero.  Work is divided over CTAs
 // by weight (paged.cuh).
+//
+// Measured (GB300): 64 requests of 500 to 4096 keys, 16 query heads on 4 of 128 (452 MB): 120 us,
+// 3.8 TB/s: the float32 pipe does 8 rows where 4 are there.  Two chunks of 1024 tokens over 2048
+// keys, the same heads: 651 us, 40 TFLOP/s of 74: shared-memory reads and the two barriers a tile
+// with 8 warps an SM (row tiles of 128 and 16 warps: 590 us here, but slower for short calls, as
+// 128 registers a thread spill).
 #include <algorithm>
 
 #include "host_util.h"

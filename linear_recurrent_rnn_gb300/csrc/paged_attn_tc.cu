@@ -1,22 +1,22 @@
-// Attention over the paged cache on the tensor cores (bf16 I/O): tcgen05 MMAs with accumulators
-// and softmax weights in TMEM, operands by TMA.
+// Attention over the paged cache on the tensor cores (bf16 I/O), many rows a request: tcgen05
+// MMAs with accumulators and softmax weights in TMEM, operands by TMA.
 //
 // One pass over the keys with a running maximum and sum.  Per row tile (up to 128 rows: whole
 // tokens x the g query heads of one key/value head) and per tile of 128 keys
 //   S = Q K^T               Q, K from shared memory, S in TMEM, float32
 //   P = 2^(c S - c m)       c = scale log2 e; one thread a row, P back to TMEM as bf16
 //   O += P V                P from TMEM, V from shared memory, O in TMEM, float32
-// with l the float32 sum of P before its rounding to bf16.  The rounding of P (relative 2^-9
-// each, as V's own storage) is what lets the second product run on the tensor cores; sums and
-// statistics stay in float32.  m is moved only when a row's maximum has grown by more than 2^8
-// in weight (O and l are then scaled): weights up to 2^8 keep bf16's relative precision, and the
-// rescaling of O, a round trip through TMEM, becomes rare.
+// with l the float32 sum of P before its rounding to bf16.  The rounding of P (8-bit significand,
+// relative 2^-8 at most, as V's own storage) is what lets the second product run on the tensor
+// cores; sums and statistics stay in float32.  m is moved only when a row's maximum has grown by
+// more than 2^8 in weight (O and l are then scaled): weights up to 2^8 keep bf16's relative
+// precision, and the rescaling of O, a round trip through TMEM, becomes rare.
 //
 // Width D <= 128: two row tiles a CTA share every key tile and alternate on the tensor cores, so
 // that one's softmax runs behind the other's products (TMEM: two S/P of 128 columns, two O of
-// D).  D <= 256: one row tile, two S buffers, the next tile's S computed behind this one's
-// softmax.  Warps: 4 softmax warps a row tile, then key/value loader, MMA
-// issuer, query loader, and one that walks the CTA's items.
+// D: full).  D <= 256: one row tile, two S buffers, the next tile's S computed behind this one's
+// softmax.  Warps: 4 softmax warps a row tile, then key/value loader, MMA issuer (one thread), one
+// that clears rows of V, and one that walks the CTA's items and loads queries.
 //
 // Pages: a key tile is copied page by page, one box of rows per page and 64 columns (128-byte
 // swizzle).  A page that the tile does not need, or whose table entry is outside the cache,
@@ -27,6 +27,15 @@
 //
 // Work is divided over the CTAs by weight (paged.cuh): one CTA per SM, each with a list of
 // items of which the first and the last may be shared with its neighbours.
+//
+// Measured (GB300): two prompts of 8192 tokens, 16 query heads on 4 of 128, 550 GFLOP: 390 us,
+// 1.41 PFLOP/s (the tensor pipe 59 % of its cycles).  What bounds it: a 128 x 128 x 16 product
+// takes the pipe 64 cycles, and Q K^T, both operands from shared memory, takes shared memory's
+// whole 128 bytes a cycle meanwhile, so the key tiles' arrival delays it; a tile's softmax (1200
+// cycles) and the latencies of its hand-overs are a little longer than the other tile's products
+// (1024).  Without any softmax the same call takes 334 us.  Heads of 256 (S two tiles ahead):
+// 1.50 PFLOP/s.  Heads of 64: 0.87 PFLOP/s, bound by the softmax (154 us of 235 without it).  Not
+// faster: weights handed over in halves, and taken at the last maximum beside the new one.
 #include <algorithm>
 
 #include "host_util.h"
