@@ -244,7 +244,10 @@ rglru_status check_queries(const paged_shape* s) {
 }
 
 // Rows (tokens x query heads of a key/value head) of a request in the mean, rounded up to whole
-// tokens: what the host knows of the lengths.  Either kernel is right for any lengths.
+// tokens: what the host knows of the lengths.  Every kernel is right for any lengths; the mean
+// chooses among them.  bf16, 64 requests of 500 to 4096 keys, 32 heads on 8 of 128, few-rows kernel
+// (tiles of 16 or 32 rows) against 128-row tiles: 4 rows a request 85 : 99 us, 16 rows 87 : 100,
+// 20 rows 92 : 100, 32 rows 100 : 100, 40 rows (two tiles, keys read twice) 174 : 101.
 int mean_rows(const paged_shape* s) {
   return (int)std::min<int64_t>(((int64_t)s->tokens + s->num_seqs - 1) / s->num_seqs * (s->Hq / s->Hkv), 1 << 30);
 }

@@ -10,9 +10,9 @@
 // maxima, sums and the exchange of P stay within 16 lanes, and only the key and value tiles
 // are shared by the CTA.  With many rows (BM = 64) all warps work on one tile of keys and the
 // kernel is bound by the float32 pipe; two products an instruction (fma.f32x2) and 4 x 4 (S) or
-// 4 x DP / 16 (O) outputs a thread keep shared memory below it.  With few (BM = 16: decode) it is
-// bound by memory, and four pairs of warps take a quarter of the tile's keys each, with maxima
-// and sums of their own that are joined when the item ends.
+// 4 x DP / 16 (O) outputs a thread keep shared memory below it.  With few (BM = 32, 16, 8:
+// drafts, decode) it is bound by memory, and groups of BM / 8 warps take a part of the tile's keys
+// each, with maxima and sums of their own that are joined when the item ends.
 // Tiles are gathered by 16-byte asynchronous copies, row by row through the block table (whose
 // entries are looked up one tile ahead): values land behind the scores, the next keys behind P V.
 // Keys that no row of the item sees are not read, their rows are zero.  Work is divided over CTAs
@@ -39,7 +39,8 @@ template <int BM, int DP>
 struct Sa {
   static constexpr int SPLIT = 64 / BM;  // key ranges of a tile
   // keys of a range: 64, or what lets a tile of all ranges fit
-  static constexpr int BN = SPLIT == 1 ? 64 : SPLIT == 4 ? (DP == 64 ? 64 : 4096 / DP) : 2048 / DP;
+  static constexpr int BN = SPLIT == 1 ? 64 : SPLIT == 2 ? (DP == 256 ? 32 : 64)
+                            : SPLIT == 4 ? (DP == 64 ? 64 : 4096 / DP) : 2048 / DP;
   static constexpr int TILE = SPLIT * BN;
   static constexpr int KS = BN / 16;     // keys a thread
   static constexpr int C4 = DP / 64;     // times four columns of O a thread
@@ -419,14 +420,16 @@ cudaError_t run_d(PagedArgs& a, cudaStream_t s, int sms) {
 cudaError_t launch_paged_attn_simt(PagedArgs a, int rows, cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorNotSupported;
-  // (rows of 256 columns leave room for ranges of 16 rows only)
+  // The row tile is the least that holds the mean's rows.  64 requests of 500 to 4096 keys, 16 heads
+  // on 4 of 128: 4 rows in tiles of 8, 16, 64: 121, 155, 379 us; 16 rows: 226 (twice), 156, 379;
+  // 20 rows: 333, 296, 223, 380 in tiles of 8, 16, 32, 64.  (Eight ranges of 256 columns do not fit.)
   if (rows <= 8 && a.D <= 128) return a.D <= 64 ? run<8, 64>(a, s, sms) : run<8, 128>(a, s, sms);
-  return rows <= 16 ? run_d<16>(a, s, sms) : run_d<64>(a, s, sms);
+  return rows <= 16 ? run_d<16>(a, s, sms) : rows <= 32 ? run_d<32>(a, s, sms) : run_d<64>(a, s, sms);
 }
 
 size_t paged_attn_simt_ws_bytes(const paged_shape* s, int rows) {
   const int sms = sm_count();
-  return paged_ws(std::min(2 * (sms > 0 ? sms : 256), PG_MAX_CTAS), rows <= 16 ? 16 : 64,
+  return paged_ws(std::min(2 * (sms > 0 ? sms : 256), PG_MAX_CTAS), rows <= 16 ? 16 : rows <= 32 ? 32 : 64,
                   s->D <= 64 ? 64 : s->D <= 128 ? 128 : 256).total;
 }
 
