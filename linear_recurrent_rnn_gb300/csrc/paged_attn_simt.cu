@@ -18,8 +18,8 @@
 // Keys that no row of the item sees are not read, their rows are zero.  Work is divided over CTAs
 // by weight (paged.cuh).
 //
-// Measured (GB300): 64 requests of 500 to 4096 keys, 16 query heads on 4 of 128 (452 MB): 120 us,
-// 3.8 TB/s: the float32 pipe does 8 rows where 4 are there.  Two chunks of 1024 tokens over 2048
+// Measured (GB300): 64 requests of 500 to 4096 keys, 16 query heads on 4 of 128 (452 MB): 112 us,
+// 4.0 TB/s: eight warps an SM do not cover the latencies of a tile's phases.  Two chunks of 1024 tokens over 2048
 // keys, the same heads: 651 us, 40 TFLOP/s of 74: shared-memory reads and the two barriers a tile
 // with 8 warps an SM (row tiles of 128 and 16 warps: 590 us here, but slower for short calls, as
 // 128 registers a thread spill).
@@ -33,21 +33,20 @@ namespace rglru {
 
 namespace {
 
-constexpr int SA_THREADS = 256;
-
 template <int BM, int DP>
 struct Sa {
-  static constexpr int SPLIT = 64 / BM;  // key ranges of a tile
+  static constexpr int THREADS = BM == 8 ? 128 : 256;
+  static constexpr int SPLIT = THREADS / 4 / BM;  // key ranges of a tile
   // keys of a range: 64, or what lets a tile of all ranges fit
   static constexpr int BN = SPLIT == 1 ? 64 : SPLIT == 2 ? (DP == 256 ? 32 : 64)
-                            : SPLIT == 4 ? (DP == 64 ? 64 : 4096 / DP) : 2048 / DP;
+                            : BM == 16 ? (DP == 64 ? 64 : 4096 / DP) : 2048 / DP;
   static constexpr int TILE = SPLIT * BN;
   static constexpr int KS = BN / 16;     // keys a thread
   static constexpr int C4 = DP / 64;     // times four columns of O a thread
   static constexpr int LD = DP + 4;      // row stride: 16-byte reads of 8 rows meet all banks
-  static constexpr int CTAS = BM == 64 && DP == 64 ? 2 : 1;  // per SM
+  static constexpr int CTAS = (BM == 64 && DP == 64) || BM == 8 ? 2 : 1;  // per SM
   // shared memory, in floats: queries, keys, values, P^T of each warp; then row offsets
-  static constexpr int Q = 0, K = Q + BM * LD, V = K + TILE * LD, P = V + TILE * LD, OFF = P + 8 * BN * 8;
+  static constexpr int Q = 0, K = Q + BM * LD, V = K + TILE * LD, P = V + TILE * LD, OFF = P + THREADS / 32 * BN * 8;
   static constexpr size_t smem = (size_t)OFF * 4 + (size_t)4 * TILE * 8;
 };
 
@@ -68,7 +67,7 @@ __device__ __forceinline__ float2 sa_fma2(float2 a, float2 b, float2 c) {
 }
 
 template <int BM, int DP>
-__global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_simt(const PagedArgs a) {
+__global__ void __launch_bounds__(Sa<BM, DP>::THREADS, Sa<BM, DP>::CTAS) k_paged_attn_simt(const PagedArgs a) {
   using C = Sa<BM, DP>;
   extern __shared__ __align__(16) float sa_sm[];
   float* s_q = sa_sm + C::Q;
@@ -128,7 +127,7 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
       float* dst = kv ? s_v : s_k;
       const float* src = static_cast<const float*>(kv ? a.vc : a.kc) + it.h * (kv ? a.vc_head : a.kc_head);
 #pragma unroll 4
-      for (int i = tid; i < C::TILE * (DP / 4); i += SA_THREADS) {
+      for (int i = tid; i < C::TILE * (DP / 4); i += C::THREADS) {
         const int r = i / (DP / 4), c = i % (DP / 4) * 4;
         const int64_t o = off[r];
         const bool read = o >= 0 && c < a.D;
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
     };
 
     look_up(j0);
-    for (int i = tid; i < BM * (DP / 4); i += SA_THREADS) {
+    for (int i = tid; i < BM * (DP / 4); i += C::THREADS) {
       const int r = i / (DP / 4), c = i % (DP / 4) * 4, t = pg_token(a, r);
       const bool read = r < rows && c < a.D;
       const float* src = static_cast<const float*>(a.q);
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
       *reinterpret_cast<float4*>(static_cast<float*>(a.o) + (int64_t)(it.r.first + t0 + t) * a.o_token +
                                  (int64_t)(it.h * a.g + r - t * a.g) * a.o_head + c) = x;
     };
-    for (int i = tid; i < rows * (DP / 4); i += SA_THREADS) {
+    for (int i = tid; i < rows * (DP / 4); i += C::THREADS) {
       const int r = i / (DP / 4), c = i % (DP / 4) * 4;
       if (c >= a.D) continue;
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
         // the item's last CTA joins its parts, up to PARTS at a time: their weights, then the sums
         __threadfence();
         float2* wt = reinterpret_cast<float2*>(s_k);  // [part][row]
-        constexpr int PARTS = C::TILE * C::LD / (BM * 2), RP = SA_THREADS * 4 / DP, PASSES = (BM + RP - 1) / RP;
+        constexpr int PARTS = C::TILE * C::LD / (BM * 2), RP = C::THREADS * 4 / DP, PASSES = (BM + RP - 1) / RP;
         constexpr int BATCH = PASSES >= 16 ? 1 : 16 / PASSES;  // parts loaded at once
         const int c = tid % (DP / 4) * 4, rr = tid / (DP / 4);
         float4 o[PASSES];
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
         float top = -INFINITY, sum = 0.0f;  // of row tid
         for (int q0 = c0; q0 <= c1; q0 += PARTS) {
           const int nq = min(PARTS, c1 - q0 + 1);
-          for (int i = tid; i < nq * BM; i += SA_THREADS)
+          for (int i = tid; i < nq * BM; i += C::THREADS)
             wt[i] = i % BM < rows ? __ldcg(g_ml + (size_t)PgWalk::slot(q0 + i / BM, c0) * BM + i % BM)
                                   : make_float2(0.0f, 0.0f);
           __syncthreads();
@@ -392,6 +391,7 @@ __global__ void __launch_bounds__(SA_THREADS, Sa<BM, DP>::CTAS) k_paged_attn_sim
 template <int BM, int DP>
 cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   using C = Sa<BM, DP>;
+  static_assert(C::TILE <= C::THREADS, "a thread looks one row up");
   static_assert(C::SPLIT * BM * DP <= C::TILE * C::LD, "the parts of the key ranges fit the key tile");
   const size_t smem = std::max(C::smem, (size_t)(a.N + 1) * 8);
   const void* f = reinterpret_cast<const void*>(k_paged_attn_simt<BM, DP>);
@@ -405,7 +405,7 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   a.tb = BM / a.g;
   pg_division(a, ctas, 128, 128, 128);
   void* args[] = {&a};
-  return launch_pdl(f, dim3(ctas), dim3(SA_THREADS), smem, s, args, 1);
+  return launch_pdl(f, dim3(ctas), dim3(C::THREADS), smem, s, args, 1);
 }
 
 template <int BM>
@@ -421,7 +421,7 @@ cudaError_t launch_paged_attn_simt(PagedArgs a, int rows, cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorNotSupported;
   // The row tile is the least that holds the mean's rows.  64 requests of 500 to 4096 keys, 16 heads
-  // on 4 of 128: 4 rows in tiles of 8, 16, 64: 121, 155, 379 us; 16 rows: 226 (twice), 156, 379;
+  // on 4 of 128: 4 rows in tiles of 8, 16, 64: 112, 155, 379 us; 16 rows: 226 (twice), 156, 379;
   // 20 rows: 333, 296, 223, 380 in tiles of 8, 16, 32, 64.  (Eight ranges of 256 columns do not fit.)
   if (rows <= 8 && a.D <= 128) return a.D <= 64 ? run<8, 64>(a, s, sms) : run<8, 128>(a, s, sms);
   return rows <= 16 ? run_d<16>(a, s, sms) : rows <= 32 ? run_d<32>(a, s, sms) : run_d<64>(a, s, sms);
