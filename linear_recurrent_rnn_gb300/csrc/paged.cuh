@@ -213,7 +213,8 @@ struct PgWalk {
   __device__ __forceinline__ bool range(const PagedArgs& a, int64_t U) {
     cta = blockIdx.x;
     // U / grid, rounded up: grid_inv is 2^64 / grid, rounded up (exact for U grid < 2^64)
-    W = max((int64_t)__umul64hi((uint64_t)U + gridDim.x - 1, a.grid_inv), (int64_t)a.min_weight);
+    W = gridDim.x == 1 ? U : (int64_t)__umul64hi((uint64_t)U + gridDim.x - 1, a.grid_inv);
+    W = max(W, (int64_t)a.min_weight);
     snap = (int)min((int64_t)a.snap, W >> 2);
     w0 = W * cta;
     w1 = min(w0 + W, U);

@@ -123,7 +123,7 @@ __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int t
   float l = 0.0f;
   for (int c = c0; c <= c1; ++c) {
     const float2 x = __ldcg(ml + (size_t)PgWalk::slot(c, c0) * R + row);
-    if (x.y != 0.0f) l += x.y * ta_ex2(x.x - m);
+    if (x.y != 0.0f) l = fmaf(x.y, ta_ex2(x.x - m), l);
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int t = row >> 7, r = row & 127;
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
                                     fmaxf(mx[2], mx[3]));
           if (j == tl.ja) {
             m = top;
-          } else if (__any_sync(0xffffffffu, (top - m) * sc > 8.0f)) {
+          } else if (__any_sync(0xffffffffu, r < tl.rows && (top - m) * sc > 8.0f)) {  // (of rows in use)
             const float f = top == m ? 1.0f : ta_ex2((top - m) * -sc);
             l *= f;
             m = top;
@@ -399,7 +399,8 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
       constexpr int R = NT * 128;
       const float2* g_ml = reinterpret_cast<const float2*>(a.ws + a.part_ml);
       const float* g_o = reinterpret_cast<const float*>(a.ws + a.part_o);
-      const float2 own = make_float2(m == -INFINITY ? m : m * sc, l);
+      // (rounded here as in memory, whichever of the two it is joined from)
+      const float2 own = make_float2(m == -INFINITY ? m : __fmul_rn(m, sc), l);
       if (here) {
         if (live) {
           const int64_t tok = it.first + tl.tok + my_tok;
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
               if (part(q).y != 0.0f) top = fmaxf(top, part(q).x);
             sum = 0.0f;
             for (int q = it.c0; q <= it.c1; ++q)
-              if (part(q).y != 0.0f) sum += part(q).y * ta_ex2(part(q).x - top);
+              if (part(q).y != 0.0f) sum = fmaf(part(q).y, ta_ex2(part(q).x - top), sum);
           }
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll 1

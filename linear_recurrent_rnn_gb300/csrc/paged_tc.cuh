@@ -24,6 +24,11 @@ struct TaAbort {
     if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, ok || slow(bar, parity));
     return ok;
   }
+  // The same for what may not come for most of a long call.
+  __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity) const {
+    const TaAbort longer{flag, status, 100 * limit_ns};
+    return longer.wait(bar, parity);
+  }
   // By one thread.
   __device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity) const {
     return tc::mbar_try_wait(bar, parity) || slow(bar, parity);
@@ -74,7 +79,7 @@ __device__ __forceinline__ void ta_clear_rows(const TaAbort& ctl, const TaClear*
   constexpr int PIECES = C::SLABS * 8;  // 16-byte pieces of a row
   const int lane = threadIdx.x & 31;
   const int piece = lane % PIECES, sub = lane / PIECES;
-  for (uint32_t n = 0; ctl.wait(&come[n % TA_CLEARS], n / TA_CLEARS & 1); ++n) {
+  for (uint32_t n = 0; ctl.wait_long(&come[n % TA_CLEARS], n / TA_CLEARS & 1); ++n) {
     const TaClear x = rec[n % TA_CLEARS];
     if (x.p0 < 0) break;
 #pragma unroll

@@ -108,3 +108,16 @@ def test_calls_launch_one_kernel_each():
     before = R.rglru_kernel_launches()
     attend(x, 0.1)
     assert R.rglru_kernel_launches() == before + 1
+
+
+def test_split_items_repeat_bitwise():
+    """Items shared by two CTAs, either of which may finish last and join them, and row tiles with
+    rows to spare (10 heads of one: 120 of 128): twenty runs give the same bits, whatever other
+    calls left in the SMs' memory between them."""
+    x = build([(1, 150), (173, 174), (173, 173), (1, 141), (173, 300)] * 6, 20, 2, 96, 16, "bf16", 9)
+    other = build([(60, 190), (128, 1000)] * 20, 4, 4, 128, 16, "bf16", 10, k_scale=40.0)
+    o, L, ws = attend(x, 96 ** -0.5)
+    for _ in range(20):
+        attend(other, 1.0)
+        o2, L2, _ = attend(x, 96 ** -0.5, ws=ws)
+        assert torch.equal(o, o2) and torch.equal(L, L2)
