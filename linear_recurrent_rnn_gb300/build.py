@@ -1,8 +1,10 @@
-"""Builds librglru.so in-tree with nvcc for sm_103a (GB300).
+"""Builds librglru.so in-tree with nvcc for sm_103a (GB300), and the Python module beside it.
 
 Each translation unit is compiled in parallel; the CUDA runtime is linked statically and the
 driver API is reached at run time through cudaGetDriverEntryPoint, so the library loads on a
-machine without a GPU (where only its symbols can be inspected).
+machine without a GPU (where only its symbols can be inspected).  The module (csrc/binding.cpp:
+checks of tensors and the calls of the paged cache) is compiled against the installed torch and
+Python; it does not link the library.
 """
 from __future__ import annotations
 
@@ -10,12 +12,14 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "librglru.so")
+BINDING = os.path.join(BUILD, "rglru_binding.so")
 SOURCES = ["api.cu", "scan_simt.cu", "gemm_simt.cu", "noalloc.cu", "host_util.cu", "fused_fwd.cu", "fused_bwd.cu",
            "decode.cu", "varlen.cu", "delta_rule.cu", "proj_tc.cu", "paged.cu", "paged_attn_simt.cu",
            "paged_attn_tc.cu", "paged_attn_few.cu"]
@@ -36,19 +40,21 @@ def _deps():
     files.append(os.path.join(ROOT, "include", "librglru.h"))
     files.append(os.path.join(ROOT, "include", "delta_rule.h"))
     files.append(os.path.join(ROOT, "include", "paged_attn.h"))
+    files.append(os.path.join(CSRC, "binding.cpp"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every kernel translation unit and link librglru.so; returns its path."""
+    """Compile every kernel translation unit and link librglru.so, compile the Python module;
+    returns the library's path."""
     if not force and not stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -66,8 +72,22 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    def compile_binding():
+        import torch
+        root = os.path.dirname(torch.__file__)
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = [nvcc, "-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-shared", os.path.join(CSRC, "binding.cpp"),
+               "-o", tmp, "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
+               "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING)
+
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        module = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        module.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -2,14 +2,17 @@
 include/paged_attn.h).
 
 Argument marshalling only: every function here checks that its tensors are contiguous CUDA
-tensors (the paged-cache calls also take strided ones, and check types and shapes), passes their
-device pointers and the current CUDA stream to the C ABI call of the same name, and raises
-``RglruError`` on a non-OK status.  No arithmetic runs in Python and there is no fallback: if
-the shared library is missing, the first call raises.
+tensors, passes their device pointers and the current CUDA stream to the C ABI call of the same
+name, and raises ``RglruError`` on a non-OK status.  The paged-cache calls also take strided
+tensors and check types, shapes and sizes (``ValueError``); they are short enough for that to be
+done in a module of its own (csrc/binding.cpp).  No arithmetic runs in Python and there is no
+fallback: if the shared library or the module is missing, the first call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import Optional
@@ -63,6 +66,7 @@ class PagedStrides(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_calls = None
 
 EXPORTS = ("rglru_status_string", "rglru_saved_bytes", "rglru_workspace_bytes",
            "rglru_gate_proj", "rglru_forward", "rglru_backward", "rglru_gate_proj_backward",
@@ -200,14 +204,8 @@ def _p(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-# The current stream's handle without the Stream object around it (a tenth of its time).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream(stream):
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -378,48 +376,35 @@ def alloc_paged_workspace(shape: PagedShape, device="cuda") -> torch.Tensor:
                        device=device)
 
 
-def _arg(t, name, dtype, shape):
-    """The address of a contiguous CUDA tensor of this dtype and shape."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name}: want a contiguous CUDA tensor, {tuple(shape)} {dtype}, not "
-                     f"{tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
+def _paged_calls():
+    """The module that checks the paged calls' tensors and makes the calls (csrc/binding.cpp)."""
+    global _calls
+    L = lib()
+    with _lock:
+        if _calls is None:
+            if not os.path.exists(_build.BINDING):
+                raise RuntimeError(f"the Python module is not built ({_build.BINDING} missing); "
+                                   "call linear_recurrent_rnn_gb300.build.build() first")
+            loader = importlib.machinery.ExtensionFileLoader("rglru_binding", _build.BINDING)
+            m = importlib.util.module_from_spec(
+                importlib.util.spec_from_loader("rglru_binding", loader))
+            loader.exec_module(m)
+            m.setup(PagedShape, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                L.paged_plan, L.paged_kv_write, L.paged_attention,
+                L.paged_attention_workspace_bytes)))
+            _calls = m
+    return _calls
 
 
-def _view(t, name, dtype, shape):
-    """The address of a CUDA tensor of this dtype and shape whose last dimension is contiguous;
-    the others may have any stride."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.stride(-1) == 1:
-        return t.data_ptr()
-    raise ValueError(f"{name}: want a CUDA tensor with a contiguous last dimension, "
-                     f"{tuple(shape)} {dtype}, not {tuple(t.shape)} {t.dtype} on {t.device} "
-                     f"with strides {t.stride()}")
-
-
-def _row_steps(t, heads, width):
-    """Token and head strides of rows [tokens, heads, width], in elements (a dimension of one
-    element has the stride that a contiguous tensor would have)."""
-    s = t.stride()
-    return s[0] if t.shape[0] > 1 else heads * width, s[1] if heads > 1 else width
-
-
-def _cache_steps(t, heads, width):
-    """Page, token and head strides of a cache [pages, page_size, heads, width]."""
-    s, n = t.stride(), t.shape
-    return s[0] if n[0] > 1 else n[1] * heads * width, s[1], s[2] if heads > 1 else width
+def _handle(stream):
+    return None if stream is None else int(getattr(stream, "cuda_stream", stream))
 
 
 def paged_plan(shape, cached_lens, new_lens, free_pages, free_state, block_table, cu_seqlens,
                kv_lens, positions, slots, free_state_out, stream=None):
-    N, T, i32 = shape.num_seqs, shape.tokens, torch.int32
-    st = (_lib or lib()).paged_plan(
-        shape, _arg(cached_lens, "cached_lens", i32, (N,)), _arg(new_lens, "new_lens", i32, (N,)),
-        _arg(free_pages, "free_pages", i32, (shape.num_pages,)),
-        _arg(free_state, "free_state", i32, (3,)),
-        _arg(block_table, "block_table", i32, (N, shape.table_width)),
-        _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,)), _arg(kv_lens, "kv_lens", i32, (N,)),
-        _arg(positions, "positions", i32, (T,)), _arg(slots, "slots", torch.int64, (T,)),
-        _arg(free_state_out, "free_state_out", i32, (3,)), _stream(stream))
+    st = (_calls or _paged_calls()).paged_plan(
+        shape, cached_lens, new_lens, free_pages, free_state, block_table, cu_seqlens, kv_lens,
+        positions, slots, free_state_out, _handle(stream))
     if st:
         _check("paged_plan", st)
 
@@ -427,17 +412,8 @@ def paged_plan(shape, cached_lens, new_lens, free_pages, free_state, block_table
 def paged_kv_write(shape, k, v, slots, k_cache, v_cache, stream=None):
     """k, v [tokens, Hkv, D] and the caches [num_pages, page_size, Hkv, D] may be strided views
     (slices of a fused projection, a cache stored head by head)."""
-    dt, T, H, D = TORCH_DT[shape.io], shape.tokens, shape.Hkv, shape.D
-    rows, cache = (T, H, D), (shape.num_pages, shape.page_size, H, D)
-    strides = None
-    if not (k.is_contiguous() and v.is_contiguous() and k_cache.is_contiguous() and
-            v_cache.is_contiguous()):
-        strides = PagedStrides(0, 0, 0, 0, *_row_steps(k, H, D), *_row_steps(v, H, D),
-                               *_cache_steps(k_cache, H, D), *_cache_steps(v_cache, H, D))
-    st = (_lib or lib()).paged_kv_write(
-        shape, strides, _view(k, "k", dt, rows), _view(v, "v", dt, rows),
-        _arg(slots, "slots", torch.int64, (T,)), _view(k_cache, "k_cache", dt, cache),
-        _view(v_cache, "v_cache", dt, cache), _stream(stream))
+    st = (_calls or _paged_calls()).paged_kv_write(shape, k, v, slots, k_cache, v_cache,
+                                                   _handle(stream))
     if st:
         _check("paged_kv_write", st)
 
@@ -446,22 +422,8 @@ def paged_attention(shape, q, k_cache, v_cache, block_table, cu_seqlens, kv_lens
                     workspace, stream=None):
     """q, o [tokens, Hq, D] and the caches [num_pages, page_size, Hkv, D] may be strided views;
     lse float32 [tokens, Hq] or None; workspace from alloc_paged_workspace."""
-    dt, T, D, i32 = TORCH_DT[shape.io], shape.tokens, shape.D, torch.int32
-    N, Hq = shape.num_seqs, shape.Hq
-    rows, cache = (T, Hq, D), (shape.num_pages, shape.page_size, shape.Hkv, D)
-    strides = None
-    if not (q.is_contiguous() and o.is_contiguous() and k_cache.is_contiguous() and
-            v_cache.is_contiguous()):
-        strides = PagedStrides(*_row_steps(q, Hq, D), *_row_steps(o, Hq, D), 0, 0, 0, 0,
-                               *_cache_steps(k_cache, shape.Hkv, D),
-                               *_cache_steps(v_cache, shape.Hkv, D))
-    st = (_lib or lib()).paged_attention(
-        shape, strides, _view(q, "q", dt, rows), _view(k_cache, "k_cache", dt, cache),
-        _view(v_cache, "v_cache", dt, cache),
-        _arg(block_table, "block_table", i32, (N, shape.table_width)),
-        _arg(cu_seqlens, "cu_seqlens", i32, (N + 1,)), _arg(kv_lens, "kv_lens", i32, (N,)),
-        scale, _view(o, "o", dt, rows),
-        None if lse is None else _arg(lse, "lse", torch.float32, (T, Hq)), _p(workspace),
-        _stream(stream))
+    st = (_calls or _paged_calls()).paged_attention(
+        shape, q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, scale, o, lse, workspace,
+        _handle(stream))
     if st:
         _check("paged_attention", st)
