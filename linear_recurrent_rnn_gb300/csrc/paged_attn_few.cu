@@ -682,7 +682,7 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   a.part_o = L.o;
   a.rows = NR;
   // an item's switch costs about a key tile's time
-  pg_division(a, sms, 128, 128, 128);
+  pg_division(a, sms, 128, 192, 128);
   void* args[] = {&mq, &mk, &mv, &a};
   return launch_pdl(f, dim3(sms), dim3(TF_THREADS), C::smem, s, args, 1);
 }

@@ -765,7 +765,7 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   a.tb = C::NT * tb1;
   a.o_32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_token % 16 == 0 && a.o_head % 16 == 0 && a.D % 16 == 0;
   // the switch of an item costs two row tiles about 9000 cycles, three key tiles' time
-  pg_division(a, sms, C::NT == 2 ? 384 : 256, 256, C::NT == 2 ? 768 : 384);
+  pg_division(a, sms, C::NT == 2 ? 384 : 256, 896, C::NT == 2 ? 768 : 384);
   void* args[] = {&mq, &mk, &mv, &a};
   return launch_pdl(f, dim3(sms), dim3(C::THREADS), C::smem, s, args, 1);
 }
