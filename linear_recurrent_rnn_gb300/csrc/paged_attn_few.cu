@@ -42,13 +42,13 @@ constexpr int TF_SOFT = 128;
 constexpr int TF_THREADS = TF_SOFT + 128;
 constexpr size_t TF_SMEM_MAX = 232448 - 4096;  // 227 KB less the static part
 
-template <int DP, int NR>
+template <int DP, int NR, bool W>
 struct Tf {
+  static constexpr bool WIDE = W;                     // TaLay
   static constexpr int SLABS = DP / 64;
   static constexpr int UPT = DP == 256 ? 2 : 1;       // ring units of a key (or value) tile
   static constexpr uint32_t UB = DP == 64 ? TA_SLAB : 2 * TA_SLAB;
   static constexpr int VROWS = TA_BN / UPT;           // rows of V in a unit
-  static constexpr uint32_t VSLAB = VROWS * 128;
   static constexpr int MH = DP == 256 ? 2 : 1;        // products of 128 columns of V
   static constexpr uint32_t QSLAB = NR * 128;         // 64 columns of the rows of Q
   static constexpr uint32_t QB = SLABS * QSLAB;
@@ -106,11 +106,11 @@ __device__ __forceinline__ float tf_lse(float ref, float sum) {
   return sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
-template <int DP, int NR>
+template <int DP, int NR, bool W>
 __global__ void __launch_bounds__(TF_THREADS, 1)
     k_paged_attn_few(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
-  using C = Tf<DP, NR>;
+  using C = Tf<DP, NR, W>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* s_ring = smem;
@@ -500,10 +500,12 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
     if (tc::elect_one()) {
       constexpr uint32_t id_s = tc::idesc_bf16(128, NR, 0, 0);
       constexpr uint32_t id_o = tc::idesc_bf16(128, NR, 1, 1);
-      const uint64_t d_k = tc::smem_desc(tc::smem_u32(s_ring), 16, 1024, tc::LAYOUT_SW128);
+      const TaLay<C> lay(a);
+      const uint64_t d_k = tc::smem_desc(tc::smem_u32(s_ring), 16, TaLay<C>::K_GROUP, tc::LAYOUT_SW128);
       const uint64_t d_q = tc::smem_desc(tc::smem_u32(s_q), 16, 1024, tc::LAYOUT_SW128);
       // V^T: 64 columns a slab; D <= 64 has one, read twice for the 128 rows of the product
-      const uint64_t d_v = tc::smem_desc(tc::smem_u32(s_ring), DP == 64 ? 0 : C::VSLAB, 1024, tc::LAYOUT_SW128);
+      const uint64_t d_v = tc::smem_desc(tc::smem_u32(s_ring), DP == 64 ? 0 : lay.v_slab(), lay.v_group(), tc::LAYOUT_SW128);
+      const uint32_t v_slab = lay.v_slab() >> 4;
       const uint64_t d_p = tc::smem_desc(tc::smem_u32(s_p), 16, 8 * C::PROW, C::P_LAYOUT);
       uint32_t st = 0, par = 0;          // next ring unit, parity of its `full`
       uint32_t step = 0, nq = 0, nc = 0; // S^T begun; items with keys; value tiles cleared
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
           for (int hm = 0; hm < C::MH; ++hm)
             tc::mma_bf16(tmem + C::O_COL + (ob * C::MH + hm) * NR,
                          d_v + (at[k * 16 / C::VROWS] * (C::UB >> 4) +
-                                ((2 * hm * C::VSLAB + k * 16 % C::VROWS * 128) >> 4)),
+                                2 * hm * v_slab + (k % (C::VROWS / 16) * TaLay<C>::V_16 >> 4)),
                          d_p + ((b * C::PB + k * 16 * C::PROW) >> 4), id_o, k > 0 ? 1u : (uint32_t)!pv.first);
           if ((k + 1) * 16 % C::VROWS == 0) tc::mma_commit(&empty[at[k * 16 / C::VROWS]]);
         }
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
               tc::tc_fence_after();
             }
             tc::mma_bf16(tmem + C::S_COL + b * NR,
-                         d_k + (at[k / 8] * (C::UB >> 4) + ((k % 8 / 4 * TA_SLAB + k % 4 * 32) >> 4)),
+                         d_k + (at[k / 8] * (C::UB >> 4) + ((k % 8 / 4 * TaLay<C>::K_SLAB + k % 4 * 32) >> 4)),
                          d_q + ((qb * C::QB + k / 4 * C::QSLAB + k % 4 * 32) >> 4), id_s, k > 0);
             if (k % 8 == 7 || k == DP / 16 - 1) tc::mma_commit(&empty[at[k / 8]]);
           }
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
     }
   } else if (role == 2) {
     // ------------------------------------------------------------ rows of V that no row sees
-    ta_clear_rows<C>(ctl, s_clear, v_come, v_clean, full, s_ring);
+    ta_clear_rows<C>(a, ctl, s_clear, v_come, v_clean, full, s_ring);
   } else {
     // ------------------------------------------------------------ walk, and queries
     uint32_t n = 0;  // query loads
@@ -666,14 +668,14 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
   }
 }
 
-template <int DP, int NR>
+template <int DP, int NR, bool W>
 cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
-  using C = Tf<DP, NR>;
+  using C = Tf<DP, NR, W>;
   a.tb = NR / a.g;
   CUtensorMap mq, mk, mv;
-  cudaError_t e = ta_maps(a, a.tb, C::VROWS, &mq, &mk, &mv);
+  cudaError_t e = ta_maps<C>(a, a.tb, &mq, &mk, &mv);
   if (e != cudaSuccess) return e;
-  const void* f = reinterpret_cast<const void*>(k_paged_attn_few<DP, NR>);
+  const void* f = reinterpret_cast<const void*>(k_paged_attn_few<DP, NR, W>);
   static std::atomic<uint64_t> ready{0};
   e = ta_prepare(f, C::smem, 0, ready);
   if (e != cudaSuccess) return e;
@@ -687,9 +689,9 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   return launch_pdl(f, dim3(sms), dim3(TF_THREADS), C::smem, s, args, 1);
 }
 
-template <int DP>
+template <int DP, bool W>
 cudaError_t run_rows(PagedArgs& a, int rows, cudaStream_t s, int sms) {
-  return rows <= 16 ? run<DP, 16>(a, s, sms) : run<DP, 32>(a, s, sms);
+  return rows <= 16 ? run<DP, 16, W>(a, s, sms) : run<DP, 32, W>(a, s, sms);
 }
 
 }  // namespace
@@ -698,9 +700,9 @@ cudaError_t launch_paged_attn_few(PagedArgs a, int rows, cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1 || sms > PG_MAX_CTAS) return cudaErrorNotSupported;
   switch (ta_width(a.D)) {
-    case 64: return run_rows<64>(a, rows, s, sms);
-    case 128: return run_rows<128>(a, rows, s, sms);
-    default: return run_rows<256>(a, rows, s, sms);
+    case 64: return run_rows<64, false>(a, rows, s, sms);
+    case 128: return ta_wide(a) ? run_rows<128, true>(a, rows, s, sms) : run_rows<128, false>(a, rows, s, sms);
+    default: return ta_wide(a) ? run_rows<256, true>(a, rows, s, sms) : run_rows<256, false>(a, rows, s, sms);
   }
 }
 

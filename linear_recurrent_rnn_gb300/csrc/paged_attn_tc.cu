@@ -45,15 +45,15 @@ namespace rglru {
 
 namespace {
 
-template <int DP>
+template <int DP, bool W>
 struct Ta {
+  static constexpr bool WIDE = W;                     // TaLay
   static constexpr int NT = DP == 256 ? 1 : 2;        // row tiles
   static constexpr int SLABS = DP / 64;
   static constexpr int UPT = DP == 256 ? 2 : 1;       // ring units of a key (or value) tile
   static constexpr uint32_t UB = DP == 64 ? TA_SLAB : 2 * TA_SLAB;
   static constexpr int STAGES = DP == 64 ? 10 : 5;
   static constexpr int VROWS = TA_BN / UPT;           // rows of V in a unit
-  static constexpr uint32_t VSLAB = VROWS * 128;
   static constexpr int SOFT = NT * 128;               // softmax threads
   static constexpr int THREADS = SOFT + 128;
   static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P buffers b at 128 b, O tiles
@@ -102,7 +102,7 @@ __device__ __forceinline__ void ta_mma_ts(uint32_t d, uint32_t a, uint64_t b_des
 template <int DP>
 __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int tb1, int tid) {
   const int c0 = it.c0, c1 = it.c1;
-  using C = Ta<DP>;
+  using C = Ta<DP, false>;
   const float2* ml = reinterpret_cast<const float2*>(a.ws + a.part_ml);
   const float* po = reinterpret_cast<const float*>(a.ws + a.part_o);
   const int R = C::NT * 128;
@@ -158,11 +158,11 @@ __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int t
     a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-template <int DP>
-__global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
+template <int DP, bool W>
+__global__ void __launch_bounds__(Ta<DP, W>::THREADS, 1)
     k_paged_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedArgs a) {
-  using C = Ta<DP>;
+  using C = Ta<DP, W>;
   constexpr int NT = C::NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -605,8 +605,9 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
         constexpr uint32_t id_qk = tc::idesc_bf16(128, TA_BN, 0, 0);
         constexpr uint32_t id_pv = tc::idesc_bf16(128, DP, 0, 1);
         const uint64_t d_q = tc::smem_desc(tc::smem_u32(s_q), 16, 1024, tc::LAYOUT_SW128);
-        const uint64_t d_k = tc::smem_desc(tc::smem_u32(s_ring), 16, 1024, tc::LAYOUT_SW128);
-        const uint64_t d_v = tc::smem_desc(tc::smem_u32(s_ring), C::VSLAB, 1024, tc::LAYOUT_SW128);
+        const TaLay<C> lay(a);
+        const uint64_t d_k = tc::smem_desc(tc::smem_u32(s_ring), 16, TaLay<C>::K_GROUP, tc::LAYOUT_SW128);
+        const uint64_t d_v = tc::smem_desc(tc::smem_u32(s_ring), lay.v_slab(), lay.v_group(), tc::LAYOUT_SW128);
         uint32_t st = 0, ph = 0;            // next ring unit, parity of its `full`
         uint32_t nq[NT] = {}, no[NT] = {};  // items of tile t so far: queries taken, O begun
         uint32_t cs[NT] = {}, cp[NT] = {};  // S of tile t issued, P taken
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
                 }
                 tc::mma_bf16(tmem + C::S_COL + b * 128,
                              d_q + (((t * C::SLABS + k / 4) * TA_SLAB + k % 4 * 32) >> 4),
-                             d_k + (k_st[k / 8] * (C::UB >> 4) + ((k % 8 / 4 * TA_SLAB + k % 4 * 32) >> 4)),
+                             d_k + (k_st[k / 8] * (C::UB >> 4) + ((k % 8 / 4 * TaLay<C>::K_SLAB + k % 4 * 32) >> 4)),
                              id_qk, k > 0);
                 if (NT == 1 && k % 8 == 7) tc::mma_commit(&empty[k_st[k / 8]]);  // a unit is free once read
               }
@@ -692,8 +693,8 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
                   tc::tc_fence_after();
                 }
                 ta_mma_ts(tmem + C::O_COL + t * DP, tmem + C::S_COL + b * 128 + k * 8,
-                          d_v + (v_st[k * 16 / C::VROWS] * (C::UB >> 4) + (k * 16 % C::VROWS * 128 >> 4)), id_pv,
-                          k > 0 ? 1u : more);
+                          d_v + (v_st[k * 16 / C::VROWS] * (C::UB >> 4) + (k % (C::VROWS / 16) * TaLay<C>::V_16 >> 4)),
+                          id_pv, k > 0 ? 1u : more);
                 if (NT == 1 && (k + 1) * 16 % C::VROWS == 0) tc::mma_commit(&empty[v_st[k * 16 / C::VROWS]]);
               }
               tc::mma_commit(&pv_done[t]);
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
       }
     } else if (role == 2) {
       // ------------------------------------------------------------ rows of V that no row sees
-      ta_clear_rows<C>(ctl, s_clear, v_come, v_clean, full, s_ring);
+      ta_clear_rows<C>(a, ctl, s_clear, v_come, v_clean, full, s_ring);
     }
   }
   tc::tc_fence_before();
@@ -746,14 +747,14 @@ __global__ void __launch_bounds__(Ta<DP>::THREADS, 1)
   }
 }
 
-template <int DP>
+template <int DP, bool W>
 cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
-  using C = Ta<DP>;
+  using C = Ta<DP, W>;
   const int tb1 = std::max(1, 128 / a.g);
   CUtensorMap mq, mk, mv;
-  cudaError_t e = ta_maps(a, tb1, C::VROWS, &mq, &mk, &mv);
+  cudaError_t e = ta_maps<C>(a, tb1, &mq, &mk, &mv);
   if (e != cudaSuccess) return e;
-  const void* f = reinterpret_cast<const void*>(k_paged_attn<DP>);
+  const void* f = reinterpret_cast<const void*>(k_paged_attn<DP, W>);
   static std::atomic<uint64_t> ready{0};
   // the register split draws on what the launch gives
   e = ta_prepare(f, C::smem, C::NT == 2 ? (256 * 208 + 128 * 88) / C::THREADS : 0, ready);
@@ -776,9 +777,9 @@ cudaError_t launch_paged_attn_tc(PagedArgs a, cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1 || sms > PG_MAX_CTAS) return cudaErrorNotSupported;
   switch (ta_width(a.D)) {
-    case 64: return run<64>(a, s, sms);
-    case 128: return run<128>(a, s, sms);
-    default: return run<256>(a, s, sms);
+    case 64: return run<64, false>(a, s, sms);
+    case 128: return ta_wide(a) ? run<128, true>(a, s, sms) : run<128, false>(a, s, sms);
+    default: return ta_wide(a) ? run<256, true>(a, s, sms) : run<256, false>(a, s, sms);
   }
 }
 

@@ -73,24 +73,54 @@ struct TaClear {
 };
 constexpr int TA_CLEARS = 16;
 
+// How a unit lies in shared memory, as slabs of 64 columns in the 128-byte swizzle.  Keys: 128 rows of
+// NS slabs, values: VROWS rows of SLABS slabs.  A box has a cost of its own (measured: some 40 cycles
+// beside 13 a KB), so with pages of up to 16 rows it holds all of a unit's slabs of 8 rows (keys,
+// whose groups of 8 rows have to lie evenly spaced) or up to 16 rows (values, read 16 rows a product);
+// otherwise a box is the rows of a page of one slab, and a slab's rows lie together.  Heads
+// whose width is not a multiple of 64 stay with the latter, as zeros fill their last slab at the
+// map's inner edge.  Measured (2 prompts of 4096, 16 heads on 4; pages of 8 and 16 rows, and of 64):
+// heads of 128: 123 and 120 us (single slabs 167 and 121), 119; heads of 256: 291 and 265 (571 and
+// 356), 212.  64 requests decoding on 4096 keys: heads of 128: 102 and 97 (143 and 95), 90; heads of
+// 256: 170 and 168 (247 and 172), 165.  A template parameter, as offsets that are not constants
+// cost the thread that issues the products 4 to 20 % of the kernel.
 template <class C>
-__device__ __forceinline__ void ta_clear_rows(const TaAbort& ctl, const TaClear* rec, uint64_t* come, uint64_t* clean,
+struct TaLay {
+  static constexpr int NS = C::SLABS / C::UPT;
+  int v_log2;  // rows of a box of values
+  __device__ __forceinline__ explicit TaLay(const PagedArgs& a)
+      : v_log2(C::WIDE ? min(a.ps_log2, 4) : C::VROWS == 128 ? 7 : 6) {}
+  // bytes from one slab to the next, from one group of 8 rows to the next, from 16 rows to the next
+  static constexpr uint32_t K_SLAB = C::WIDE ? 1024 : TA_SLAB;
+  static constexpr uint32_t K_GROUP = C::WIDE ? NS * 1024 : 1024;
+  static constexpr uint32_t V_16 = C::WIDE ? C::SLABS * 2048 : 2048;
+  __device__ __forceinline__ uint32_t v_slab() const { return 128u << v_log2; }
+  __device__ __forceinline__ uint32_t v_group() const { return v_log2 == 3 ? C::SLABS * 1024 : 1024; }
+  __device__ __forceinline__ uint32_t v_row(int r) const {
+    return ((r >> v_log2) * (C::SLABS << v_log2) + (r & ((1 << v_log2) - 1))) * 128;
+  }
+};
+inline bool ta_wide(const PagedArgs& a) { return a.D > 64 && a.D % 64 == 0 && a.ps_log2 <= 4; }
+
+template <class C>
+__device__ __forceinline__ void ta_clear_rows(const PagedArgs& a, const TaAbort& ctl, const TaClear* rec, uint64_t* come, uint64_t* clean,
                                               uint64_t* full, uint8_t* ring) {
   constexpr int PIECES = C::SLABS * 8;  // 16-byte pieces of a row
   const int lane = threadIdx.x & 31;
   const int piece = lane % PIECES, sub = lane / PIECES;
+  const TaLay<C> lay(a);
   for (uint32_t n = 0; ctl.wait_long(&come[n % TA_CLEARS], n / TA_CLEARS & 1); ++n) {
     const TaClear x = rec[n % TA_CLEARS];
     if (x.p0 < 0) break;
 #pragma unroll
     for (int u = 0; u < C::UPT; ++u) {
       if (!ctl.wait(&full[x.st[u]], x.par[u])) return;
-      uint8_t* dst = ring + x.st[u] * C::UB + piece / 8 * C::VSLAB + piece % 8 * 16;
+      uint8_t* dst = ring + x.st[u] * C::UB + piece / 8 * lay.v_slab() + piece % 8 * 16;
       const int p = x.p0 + u * C::VROWS;
       for (int r = sub; r < min(x.lo - p, C::VROWS); r += 32 / PIECES)
-        *reinterpret_cast<uint4*>(dst + r * 128) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dst + lay.v_row(r)) = make_uint4(0, 0, 0, 0);
       for (int r = max(x.hi - p, 0) + sub; r < C::VROWS; r += 32 / PIECES)
-        *reinterpret_cast<uint4*>(dst + r * 128) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dst + lay.v_row(r)) = make_uint4(0, 0, 0, 0);
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
@@ -99,8 +129,8 @@ __device__ __forceinline__ void ta_clear_rows(const TaAbort& ctl, const TaClear*
 }
 
 // Copies key and value tiles into the ring, by one warp.  A tile is UPT units of UB bytes: keys
-// 128 rows of 128 (or 64) columns a unit, values VROWS rows of all columns, both as slabs of 64
-// columns in the 128-byte swizzle, page by page.  C: the kernel's constants.
+// 128 rows of 128 (or 64) columns a unit, values VROWS rows of all columns, page by page (TaLay).
+// C: the kernel's constants.
 template <class C>
 struct TaLoader {
   const PagedArgs& a;
@@ -123,13 +153,22 @@ struct TaLoader {
     const int id = __ldg(a.table + (int64_t)it.n * a.table_width + pg);
     return id >= 0 && id < a.P ? id : a.P;
   }
-  // Rows [r0, r0 + NR) of tile j, NS slabs from s0 on, SB bytes apart.
-  template <int NR, int NS, uint32_t SB>
-  __device__ __forceinline__ bool unit(const CUtensorMap* tm, int j, int id, int h, int r0, int s0) {
+  // Rows [r0, r0 + NR) of tile j, NS slabs from s0 on (wide: in boxes of 2^box_log2 rows; else a slab's
+  // rows together).
+  template <int NR, int NS>
+  __device__ __forceinline__ bool unit(const CUtensorMap* tm, int j, int id, int h, int r0, int s0, int box_log2) {
+    constexpr uint32_t SB = NR * 128;
     const int lane = threadIdx.x & 31, ps = 1 << a.ps_log2;
     if (!ctl.wait(&empty[st], ph)) return false;
     if (lane == 0) tc::mbar_expect_tx(&full[st], C::UB);
     __syncwarp();
+    if (C::WIDE) {
+      const int r = r0 + (lane << box_log2);  // this lane's box: its first row, its page's entry
+      const int page = __shfl_sync(0xffffffffu, id, (r & (TA_BN - 1)) >> a.ps_log2);
+      if (lane < NR >> box_log2)
+        tc::tma_load_5d(ring + st * C::UB + lane * (NS * 128 << box_log2), tm, &full[st], 0, r & (ps - 1), s0, h, page);
+      return advance();
+    }
     const int bx = min(ps, NR);                                    // rows of a box
     const int i = lane - (ps >= TA_BN ? 0 : r0 >> a.ps_log2);      // box of this lane's page
     if (i >= 0 && i < max(1, NR >> a.ps_log2)) {
@@ -138,6 +177,9 @@ struct TaLoader {
 #pragma unroll
       for (int s = 0; s < NS; ++s) tc::tma_load_4d(dst + s * SB, tm, &full[st], (s0 + s) * 64, off, h, id);
     }
+    return advance();
+  }
+  __device__ __forceinline__ bool advance() {
     __syncwarp();
     ++issued;
     if (++st == C::STAGES) {
@@ -150,7 +192,7 @@ struct TaLoader {
     constexpr int NS = C::SLABS / C::UPT;
 #pragma unroll
     for (int u = 0; u < C::UPT; ++u)
-      if (!unit<TA_BN, NS, TA_SLAB>(tm, j, id, h, 0, NS * u)) return false;
+      if (!unit<TA_BN, NS>(tm, j, id, h, 0, NS * u, 3)) return false;
     return true;
   }
   // Keys [lo, hi) are seen by the tile's item.
@@ -163,7 +205,7 @@ struct TaLoader {
     for (int u = 0; u < C::UPT; ++u) {
       x.st[u] = st;
       x.par[u] = ph ^ 1;
-      if (!unit<C::VROWS, C::SLABS, C::VSLAB>(tm, j, id, h, u * C::VROWS, 0)) return false;
+      if (!unit<C::VROWS, C::SLABS>(tm, j, id, h, u * C::VROWS, 0, min(a.ps_log2, 4))) return false;
     }
     if (ta_cut(j, lo, hi)) clear(x);
     return true;
@@ -188,8 +230,9 @@ struct TaLoader {
 inline int ta_width(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 // Tensor maps: queries in boxes of tb tokens x g heads x 64 columns, the caches in boxes of one
-// page's rows (at most a tile's, for values VROWS) x 64 columns.
-inline cudaError_t ta_maps(const PagedArgs& a, int tb, int vrows, CUtensorMap* mq, CUtensorMap* mk, CUtensorMap* mv) {
+// page's rows (at most a tile's, for values VROWS) x 64 columns, or of several slabs (TaLay).
+template <class C>
+cudaError_t ta_maps(const PagedArgs& a, int tb, CUtensorMap* mq, CUtensorMap* mk, CUtensorMap* mv) {
   const int ps = 1 << a.ps_log2;
   const uint64_t dq[3] = {(uint64_t)a.D, (uint64_t)a.Hq, (uint64_t)a.T};
   const uint64_t sq[2] = {(uint64_t)a.q_head * 2, (uint64_t)a.q_token * 2};
@@ -198,8 +241,18 @@ inline cudaError_t ta_maps(const PagedArgs& a, int tb, int vrows, CUtensorMap* m
   const uint64_t sk[3] = {(uint64_t)a.kc_token * 2, (uint64_t)a.kc_head * 2, (uint64_t)a.kc_page * 2};
   const uint64_t sv[3] = {(uint64_t)a.vc_token * 2, (uint64_t)a.vc_head * 2, (uint64_t)a.vc_page * 2};
   const uint32_t bk[4] = {64, (uint32_t)(ps < TA_BN ? ps : TA_BN), 1, 1};
-  const uint32_t bv[4] = {64, (uint32_t)(ps < vrows ? ps : vrows), 1, 1};
+  const uint32_t bv[4] = {64, (uint32_t)(ps < C::VROWS ? ps : C::VROWS), 1, 1};
   cudaError_t e = encode_tmap(mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (C::WIDE) {
+    const uint64_t dw[5] = {64, (uint64_t)ps, (uint64_t)a.D / 64, (uint64_t)a.Hkv, (uint64_t)a.P};
+    const uint64_t wk[4] = {sk[0], 128, sk[1], sk[2]}, wv[4] = {sv[0], 128, sv[1], sv[2]};
+    const uint32_t xk[5] = {64, 8, C::SLABS / C::UPT, 1, 1}, xv[5] = {64, (uint32_t)ps, C::SLABS, 1, 1};
+    if (e == cudaSuccess)
+      e = encode_tmap(mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, a.kc, dw, wk, xk, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess)
+      e = encode_tmap(mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, a.vc, dw, wv, xv, CU_TENSOR_MAP_SWIZZLE_128B);
+    return e;
+  }
   if (e == cudaSuccess)
     e = encode_tmap(mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.kc, dk, sk, bk, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e == cudaSuccess)

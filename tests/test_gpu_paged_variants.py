@@ -121,3 +121,18 @@ def test_split_items_repeat_bitwise():
         attend(other, 1.0)
         o2, L2, _ = attend(x, 96 ** -0.5, ws=ws)
         assert torch.equal(o, o2) and torch.equal(L, L2)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("layout", ["nhd", "hnd"])
+@pytest.mark.parametrize("D", [64, 80, 128, 192, 256])
+@pytest.mark.parametrize("s", [8, 16, 32, 128])
+def test_pages_and_widths(s, D, layout, new):
+    """Pages from one swizzle atom to a whole tile, for widths with and without boxes of several
+    column slabs: tiles cut at either end and inside a page, caches stored either way round."""
+    lens = [(new, 300), (new, 131), (new, new), (new, 256)]
+    for window in (0, 75):
+        x = build(lens, 6, 2, D, s, "bf16", s + D, layout)
+        o, L, ws = attend(x, D ** -0.5, window)
+        assert R.rglru_sync_status(ws) == R.OK
+        compare(o, L, expect(x, D ** -0.5, window), "bf16")
