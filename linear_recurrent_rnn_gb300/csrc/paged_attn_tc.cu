@@ -87,6 +87,9 @@ __device__ __forceinline__ void ta_store32(bf16* p, const uint32_t* u) {
                : "memory");
 }
 
+// Bits 0 to h, none for a negative h.
+__device__ __forceinline__ uint32_t ta_bits(int h) { return h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1; }
+
 // D[tmem] (+)= A[tmem] B[smem]
 __device__ __forceinline__ void ta_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -305,8 +308,11 @@ __global__ void __launch_bounds__(Ta<DP, W>::THREADS, 1)
           const int k0 = j * TA_BN;
           if (k0 + TA_BN - 1 > p_first || (a.window && k0 < p_last - a.window + 1)) {
             const int hi = pos - k0, lo = a.window ? hi - a.window : -1;  // lo < column <= hi
+            uint32_t bits[4];  // one a column: a test and a select a score
 #pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = c <= hi && c > lo ? s[c] : -INFINITY;
+            for (int w = 0; w < 4; ++w) bits[w] = ta_bits(hi - 32 * w) & ~ta_bits(lo - 32 * w);
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = bits[c / 32] & (1u << c % 32) ? s[c] : -INFINITY;
           }
           float mx[4] = {m, s[1], s[2], s[3]};
           mx[0] = fmaxf(m, s[0]);
