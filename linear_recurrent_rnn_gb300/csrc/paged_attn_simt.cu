@@ -15,11 +15,13 @@
 // each, with maxima and sums of their own that are joined when the item ends.
 // Tiles are gathered by 16-byte asynchronous copies, row by row through the block table (whose
 // entries are looked up one tile ahead): values land behind the scores, the next keys behind P V.
-// Keys that no row of the item sees are not read, their rows are zero.  Work is divided over CTAs
+// Keys that no row of the item sees are not read, their rows are zero.  Products
+// run over the columns in use, not the tile's width (heads of 192, 64 requests with a window of 256: 137 -> 116
+// us; heads of 96, 249 requests decoding: 408 -> 368).  Work is divided over CTAs
 // by weight (paged.cuh).
 //
-// Measured (GB300): 64 requests of 500 to 4096 keys, 16 query heads on 4 of 128 (452 MB): 112 us,
-// 4.0 TB/s: eight warps an SM do not cover the latencies of a tile's phases.  Two chunks of 1024 tokens over 2048
+// Measured (GB300): 64 requests of 500 to 4096 keys, 16 query heads on 4 of 128 (452 MB): 111 us,
+// 4.1 TB/s: eight warps an SM do not cover the latencies of a tile's phases.  Two chunks of 1024 tokens over 2048
 // keys, the same heads: 651 us, 40 TFLOP/s of 74: shared-memory reads and the two barriers a tile
 // with 8 warps an SM (row tiles of 128 and 16 warps: 590 us here, but slower for short calls, as
 // 128 registers a thread spill).
@@ -43,6 +45,7 @@ struct Sa {
   static constexpr int TILE = SPLIT * BN;
   static constexpr int KS = BN / 16;     // keys a thread
   static constexpr int C4 = DP / 64;     // times four columns of O a thread
+  static constexpr int DS = KS > 2 ? 16 : 32;  // columns of Q K^T at a time
   static constexpr int LD = DP + 4;      // row stride: 16-byte reads of 8 rows meet all banks
   static constexpr int CTAS = (BM == 64 && DP == 64) || BM == 8 ? 2 : 1;  // per SM
   // shared memory, in floats: queries, keys, values, P^T of each warp; then row offsets
@@ -170,21 +173,24 @@ __global__ void __launch_bounds__(Sa<BM, DP>::THREADS, Sa<BM, DP>::CTAS) k_paged
         for (int k = 0; k < C::KS; ++k) s2[i][k] = make_float2(0.0f, 0.0f);
       const float* kp = s_k + (sp * C::BN + tx) * C::LD;
       const float* qp = s_q + r0 * C::LD;
-#pragma unroll 4
-      for (int d = 0; d < DP; d += 4) {
-        float4 q[4];
+      // (columns past D are zero up to the next multiple of DS)
+#pragma unroll 1
+      for (int d0 = 0; d0 < a.D; d0 += C::DS)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(qp + i * C::LD + d);
+        for (int d = d0; d < d0 + C::DS; d += 4) {
+          float4 q[4];
 #pragma unroll
-        for (int k = 0; k < C::KS; ++k) {
-          const float4 x = *reinterpret_cast<const float4*>(kp + k * 16 * C::LD + d);
+          for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(qp + i * C::LD + d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s2[i][k] = sa_fma2(make_float2(q[i].x, q[i].y), make_float2(x.x, x.y), s2[i][k]);
-            s2[i][k] = sa_fma2(make_float2(q[i].z, q[i].w), make_float2(x.z, x.w), s2[i][k]);
+          for (int k = 0; k < C::KS; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(kp + k * 16 * C::LD + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s2[i][k] = sa_fma2(make_float2(q[i].x, q[i].y), make_float2(x.x, x.y), s2[i][k]);
+              s2[i][k] = sa_fma2(make_float2(q[i].z, q[i].w), make_float2(x.z, x.w), s2[i][k]);
+            }
           }
         }
-      }
       float p[4][C::KS];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -220,12 +226,13 @@ __global__ void __launch_bounds__(Sa<BM, DP>::THREADS, Sa<BM, DP>::CTAS) k_paged
       __syncthreads();  // for everyone, and the keys are used
       if (j + 1 < j1) load(j + 1, 0);
       const float* vp = s_v + sp * C::BN * C::LD + tx * 4;
-#pragma unroll 4
+#pragma unroll (C::C4 > 1 || BM == 64 ? 4 : 8)
       for (int k = 0; k < C::BN; ++k) {
         const float4 x = *reinterpret_cast<const float4*>(s_p + k * 8);
         const float pr[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int c = 0; c < C::C4; ++c) {
+          if (c > C::C4 / 2 && 64 * c >= a.D) break;  // (D is above DP / 2)
           const float4 v = *reinterpret_cast<const float4*>(vp + k * C::LD + 64 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
