@@ -2,7 +2,7 @@
 // and the call, in one step.  A step of a serving loop makes three calls whose kernels take 2 to
 // 10 us, and reading dtype, shape, device and strides of ten tensors through Python takes 4 us
 // more than reading them here (measured for paged_plan: 8.0 us a call through Python, of which
-// 2.2 us the ctypes call; 4.4 from here; the kernel takes 4.2).
+// 2.2 us the ctypes call; 3.3 from here).
 //
 // The library is not linked: setup() is handed the addresses of its functions, so that
 // whichever librglru.so the package has loaded is the one that is called.

@@ -19,10 +19,10 @@ namespace {
 // all have read before one writes, so they are then one cluster, which meets in between.
 // Tokens: a warp takes 32 in a row and searches the offsets for the first; the others are mostly
 // in the same request.  Latency-bound: the floor is a launch, two dependent reads (lengths, then
-// table or ring) and the writes.  Measured (GB300): 4.0 us for 8 requests, 5.0 for 512, 7.2 for 1024
+// table or ring) and the writes.  Measured (GB300): 3.0 us for 8 requests, 4.8 for 512, 6.1 for 1024
 // requests with 130 000 new tokens.
 struct PlanArgs {
-  int N, T, P, s, s_log2, width;
+  int N, T, P, s, s_log2, width, cluster;
   const int32_t* cached;
   const int32_t* fresh;
   const int32_t* ring;
@@ -47,73 +47,79 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
   int32_t* s_cu = plan_sm;
   int32_t* s_off = s_cu + a.N + 1;
   int32_t* s_c = s_off + a.N + 1;
-  __shared__ int64_t s_warp[2][32];
+  __shared__ int64_t s_warp[3][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   tc::griddep_wait();
   tc::griddep_launch_dependents();
   const int head = a.state[0], count = min(max(a.state[1], 0), a.P);
-  int64_t base_q = 0, base_p = 0, over = 0;  // over: pages wanted past the table's width
-  for (int n0 = 0; n0 < a.N; n0 += blockDim.x) {
-    const int n = n0 + tid;
-    int c = 0, q = 0, need = 0;
-    if (n < a.N) {
-      c = max(a.cached[n], 0);
-      q = max(a.fresh[n], 0);
-      const int held = min(plan_ceil(c, a), a.width);
-      const int want = plan_ceil((int64_t)c + q, a);
-      need = max(min(want, a.width) - held, 0);
-      over += max(want - max(plan_ceil(c, a), a.width), 0);
-    }
-    int64_t sq = q, sp = need;
+  // a thread's requests are neighbours: one scan over the CTA whatever their number
+  const int per = a.N <= (int)blockDim.x ? 1 : (a.N + blockDim.x - 1) / blockDim.x;
+  const int n0 = min(tid * per, a.N), n1 = min(n0 + per, a.N);
+  int64_t q_sum = 0, p_sum = 0, over = 0;  // over: pages wanted past the table's width
+  for (int n = n0; n < n1; ++n) {
+    const int c = max(a.cached[n], 0), q = max(a.fresh[n], 0);
+    const int held = plan_ceil(c, a), want = plan_ceil((int64_t)c + q, a);
+    const int need = max(min(want, a.width) - min(held, a.width), 0);
+    over += max(want - max(held, a.width), 0);
+    s_c[n] = c;
+    s_cu[n] = q;
+    s_off[n] = need;
+    q_sum += q;
+    p_sum += need;
+  }
+  int64_t sq = q_sum, sp = p_sum;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, sq, d), v = __shfl_up_sync(0xffffffffu, sp, d);
-      if (lane >= d) {
-        sq += u;
-        sp += v;
-      }
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, sq, d), v = __shfl_up_sync(0xffffffffu, sp, d);
+    if (lane >= d) {
+      sq += u;
+      sp += v;
     }
-    if (lane == 31) {
-      s_warp[0][warp] = sq;
-      s_warp[1][warp] = sp;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) over += __shfl_xor_sync(0xffffffffu, over, d);
+  if (lane == 31) {
+    s_warp[0][warp] = sq;
+    s_warp[1][warp] = sp;
+    s_warp[2][warp] = over;
+  }
+  __syncthreads();
+  int64_t all_q = 0, all_p = 0, all_over = 0;
+  sq -= q_sum;
+  sp -= p_sum;
+  for (int k = 0; k < nw; ++k) {
+    const int64_t u = s_warp[0][k], v = s_warp[1][k];
+    all_q += u;
+    all_p += v;
+    all_over += s_warp[2][k];
+    if (k < warp) {
+      sq += u;
+      sp += v;
     }
-    __syncthreads();
-    for (int k = 0; k < nw; ++k) {
-      const int64_t u = s_warp[0][k], v = s_warp[1][k];
-      if (k < warp) {
-        sq += u;
-        sp += v;
-      }
-    }
-    if (n < a.N) {
-      s_cu[n] = (int)min(base_q + sq - q, (int64_t)0x7fffffff);
-      s_off[n] = (int)min(base_p + sp - need, (int64_t)0x7fffffff);
-      s_c[n] = c;
-    }
-    for (int k = 0; k < nw; ++k) {
-      base_q += s_warp[0][k];
-      base_p += s_warp[1][k];
-    }
-    __syncthreads();
+  }
+  for (int n = n0; n < n1; ++n) {
+    const int q = s_cu[n], need = s_off[n];
+    s_cu[n] = (int)min(sq, (int64_t)0x7fffffff);
+    s_off[n] = (int)min(sp, (int64_t)0x7fffffff);
+    sq += q;
+    sp += need;
   }
   if (tid == 0) {
-    s_cu[a.N] = (int)min(base_q, (int64_t)0x7fffffff);
-    s_off[a.N] = (int)min(base_p, (int64_t)0x7fffffff);
+    s_cu[a.N] = (int)min(all_q, (int64_t)0x7fffffff);
+    s_off[a.N] = (int)min(all_p, (int64_t)0x7fffffff);
   }
-  for (int d = 16; d; d >>= 1) over += __shfl_xor_sync(0xffffffffu, over, d);
-  if (lane == 0) s_warp[0][warp] = over;
   // in place: every CTA has read its inputs before any CTA writes
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (a.cluster > 1)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
-  const int h0 = a.P > 0 ? ((head % a.P) + a.P) % a.P : 0;
+  const int h0 = (uint32_t)head < (uint32_t)a.P ? head : (head % a.P + a.P) % a.P;
   const int stride = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + tid;
   if (first == 0) {
-    int64_t o = 0;
-    for (int k = 0; k < nw; ++k) o += s_warp[0][k];
     const int taken = min(s_off[a.N], count);
-    a.state_out[0] = (int)(((int64_t)h0 + taken) % a.P);
+    const int64_t next = (int64_t)h0 + taken;  // (taken <= P: at most once around)
+    a.state_out[0] = (int)(next < a.P ? next : next - a.P);
     a.state_out[1] = count - taken;
-    a.state_out[2] = (int)min((int64_t)s_off[a.N] - taken + o, (int64_t)0x7fffffff);
+    a.state_out[2] = (int)min((int64_t)s_off[a.N] - taken + all_over, (int64_t)0x7fffffff);
   }
   auto owner = [&](const int32_t* v, int x) {  // the last n with v[n] <= x
     int l = 0, h = a.N - 1;
@@ -341,9 +347,12 @@ extern "C" rglru_status paged_plan(const paged_shape* s, const int32_t* cached_l
     ctas = in_place ? PLAN_CLUSTER : std::min(PLAN_CTAS, (s->tokens + PLAN_THREADS - 1) / PLAN_THREADS);
     cluster = in_place ? PLAN_CLUSTER : 1;
   }
+  a.cluster = cluster;
+  // no more warps than requests and rows ask for: every warp reads every other's sums
+  const int threads = (std::min(PLAN_THREADS, std::max(s->num_seqs, s->tokens)) + 31) / 32 * 32;
   void* args[] = {&a};
   return cuda_status(launch_pdl(reinterpret_cast<const void*>(k_paged_plan), dim3(ctas),
-                                dim3(PLAN_THREADS), smem, stream, args, cluster));
+                                dim3(threads), smem, stream, args, cluster));
 }
 
 extern "C" rglru_status paged_kv_write(const paged_shape* s, const paged_strides* strides,
