@@ -6,7 +6,8 @@ import pytest
 import torch
 
 from linear_recurrent_rnn_gb300 import librglru as R
-from test_gpu_paged import attend, build, compare, expect, f64
+from oracle import paged as O
+from test_gpu_paged import attend, build, compare, expect, f64, run_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +137,20 @@ def test_pages_and_widths(s, D, layout, new):
         o, L, ws = attend(x, D ** -0.5, window)
         assert R.rglru_sync_status(ws) == R.OK
         compare(o, L, expect(x, D ** -0.5, window), "bf16")
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("N,tokens", [(1, 0), (1, 3), (32, 32), (33, 40), (513, 20), (513, 700), (1025, 1025), (2049, 5)])
+def test_plan_where_its_warps_are_not_full(N, tokens, in_place):
+    """Requests and rows about the sizes at which a warp, a CTA or a thread's share fills up; some
+    requests past the table's width, rows short of the new tokens or beyond them."""
+    rng = np.random.default_rng(N + tokens)
+    cached = rng.integers(0, 60, N)
+    new = np.where(rng.random(N) < min(1.0, tokens / N), rng.integers(0, 3, N), 0)
+    P = 4 * N + 7
+    table, free = rng.integers(0, P, (N, 4)), rng.permutation(P)
+    args = (cached, new, free, [P - 3, N + 2, 0], table, 16)
+    want = O.plan(*args, tokens)
+    got = run_plan(*args, tokens, in_place)
+    for n, a, b in zip(("table", "cu", "kv_lens", "positions", "slots", "state"), got, want):
+        np.testing.assert_array_equal(a, b, err_msg=n)
