@@ -25,7 +25,7 @@
 // Measured (GB300): 64 requests of 4096 keys, 16 heads of 128: 314 us, 6.7 TB/s, the copy
 // bandwidth.  256 requests of 64 to 8192 keys, 32 query heads on 8 (1.78 GB): 290 us, 6.1 TB/s;
 // what is missing is the switch from item to item where they have one or two key tiles, and the
-// start.  128 requests with a window of 2048, 10 query heads of 256 on one (227 MB): 49 us, 4.6
+// start.  128 requests with a window of 2048, 10 query heads of 256 on one (227 MB): 48.4 us, 4.7
 // TB/s: 14 key tiles a CTA, of which one is a rounding loss, 3 us of start and 4 us of joining
 // parts.  One request of 1000 keys: 10.6 us, all latency: 4 us to the first product (lengths,
 // division of work, table entry, copy: each a round trip), 3 to the parts, 3 to their join.
@@ -683,8 +683,8 @@ cudaError_t run(PagedArgs& a, cudaStream_t s, int sms) {
   a.part_ml = L.ml;
   a.part_o = L.o;
   a.rows = NR;
-  // an item's switch costs about a key tile's time
-  pg_division(a, sms, 128, 192, 128);
+  // an item's switch costs about a key tile's time, a part's hand-over and join more
+  pg_division(a, sms, 128, 192, 256);
   void* args[] = {&mq, &mk, &mv, &a};
   return launch_pdl(f, dim3(sms), dim3(TF_THREADS), C::smem, s, args, 1);
 }
