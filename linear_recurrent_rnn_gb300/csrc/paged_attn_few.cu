@@ -19,7 +19,9 @@
 // The steps (key tiles) of all of a CTA's items form one stream: loads, products and softmax run
 // on across the items' ends, with two buffers of S^T, P^T and O^T and several of Q, so that the
 // ring of key and value tiles never runs dry.  Step i's S^T is computed before step i - 1's O^T,
-// behind whose softmax it runs.  Warps: 4 softmax, key/value loader, MMA issuer (one thread), one
+// behind whose softmax it runs; an item without keys (rows before position 0, a request without
+// any) has no step to put the last O^T behind, so there it is computed at once: the softmax warps
+// keep an item's record until its O^T is done, and records are few.  Warps: 4 softmax, key/value loader, MMA issuer (one thread), one
 // that clears rows of V that no row sees, and one that walks the items and loads queries.
 //
 // Measured (GB300): 64 requests of 4096 keys, 16 heads of 128: 314 us, 6.7 TB/s, the copy
@@ -478,6 +480,10 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
       if (it.n < 0) break;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
+      if (it.j1 <= it.j0 && pend) {  // (as the MMA issuer does)
+        ok = ld.values(&tm_v, pj, pid, ph, plo, phi);
+        pend = false;
+      }
       int id = ld.page_of(it, it.j0);
       for (int j = it.j0; j < it.j1 && ok; ++j) {
         const int id_next = ld.page_of(it, j + 1);
@@ -562,6 +568,10 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
         if (it.n < 0) break;
         const int j0 = it.j0, j1 = it.j1, lo = it.lo, hi = it.hi;
         tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
+        if (j1 <= j0 && pend) {  // no step to wait for: items without keys may follow one another
+          product();
+          pend = false;
+        }
         const uint32_t qb = nq % C::QBUF;
         for (int j = j0; j < j1 && ok; ++j, ++step) {
           uint32_t at[C::UPT], arr[C::UPT];
