@@ -266,7 +266,9 @@ __global__ void __launch_bounds__(STC_THREADS, 1)
     tc::tmem_relinquish();
   }
   tc::griddep_wait();
-  tc::griddep_launch_dependents();
+  // By the warp that holds the TMEM, not before: a CTA of the next grid (a step's, or one of the
+  // paged attention) that takes TMEM keeps it until this grid has ended.
+  if (warp == 1) tc::griddep_launch_dependents();
   // the operand loads go out first: thread 0 issues them at once
   if (threadIdx.x == 0) {
     tc::mbar_expect_tx(full, XB + 4 * WS);

@@ -182,7 +182,9 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
   for (uint32_t i = tid; i < C::QBUF * C::QB / 16; i += TF_THREADS)
     reinterpret_cast<uint4*>(s_q)[i] = make_uint4(0, 0, 0, 0);
   tc::griddep_wait();
-  tc::griddep_launch_dependents();
+  // By the warp that holds the TMEM, not before: a CTA of the next grid that takes TMEM (a decode
+  // step's fits beside this one) keeps it until this grid has ended.
+  if (role == 1) tc::griddep_launch_dependents();
   PgWalk w;
   PgWalk::Found start;
   if (a.N <= PG_WARP_SEQS) {
