@@ -109,8 +109,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
     s_off[a.N] = (int)min(all_p, (int64_t)0x7fffffff);
   }
   // in place: every CTA has read its inputs before any CTA writes
-  if (a.cluster > 1)
+  if (a.cluster > 1) {
+    __syncwarp();  // the barrier's form is the warp-aligned one
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
   __syncthreads();
   const int h0 = (uint32_t)head < (uint32_t)a.P ? head : (head % a.P + a.P) % a.P;
   const int stride = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + tid;

@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
         int h = 0;
 #pragma unroll 1
         for (int c = 0; c < rows; c += 4) {
+          __syncwarp();  // (TMEM is read by whole warps)
           float o[C::MH][4];
 #pragma unroll
           for (int hm = 0; hm < C::MH; ++hm)

@@ -425,6 +425,7 @@ __global__ void __launch_bounds__(Ta<DP, W>::THREADS, 1)
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll 1
           for (int c = 0; c < DP && c < a.D; c += 32) {
+            __syncwarp();  // (TMEM is read by whole warps)
             float v[32];
             if (any) {
               tc::tmem_ld16(t_o + c, *reinterpret_cast<float(*)[16]>(v));
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(Ta<DP, W>::THREADS, 1)
             float* po = const_cast<float*>(g_o) + (size_t)it.slot * DP * R + row;
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
+              __syncwarp();
               float v[32];
               tc::tmem_ld16(t_o + c, *reinterpret_cast<float(*)[16]>(v));
               tc::tmem_ld16(t_o + c + 16, *reinterpret_cast<float(*)[16]>(v + 16));

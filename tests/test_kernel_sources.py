@@ -57,3 +57,50 @@ def test_the_next_grid_starts_after_tmem_is_held(name):
         go = re.search(r"(?:if \(([^\n]*)\) )?(?:tc::)?griddep_launch_dependents\(\)", body)
         assert alloc and go and alloc.start() < go.start()
         assert go.group(1) == alloc.group(1) or "__syncthreads()" in body[alloc.end():go.start()], name
+
+
+def loops(body):
+    """The bodies of the innermost braced loops around each TMEM access."""
+    spans = []
+    for m in re.finditer(r"\bfor \(", body):
+        depth, i = 0, m.end() - 1
+        while True:
+            depth += {"(": 1, ")": -1}.get(body[i], 0)
+            i += 1
+            if not depth:
+                break
+        while body[i] in " \n":
+            i += 1
+        if body[i] != "{":
+            continue
+        j, depth = i, 0
+        while True:
+            depth += {"{": 1, "}": -1}.get(body[j], 0)
+            j += 1
+            if not depth:
+                break
+        spans.append((i, j))
+    for m in re.finditer(r"tc::tmem_(ld|st)\d", body):
+        inside = [s for s in spans if s[0] < m.start() < s[1]]
+        if inside:
+            i, j = max(inside)
+            yield body[i:j], m.start() - i
+
+
+@pytest.mark.parametrize("name", ["paged_attn_tc.cu", "paged_attn_few.cu"])
+def test_tmem_is_read_by_converged_warps(name):
+    """tcgen05's loads and stores want all lanes of the warp there: a loop whose body branches by
+    thread brings them together before the access."""
+    seen = 0
+    for body in kernels(name):
+        for loop, at in loops(body):
+            if re.search(r"\b(mine|tid)\b", loop):
+                seen += 1
+                assert re.search(r"__syncwarp\(\)|ctl\.wait\(|tf_any\(", loop[:at]), loop[:200]
+    assert seen
+
+
+@pytest.mark.parametrize("name", [f for f in FILES if f.startswith("paged")])
+def test_aligned_cluster_barriers_are_met_by_converged_warps(name):
+    for m in re.finditer(r"barrier\.cluster\.arrive[.\w]*\.aligned", source(name)):
+        assert re.search(r"__syncwarp\(\);\s*asm volatile\(\"$", source(name)[:m.start()])
