@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(WRITE_THREADS) k_paged_write(const WriteArgs a
         if (i >= 2 * a.pieces) continue;
         const int kv = i >= a.pieces, c = kv ? i - a.pieces : i;
         const int h = c / a.head_pieces, b = (c - h * a.head_pieces) * 16;
-        x[e] = __ldg(reinterpret_cast<const uint4*>(a.src[kv] + t * a.src_token[kv] + h * a.src_head[kv] + b));
+        x[e] = *reinterpret_cast<const uint4*>(a.src[kv] + t * a.src_token[kv] + h * a.src_head[kv] + b);
         to[e] = a.dst[kv] + page * a.dst_page[kv] + off * a.dst_token[kv] + h * a.dst_head[kv] + b;
       }
 #pragma unroll

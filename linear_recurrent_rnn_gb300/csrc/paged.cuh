@@ -357,7 +357,9 @@ size_t paged_attn_few_ws_bytes(const paged_shape* s, int rows);
 cudaError_t launch_paged_attn_simt(PagedArgs a, int rows, cudaStream_t s);
 size_t paged_attn_simt_ws_bytes(const paged_shape* s, int rows);
 
-// One kernel on `s` with programmatic stream serialisation (and clusters of `cluster` CTAs).
+// One kernel on `s` with programmatic stream serialisation (and clusters of `cluster` CTAs).  Such a
+// kernel's lifetime overlaps the one before it, which may be writing what this one reads: what
+// comes after griddep_wait are ordinary loads, none through the non-coherent path (__ldg).
 cudaError_t launch_pdl(const void* f, dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        void** args, int cluster);
 

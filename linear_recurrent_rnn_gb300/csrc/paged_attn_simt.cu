@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(Sa<BM, DP>::THREADS, Sa<BM, DP>::CTAS) k_paged
       int64_t ko = -1, vo = -1;
       if (p >= it.lo && p < it.hi) {
         const int pg = p >> a.ps_log2, off = p & ((1 << a.ps_log2) - 1);
-        const int id = pg < a.table_width ? __ldg(a.table + (int64_t)it.n * a.table_width + pg) : -1;
+        const int id = pg < a.table_width ? a.table[(int64_t)it.n * a.table_width + pg] : -1;
         if (id >= 0 && id < a.P) {
           ko = id * a.kc_page + off * a.kc_token;
           vo = id * a.vc_page + off * a.vc_token;

@@ -150,7 +150,7 @@ struct TaLoader {
     if (j >= it.j1 || lane >= max(1, TA_BN >> a.ps_log2)) return a.P;
     const int pos = j * TA_BN + (lane << a.ps_log2), pg = pos >> a.ps_log2;
     if (pos >= it.hi || pos + min(1 << a.ps_log2, TA_BN) <= it.lo || pg >= a.table_width) return a.P;
-    const int id = __ldg(a.table + (int64_t)it.n * a.table_width + pg);
+    const int id = a.table[(int64_t)it.n * a.table_width + pg];
     return id >= 0 && id < a.P ? id : a.P;
   }
   // Rows [r0, r0 + NR) of tile j, NS slabs from s0 on (wide: in boxes of 2^box_log2 rows; else a slab's

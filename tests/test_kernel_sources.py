@@ -104,3 +104,10 @@ def test_tmem_is_read_by_converged_warps(name):
 def test_aligned_cluster_barriers_are_met_by_converged_warps(name):
     for m in re.finditer(r"barrier\.cluster\.arrive[.\w]*\.aligned", source(name)):
         assert re.search(r"__syncwarp\(\);\s*asm volatile\(\"$", source(name)[:m.start()])
+
+
+@pytest.mark.parametrize("name", sorted({f for f in FILES if any(early(b) for b in kernels(f))} | {"paged.cuh", "paged_tc.cuh"}))
+def test_kernels_that_start_early_use_coherent_loads(name):
+    """The non-coherent path is for memory that nothing writes while the kernel lives; the life of
+    a kernel with programmatic stream serialisation overlaps that of the grid before it."""
+    assert not re.search(r"__ldg\b|\.nc\b|ld\.global\.nc|__restrict__", source(name))
