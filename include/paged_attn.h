@@ -22,11 +22,12 @@
  *     request n's are [cu_seqlens[n], cu_seqlens[n + 1]).  Rows past cu_seqlens[num_seqs] are
  *     padding.  A request may have no new token.
  *   - Supported: page_size a power of two from 8 to 4096; 1 <= num_seqs <= 8192;
- *     num_pages * page_size < 2^31; for paged_kv_write and paged_attention 8 <= D <= 256 with
- *     D * sizeof(io) a multiple of 16 bytes, and for paged_attention Hq a multiple of Hkv with
- *     Hq / Hkv <= 64; else RGLRU_ERR_UNSUPPORTED (RGLRU_ERR_INVALID_ARG where a size has no
- *     meaning).  Pointers to q, k, v, o and the caches are 16-byte aligned and their strides
- *     positive multiples of 16 bytes; the other arrays are aligned to their element.
+ *     num_pages * page_size < 2^31; num_seqs * table_width < 2^31; tokens <= 2^30; for
+ *     paged_kv_write and paged_attention 8 <= D <= 256 with D * sizeof(io) a multiple of 16
+ *     bytes, and for paged_attention Hq a multiple of Hkv with Hq / Hkv <= 64; else
+ *     RGLRU_ERR_UNSUPPORTED (RGLRU_ERR_INVALID_ARG where a size has no meaning).  Pointers to
+ *     q, k, v, o and the caches are 16-byte aligned and their strides positive multiples of 16
+ *     bytes; the other arrays are aligned to their element.
  *   - Values read from device memory are never trusted with an address: lengths and offsets
  *     out of range are clamped, a slot outside the cache is skipped, a table entry outside the
  *     cache (or past table_width) reads as zero keys and values.  Such input gives wrong

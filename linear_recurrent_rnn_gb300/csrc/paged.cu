@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
     if (n < a.N)
       a.kv_lens[n] = (int)min((int64_t)s_c[n] + (s_cu[n + 1] - s_cu[n]), (int64_t)0x7fffffff);
   }
-  for (int i = first; i < s_off[a.N]; i += stride) {
-    const int n = owner(s_off, i);
+  for (int64_t k = first; k < s_off[a.N]; k += stride) {  // (a step past the end may pass 2^31)
+    const int i = (int)k, n = owner(s_off, i);
     a.table[(size_t)n * a.width + plan_ceil(s_c[n], a) + (i - s_off[n])] = ring(i);
   }
   const int total = s_cu[a.N];
@@ -233,7 +233,8 @@ rglru_status check_cache(const paged_shape* s) {
       s->table_width < 1)
     return RGLRU_ERR_INVALID_ARG;
   if ((s->page_size & (s->page_size - 1)) || s->page_size < 8 || s->page_size > 4096 ||
-      s->num_seqs > PG_MAX_SEQS || (int64_t)s->num_pages * s->page_size > 0x7fffffffLL)
+      s->num_seqs > PG_MAX_SEQS || (int64_t)s->num_pages * s->page_size > 0x7fffffffLL ||
+      s->tokens > PG_MAX_TOKENS || (int64_t)s->num_seqs * s->table_width > 0x7fffffffLL)
     return RGLRU_ERR_UNSUPPORTED;
   return RGLRU_OK;
 }

@@ -26,6 +26,7 @@
 namespace rglru {
 
 constexpr int PG_MAX_SEQS = 8192;
+constexpr int PG_MAX_TOKENS = 1 << 30;  // rows and lengths up to 2^30: sums of two, or a step past the end, fit 32 bits
 constexpr int PG_MAX_CTAS = 1024;
 constexpr int PG_WARP_SEQS = 32;  // requests that one warp scans alone
 
