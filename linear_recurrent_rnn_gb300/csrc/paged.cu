@@ -39,6 +39,8 @@ constexpr int PLAN_THREADS = 512;
 constexpr int PLAN_CLUSTER = 8;   // CTAs in place
 constexpr int PLAN_CTAS = 128;    // CTAs otherwise, at most
 
+constexpr size_t plan_smem(int N) { return (size_t)(3 * N + 2) * 4; }
+
 __device__ __forceinline__ int plan_ceil(int64_t x, const PlanArgs& a) { return (int)((x + a.s - 1) >> a.s_log2); }
 
 __global__ void __launch_bounds__(PLAN_THREADS) k_paged_plan(const PlanArgs a) {
@@ -337,12 +339,12 @@ extern "C" rglru_status paged_plan(const paged_shape* s, const int32_t* cached_l
   a.positions = positions;
   a.slots = slots;
   a.state_out = free_state_out;
-  const size_t smem = (size_t)(3 * a.N + 2) * 4;
-  if (smem > 48 << 10) {
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k_paged_plan),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return cuda_status(e);
-  }
+  // once a device, to what the most requests take: a limit set call by call would be another
+  // thread's too, between its own setting and its launch
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = ta_prepare(reinterpret_cast<const void*>(k_paged_plan), plan_smem(PG_MAX_SEQS), 0, ready);
+  if (e != cudaSuccess) return cuda_status(e);
+  const size_t smem = plan_smem(a.N);
   // one CTA up to a row a thread; beyond, one to two rows a thread, or the cluster
   const bool in_place = kv_lens == cached_lens || free_state_out == free_state;
   int ctas = 1, cluster = 1;

@@ -1,6 +1,12 @@
-"""The paged cache at its edges: requests and row tiles without keys in the middle of a CTA's work.
-Tolerances as in test_gpu_paged.py."""
+"""The paged cache at its edges: requests and row tiles without keys in the middle of a CTA's work, and plans
+of the largest sizes.  Tolerances as in test_gpu_paged.py."""
+import os
+import subprocess
+import sys
+import threading
+
 import pytest
+import torch
 
 from linear_recurrent_rnn_gb300 import librglru as R
 from test_gpu_paged import attend, build, compare, expect
@@ -40,3 +46,54 @@ def test_row_tiles_without_keys_many_rows(D):
     o, L, ws = attend(x, D ** -0.5)
     assert R.rglru_sync_status(ws) == R.OK
     compare(o, L, expect(x, D ** -0.5), "bf16")
+
+
+# ---------------------------------------------------------------- the plan's largest sizes
+PLANS_IN_ORDER = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import numpy as np
+from oracle import paged as O
+from test_gpu_paged import run_plan
+for N in (4031, 4032, 4095, 4096):
+    rng = np.random.default_rng(N)
+    cached, new = rng.integers(0, 60, N), rng.integers(0, 2, N)
+    table, free = rng.integers(0, 4 * N, (N, 4)), rng.permutation(4 * N)
+    args = (cached, new, free, [3, N, 0], table, 16)
+    for a, b in zip(run_plan(*args, 5000, False), O.plan(*args, 5000)):
+        np.testing.assert_array_equal(a, b)
+print("plans are right")
+"""
+
+
+def test_plans_about_the_default_shared_memory():
+    """In a process of its own, from the smallest on: no larger call has raised the limit before."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", PLANS_IN_ORDER.format(root=os.path.dirname(tests), tests=tests)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "plans are right" in r.stdout, r.stdout + r.stderr
+
+
+def test_plans_of_two_sizes_from_two_threads():
+    """Each call takes the shared memory that it needs, whatever another thread calls for meanwhile."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    wrong = []
+
+    def calls(N):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                sh = R.make_paged_shape(N, 1, num_pages=8, page_size=16, table_width=1)
+                z = lambda n: torch.zeros(n, **i32)
+                a = (z(N), z(N), z(8), z(3), z((N, 1)), z(N + 1), z(N), z(1), torch.zeros(1, dtype=torch.int64, device="cuda"), z(3))
+                for _ in range(5000):
+                    R.paged_plan(sh, *a)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001  (reported by the test)
+            wrong.append((N, e))
+
+    threads = [threading.Thread(target=calls, args=(N,)) for N in (8192, 5000, 6000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
