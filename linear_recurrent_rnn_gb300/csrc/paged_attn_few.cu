@@ -264,7 +264,11 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
           if (tid < NR) {
             // below every score, and finite: so that a key that is not seen weighs 0
             const float m0 = j == j0 ? -1e30f : s_ref[tid];
-            const float m = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), m0);
+            const float top = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), m0);
+            // Rows that the tile has to spare hold other requests' queries and see stale keys: with
+            // an infinite reference they weigh nothing and never ask for a change, which would move
+            // the item's own references (and so the rounding of its weights) too.
+            const float m = tid < rows ? top : INFINITY;
             s_scale[tid] = m0 == m ? 1.0f : ta_ex2(m0 - m);
             s_ref[tid] = m;
           }

@@ -1,5 +1,5 @@
-"""The paged cache at its edges: requests and row tiles without keys in the middle of a CTA's work, and plans
-of the largest sizes.  Tolerances as in test_gpu_paged.py."""
+"""The paged cache at its edges: requests and row tiles without keys in the middle of a CTA's work, plans of
+the largest sizes, and what a request's result may not depend on.  Tolerances as in test_gpu_paged.py."""
 import os
 import subprocess
 import sys
@@ -97,3 +97,39 @@ def test_plans_of_two_sizes_from_two_threads():
     for t in threads:
         t.join()
     assert not wrong
+
+
+# ---------------------------------------------------------------- what a request's bits depend on
+# (new, all) tokens: tiles of 16, 32 and 128 rows that are not full
+UNSEEN = {"tiles-of-16": [(1, 300), (1, 77), (2, 131), (1, 20)], "tiles-of-32": [(5, 300), (4, 77), (6, 131), (5, 20)],
+          "tiles-of-128": [(20, 300), (9, 77), (30, 131), (13, 20)]}
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("name", list(UNSEEN))
+def test_unseen_values_change_no_bit(name, io):
+    """Finite values, however large, in the other requests' queries, in padding rows and in cache
+    slots past a request's length leave a request's output as it was, bit by bit."""
+    lens = UNSEEN[name]
+    x = build(lens, 8, 2, 64, 16, io, 21, spare_rows=6)
+    T = sum(q for q, _ in lens)
+    for c in ("kc", "vc"):
+        x[c] = torch.nan_to_num(x[c], nan=0.0)
+    x["q"][T:] = 0
+    o, L, _ = attend(x, 0.125)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    table = x["table"].cpu().numpy()
+    for n, (_, kv) in enumerate(lens):
+        if kv % 16:
+            for c in ("kc", "vc"):
+                stale = x[c][int(table[n, kv // 16]), kv % 16:]
+                stale.copy_(torch.randn(stale.shape, generator=g, device="cuda") * 1000)
+    x["q"][T:] = torch.randn(x["q"][T:].shape, generator=g, device="cuda").to(x["q"].dtype) * 1000
+    o2, L2, _ = attend(x, 0.125)
+    assert torch.equal(o, o2) and torch.equal(L, L2)
+    for n in range(len(lens)):
+        a, b = int(x["cu"][n]), int(x["cu"][n + 1])
+        q = x["q"] * 300
+        q[a:b] = x["q"][a:b]
+        o2, L2, _ = attend(dict(x, q=q), 0.125)
+        assert torch.equal(o[a:b], o2[a:b]) and torch.equal(L[a:b], L2[a:b])
