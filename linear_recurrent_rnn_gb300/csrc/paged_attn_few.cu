@@ -31,6 +31,8 @@
 // TB/s: 14 key tiles a CTA, of which one is a rounding loss, 3 us of start and 4 us of joining
 // parts.  One request of 1000 keys: 10.6 us, all latency: 4 us to the first product (lengths,
 // division of work, table entry, copy: each a round trip), 3 to the parts, 3 to their join.
+#include <float.h>
+
 #include <algorithm>
 
 #include "host_util.h"
@@ -262,8 +264,8 @@ __global__ void __launch_bounds__(TF_THREADS, 1)
             break;
           }
           if (tid < NR) {
-            // below every score, and finite: so that a key that is not seen weighs 0
-            const float m0 = j == j0 ? -1e30f : s_ref[tid];
+            // the lowest finite number: no score is below it, and a key that is not seen (-inf) weighs 0
+            const float m0 = j == j0 ? -FLT_MAX : s_ref[tid];
             const float top = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), m0);
             // Rows that the tile has to spare hold other requests' queries and see stale keys: with
             // an infinite reference they weigh nothing and never ask for a change, which would move

@@ -133,3 +133,21 @@ def test_unseen_values_change_no_bit(name, io):
         q[a:b] = x["q"][a:b]
         o2, L2, _ = attend(dict(x, q=q), 0.125)
         assert torch.equal(o[a:b], o2[a:b]) and torch.equal(L[a:b], L2[a:b])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 12, 40])
+def test_scores_near_the_type_s_lowest(new, io):
+    """Every score of a row far below -1e30, yet finite: with equal keys the weights are equal.  All
+    values are 3, and so is every output."""
+    x = build([(new, 64 + new)] * 2, 2, 1, 64, 16, io, 23)
+    T, w = 2 * new, 64
+    x["q"].fill_(-2.0 ** 58)
+    x["kc"] = torch.where(torch.isnan(x["kc"]), x["kc"], torch.full_like(x["kc"], 2.0 ** 58))
+    x["vc"] = torch.where(torch.isnan(x["vc"]), x["vc"], torch.full_like(x["vc"], 3.0))
+    o, L, ws = attend(x, 1.0, w)
+    assert R.rglru_sync_status(ws) == R.OK
+    score = -64.0 * 2.0 ** 116
+    assert score < -5e36
+    assert (o == 3.0).all()
+    assert ((L.double() / score - 1).abs() <= 2.0 ** -20).all()   # e of the module's tolerances, relative
