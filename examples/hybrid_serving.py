@@ -52,7 +52,8 @@ class Server:
         self.width = -(-longest // page_size)
         self.lens = torch.zeros(requests, **i32)
         self.free_pages = torch.arange(pages, **i32)              # the ring of free pages
-        self.free_state = torch.tensor([0, pages, 0], **i32)      # its head, its count, pages wanting
+        self.free_state = torch.tensor([0, pages, 0], **i32)      # its head, its count, pages wanting in the last step
+        self.wanting = torch.zeros(1, **i32)                      # and in all steps
         self.table = torch.full((requests, self.width), -1, **i32)
         self.cu = torch.zeros(requests + 1, **i32)
         self.states = [torch.zeros(requests, m.W, device="cuda") for _ in m.pairs]
@@ -78,6 +79,7 @@ class Server:
         shape, ws, positions, slots, rec, saved = self._buffers(x.shape[0], decode)
         R.paged_plan(shape, self.lens, new, self.free_pages, self.free_state, self.table, self.cu, self.lens, positions,
                      slots, self.free_state)
+        self.wanting += self.free_state[2]
         angle = positions[:, None] * torch.exp2(torch.arange(m.D // 2, device="cuda") * (-20.0 / m.D))
         cos, sin = angle.cos()[:, None], angle.sin()[:, None]
 
@@ -110,8 +112,8 @@ class Server:
 
     def check(self):
         """Raises if a step wanted pages it did not get, or a device wait ran out (synchronises)."""
-        if int(self.free_state[2]):
-            raise RuntimeError(f"the cache is short of {int(self.free_state[2])} pages")
+        if int(self.wanting):
+            raise RuntimeError(f"the cache was short of {int(self.wanting)} pages")
         for shape, ws, _, _, _, saved in self.buffers.values():
             for b in (ws,) if saved is None else (ws, saved):
                 if R.rglru_sync_status(b) != R.OK:
