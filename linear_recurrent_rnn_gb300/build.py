@@ -19,7 +19,21 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "librglru.so")
-BINDING = os.path.join(BUILD, "rglru_binding.so")
+
+
+def binding_path() -> str:
+    """The Python module's file.  It reads torch's tensors through the headers that it was compiled
+    with, so its name says which torch and which Python those are: another's is not there, rather
+    than loaded."""
+    try:
+        import torch
+        version = torch.__version__
+    except ImportError:
+        version = "-none"
+    return os.path.join(BUILD, f"rglru_binding-torch{version}-{sysconfig.get_config_var('SOABI')}.so")
+
+
+BINDING = binding_path()
 SOURCES = ["api.cu", "scan_simt.cu", "gemm_simt.cu", "noalloc.cu", "host_util.cu", "fused_fwd.cu", "fused_bwd.cu",
            "decode.cu", "varlen.cu", "delta_rule.cu", "proj_tc.cu", "paged.cu", "paged_attn_simt.cu",
            "paged_attn_tc.cu", "paged_attn_few.cu"]
