@@ -59,16 +59,29 @@ def _deps():
     return files
 
 
+def missing_headers() -> list:
+    """Headers that the Python module wants and that are not installed; the library wants none of them."""
+    want = [os.path.join(sysconfig.get_paths()["include"], "Python.h")]
+    try:
+        import torch
+        want.append(os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "autograd",
+                                 "python_variable.h"))
+    except ImportError:
+        want.append("torch/csrc/autograd/python_variable.h")
+    return [f for f in want if not os.path.exists(f)]
+
+
 def stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
+    made = [LIB] if missing_headers() else [LIB, BINDING]
+    if not all(map(os.path.exists, made)):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(map(os.path.getmtime, made))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every kernel translation unit and link librglru.so, compile the Python module;
-    returns the library's path."""
+    """Compile every kernel translation unit and link librglru.so, compile the Python module (without
+    its headers: a note instead, and the calls that need the module raise); returns the library's path."""
     if not force and not stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -101,15 +114,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         os.replace(tmp, BINDING)
 
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        module = ex.submit(compile_binding)
+        missing = missing_headers()
+        module = None if missing else ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
-        module.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)  # (there whatever becomes of the module)
+        if module:
+            module.result()
+        else:
+            sys.stderr.write(f"librglru: the Python module is not built: {', '.join(missing)} missing\n")
     return LIB
 
 
