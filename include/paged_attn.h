@@ -112,11 +112,12 @@ size_t paged_attention_workspace_bytes(const paged_shape *shape);
  *   s_j = scale q.k_j,  lse = ln sum_J exp(s_j),  o = sum_J exp(s_j - lse) v_j.
  * A token that sees nothing (p < 0: kv_lens[n] < q_n) gets o = 0 and lse = -inf.  Padding rows
  * of o and lse are not written.  o [tokens][Hq][D] by strides in shape.io; lse float32
- * [tokens][Hq], may be NULL; scale finite and > 0.  Whatever the cache holds at positions that
- * no new token sees (past kv_lens, before every window, other requests' pages) has no effect,
- * NaN and infinities included; a NaN or infinity at a position that some new token of a
- * request sees may reach other new tokens of that request.  Scores, softmax and sums are held
- * in float32; with bf16 the weights exp(s_j - max) are rounded to bf16 before they meet v.
+ * [tokens][Hq], may be NULL; scale > 0 with scale log2(e) finite, and scores are held times
+ * log2(e) (so up to 2.3e38).  Whatever the cache holds at positions that no new token sees (past
+ * kv_lens, before every window, other requests' pages) has no effect, NaN and infinities
+ * included; a NaN or infinity at a position that some new token of a request sees may reach
+ * other new tokens of that request.  Scores, softmax and sums are held in float32; with bf16 the
+ * weights exp(s_j - max) are rounded to bf16 before they meet v.
  * strides NULL: everything contiguous.  The result does not depend on timing (sums in a fixed
  * order).  A device wait that runs out marks the workspace (rglru_sync_status gives
  * RGLRU_ERR_TIMEOUT); zero it before using it again.  Tests bring that about with

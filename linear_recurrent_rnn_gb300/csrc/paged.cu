@@ -418,7 +418,8 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
   if (st == RGLRU_OK) st = check_heads(s);
   if (st == RGLRU_OK) st = check_queries(s);
   if (st != RGLRU_OK) return st;
-  if (!(scale > 0.0f) || !isfinite(scale)) return RGLRU_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.0f) || !isfinite(scale_log2)) return RGLRU_ERR_INVALID_ARG;
   if (s->tokens == 0) return RGLRU_OK;
   if (!req(q) || !req(k_cache) || !req(v_cache) || !aligned(block_table, 4) ||
       !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) || !req(o) ||
@@ -440,7 +441,7 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
   a.ps_log2 = log2_exact(s->page_size);
   a.table_width = s->table_width;
   a.window = s->window < 1 << 30 ? s->window : 0;  // (lengths are clamped to 2^30)
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.q = q;
   a.kc = k_cache;
   a.vc = v_cache;

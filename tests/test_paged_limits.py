@@ -18,3 +18,9 @@ def test_counts_that_pass_32_bits_are_refused(lib, kw):  # noqa: F811
 def test_the_largest_sizes_are_taken(lib):  # noqa: F811
     for kw in (dict(tokens=2 ** 30), dict(num_seqs=8192, table_width=2 ** 18 - 1)):
         assert R.paged_attention_workspace_bytes(shape(**kw)) > 0
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3.4028235e38])
+def test_scales_that_overflow_in_log2_units_are_refused(lib, scale):  # noqa: F811
+    """Scores are held times log2 e: such a scale would be infinite there, and every weight NaN."""
+    assert attend(lib, shape(), scale=scale) == R.ERR_INVALID_ARG
