@@ -362,8 +362,11 @@ def make_paged_shape(num_seqs, tokens, Hq=1, Hkv=1, D=8, num_pages=1, page_size=
     """Sizes of one step over a paged cache (paged_plan ignores the heads, D, io and window)."""
     if isinstance(io, torch.dtype):
         io = _DT[io]
-    return PagedShape(int(num_seqs), int(tokens), int(Hq), int(Hkv), int(D), int(num_pages),
-                      int(page_size), int(table_width), int(io), int(window))
+    sizes = [int(v) for v in (num_seqs, tokens, Hq, Hkv, D, num_pages, page_size, table_width, io, window)]
+    for (name, _), v in zip(PagedShape._fields_, sizes):
+        if not -2 ** 31 <= v < 2 ** 31:  # (ctypes would keep the low 32 bits)
+            raise ValueError(f"{name}: {v} does not fit 32 bits")
+    return PagedShape(*sizes)
 
 
 def paged_attention_workspace_bytes(shape: PagedShape) -> int:

@@ -24,3 +24,11 @@ def test_the_largest_sizes_are_taken(lib):  # noqa: F811
 def test_scales_that_overflow_in_log2_units_are_refused(lib, scale):  # noqa: F811
     """Scores are held times log2 e: such a scale would be infinite there, and every weight NaN."""
     assert attend(lib, shape(), scale=scale) == R.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", ["num_seqs", "tokens", "Hq", "Hkv", "D", "num_pages", "page_size", "table_width", "io", "window"])
+def test_sizes_beyond_32_bits_are_refused(name):
+    """Not taken for their low 32 bits (a window of 2^32 + 64 would be one of 64)."""
+    for v in (2 ** 32 + 64, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match=f"^{name}: "):
+            shape(**{name: v})
