@@ -171,7 +171,7 @@ def measured_peaks():
 # dram__bytes_write.sum from one ncu capture; writes still resident in L2 when the kernel
 # ends are not counted).  It holds for the kernel sources whose hash is recorded beside it;
 # when they have changed since, the line reports null until the counters are taken again.
-TRAFFIC = {"bytes": 70497792 + 12541952, "sources_sha16": "99e6a620ffd40735"}
+TRAFFIC = {"bytes": 70497280 + 12653056, "sources_sha16": "8fec640c468e6445"}
 KERNEL_SOURCES = ("fused_bwd.cu", "tc.cuh", "common.cuh", "lookback.cuh", "internal.h")
 
 
