@@ -19,8 +19,8 @@ namespace {
 // all have read before one writes, so they are then one cluster, which meets in between.
 // Tokens: a warp takes 32 in a row and searches the offsets for the first; the others are mostly
 // in the same request.  Latency-bound: the floor is a launch, two dependent reads (lengths, then
-// table or ring) and the writes.  Measured (GB300): 3.0 us for 8 requests, 4.8 for 512, 6.1 for 1024
-// requests with 130 000 new tokens.
+// table or ring) and the writes.  Measured (GB300): 3.0 us for 8 requests, 4.8 for 512, 6.0 for 1024
+// requests with 83 000 new tokens; the last one in place, on the cluster's 8 CTAs, 23.
 struct PlanArgs {
   int N, T, P, s, s_log2, width, cluster;
   const int32_t* cached;
@@ -258,7 +258,10 @@ rglru_status check_queries(const paged_shape* s) {
 // tokens: what the host knows of the lengths.  Every kernel is right for any lengths; the mean
 // chooses among them.  bf16, 64 requests of 500 to 4096 keys, 32 heads on 8 of 128, few-rows kernel
 // (tiles of 16 or 32 rows) against 128-row tiles: 4 rows a request 85 : 99 us, 16 rows 87 : 100,
-// 20 rows 92 : 100, 32 rows 100 : 100, 40 rows (two tiles, keys read twice) 174 : 101.
+// 20 rows 92 : 100, 32 rows 100 : 100, 40 rows (two tiles, keys read twice) 174 : 101.  These are
+// batches of equal requests; the mean serves one long chunk among many decodes badly: 255 decodes of
+// 64 to 8192 keys (292 us) and a chunk of 512 tokens on 4096 (50 us) take 561 us in one call, as the
+// chunk's keys are read for every 4 of its tokens: better two calls.
 int mean_rows(const paged_shape* s) {
   return (int)std::min<int64_t>(((int64_t)s->tokens + s->num_seqs - 1) / s->num_seqs * (s->Hq / s->Hkv), 1 << 30);
 }

@@ -25,11 +25,11 @@
 // that clears rows of V that no row sees, and one that walks the items and loads queries.
 //
 // Measured (GB300): 64 requests of 4096 keys, 16 heads of 128: 314 us, 6.7 TB/s, the copy
-// bandwidth.  256 requests of 64 to 8192 keys, 32 query heads on 8 (1.78 GB): 290 us, 6.1 TB/s;
+// bandwidth.  256 requests of 64 to 8192 keys, 32 query heads on 8 (1.78 GB): 284 us, 6.3 TB/s;
 // what is missing is the switch from item to item where they have one or two key tiles, and the
 // start.  128 requests with a window of 2048, 10 query heads of 256 on one (227 MB): 48.4 us, 4.7
 // TB/s: 14 key tiles a CTA, of which one is a rounding loss, 3 us of start and 4 us of joining
-// parts.  One request of 1000 keys: 10.6 us, all latency: 4 us to the first product (lengths,
+// parts.  One request of 1000 keys: 10.7 us, all latency: 4 us to the first product (lengths,
 // division of work, table entry, copy: each a round trip), 3 to the parts, 3 to their join.
 #include <float.h>
 
