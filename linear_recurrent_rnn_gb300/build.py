@@ -36,7 +36,7 @@ def binding_path() -> str:
 BINDING = binding_path()
 SOURCES = ["api.cu", "scan_simt.cu", "gemm_simt.cu", "noalloc.cu", "host_util.cu", "fused_fwd.cu", "fused_bwd.cu",
            "decode.cu", "varlen.cu", "delta_rule.cu", "proj_tc.cu", "paged.cu", "paged_attn_simt.cu",
-           "paged_attn_tc.cu", "paged_attn_few.cu"]
+           "paged_attn_tc.cu", "paged_attn_few.cu", "paged_pages.cu"]
 HEADERS = ["common.cuh", "internal.h", "tc.cuh", "host_util.h", "lookback.cuh",
            "paged.cuh", "paged_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -54,6 +54,7 @@ def _deps():
     files.append(os.path.join(ROOT, "include", "librglru.h"))
     files.append(os.path.join(ROOT, "include", "delta_rule.h"))
     files.append(os.path.join(ROOT, "include", "paged_attn.h"))
+    files.append(os.path.join(ROOT, "include", "paged_pages.h"))
     files.append(os.path.join(CSRC, "binding.cpp"))
     files.append(os.path.abspath(__file__))
     return files

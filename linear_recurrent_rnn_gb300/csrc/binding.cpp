@@ -16,8 +16,10 @@
 #include <cstring>
 #include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "../../include/paged_attn.h"
+#include "../../include/paged_pages.h"
 
 namespace {
 
@@ -25,6 +27,11 @@ decltype(&paged_plan) f_plan;
 decltype(&paged_kv_write) f_write;
 decltype(&paged_attention) f_attention;
 decltype(&paged_attention_workspace_bytes) f_ws_bytes;
+decltype(&paged_fork) f_fork;
+decltype(&paged_release) f_release;
+decltype(&paged_compact) f_compact;
+decltype(&paged_copy) f_copy;
+decltype(&paged_pages_workspace_bytes) f_pages_ws_bytes;
 PyObject* g_shape_type;  // the package's PagedShape
 
 // A call's arguments as they are taken one by one; after the first wrong one `ok` is false and a
@@ -92,6 +99,47 @@ struct Args {
     for (PyObject* x : {n, sizes, dtype, dev, st}) Py_XDECREF(x);
   }
 
+  int32_t* i32(const char* name, std::initializer_list<int64_t> sizes) {
+    return static_cast<int32_t*>(tensor(name, at::kInt, sizes));
+  }
+
+  // The number of rows of the next argument, 0 where it has none; it is not taken yet.
+  int64_t rows() const {
+    if (!ok || !THPVariable_Check(*at)) return 0;
+    const at::Tensor& t = THPVariable_Unpack(*at);
+    return t.dim() > 0 && t.layout() == at::kStrided ? t.size(0) : 0;
+  }
+
+  // A cache of this many pages: of any type, its pages apart from one another.
+  bool pages(PyObject* o, int64_t num_pages, void** base, int64_t* stride, int64_t* bytes) {
+    if (!ok) return false;
+    if (!THPVariable_Check(o)) {
+      PyErr_Format(PyExc_TypeError, "caches: want tensors, not %R", o);
+      return ok = false;
+    }
+    const at::Tensor& t = THPVariable_Unpack(o);
+    const bool strided = t.layout() == at::kStrided;
+    int64_t span = 1;  // elements from a page's first to its last
+    if (strided)
+      for (int64_t d = 1; d < t.dim(); ++d) span += (t.size(d) - 1) * t.stride(d);
+    if (!strided || !t.is_cuda() || t.dim() < 1 || t.size(0) != num_pages || t.numel() == 0 ||
+        (num_pages > 1 && t.stride(0) < span) || (device >= 0 && t.get_device() != device)) {
+      PyObject* n = PyObject_GetAttrString(o, "shape");
+      PyObject* dev = n ? PyObject_GetAttrString(o, "device") : nullptr;
+      if (dev)  // (else one of them has raised)
+        PyErr_Format(PyExc_ValueError, "caches: want CUDA tensors of %lld pages that lie apart, on one device, not %S on %S",
+                     (long long)num_pages, n, dev);
+      Py_XDECREF(n);
+      Py_XDECREF(dev);
+      return ok = false;
+    }
+    device = t.get_device();
+    *base = t.data_ptr();
+    *bytes = span * t.element_size();
+    *stride = num_pages > 1 ? t.stride(0) * t.element_size() : *bytes;
+    return true;
+  }
+
   // The next argument: a contiguous CUDA tensor of any type, of that many bytes or more.
   void* scratch(const char* name, size_t bytes) {
     PyObject* o = *at;
@@ -157,9 +205,7 @@ PyObject* py_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
     paged_shape s;
     if (!a.shape(&s)) return nullptr;
     const int64_t N = s.num_seqs, T = s.tokens;
-    auto i32 = [&](const char* name, std::initializer_list<int64_t> sizes) {
-      return static_cast<int32_t*>(a.tensor(name, at::kInt, sizes));
-    };
+    auto i32 = [&](const char* name, std::initializer_list<int64_t> sizes) { return a.i32(name, sizes); };
     int32_t* cached = i32("cached_lens", {N});
     int32_t* fresh = i32("new_lens", {N});
     int32_t* ring = i32("free_pages", {s.num_pages});
@@ -232,12 +278,104 @@ PyObject* py_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// setup(PagedShape, addresses of paged_plan, paged_kv_write, paged_attention and
-// paged_attention_workspace_bytes)
+PyObject* py_fork(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return call("paged_fork", n, 14, [&]() -> PyObject* {
+    Args a{args};
+    paged_shape s;
+    if (!a.shape(&s)) return nullptr;
+    const int64_t N = s.num_seqs, W = s.table_width, P = s.num_pages, M = a.rows();
+    int32_t* parents = a.i32("parents", {M});
+    int32_t* children = a.i32("children", {M});
+    int32_t* table = a.i32("block_table", {N, W});
+    int32_t* lens = a.i32("kv_lens", {N});
+    int32_t* holders = a.i32("holders", {P});
+    int32_t* ring = a.i32("free_pages", {P});
+    int32_t* state = a.i32("free_state", {3});
+    int32_t* table_out = a.i32("block_table_out", {N, W});
+    int32_t* lens_out = a.i32("kv_lens_out", {N});
+    int32_t* holders_out = a.i32("holders_out", {P});
+    int32_t* moves = a.i32("moves", {M, 2});
+    int32_t* out = a.i32("free_state_out", {3});
+    const cudaStream_t stream = a.stream();
+    if (!a.ok) return nullptr;
+    const int32_t m = M > 0x7fffffff ? -1 : (int32_t)M;
+    return launch([&] {
+      return f_fork(&s, m, parents, children, table, lens, holders, ring, state, table_out, lens_out, holders_out, moves, out, stream);
+    });
+  });
+}
+
+PyObject* py_release(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return call("paged_release", n, 12, [&]() -> PyObject* {
+    Args a{args};
+    paged_shape s;
+    if (!a.shape(&s)) return nullptr;
+    const int64_t N = s.num_seqs, W = s.table_width, P = s.num_pages;
+    int32_t* first = a.i32("first_pages", {N});
+    int32_t* end = a.i32("end_pages", {N});
+    int32_t* table = a.i32("block_table", {N, W});
+    int32_t* holders = a.i32("holders", {P});
+    int32_t* ring = a.i32("free_pages", {P});
+    int32_t* state = a.i32("free_state", {3});
+    int32_t* table_out = a.i32("block_table_out", {N, W});
+    int32_t* holders_out = a.i32("holders_out", {P});
+    int32_t* out = a.i32("free_state_out", {3});
+    void* ws = a.scratch("workspace", f_pages_ws_bytes(&s));
+    const cudaStream_t stream = a.stream();
+    if (!a.ok) return nullptr;
+    return launch([&] { return f_release(&s, first, end, table, holders, ring, state, table_out, holders_out, out, ws, stream); });
+  });
+}
+
+PyObject* py_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return call("paged_compact", n, 11, [&]() -> PyObject* {
+    Args a{args};
+    paged_shape s;
+    if (!a.shape(&s)) return nullptr;
+    const int64_t N = s.num_seqs, W = s.table_width, P = s.num_pages;
+    int32_t* lens = a.i32("kv_lens", {N});
+    int32_t* table = a.i32("block_table", {N, W});
+    int32_t* holders = a.i32("holders", {P});
+    int32_t* table_out = a.i32("block_table_out", {N, W});
+    int32_t* holders_out = a.i32("holders_out", {P});
+    int32_t* ring = a.i32("free_pages", {P});
+    int32_t* out = a.i32("free_state_out", {3});
+    int32_t* moves = a.i32("moves", {P / 2, 2});
+    void* ws = a.scratch("workspace", f_pages_ws_bytes(&s));
+    const cudaStream_t stream = a.stream();
+    if (!a.ok) return nullptr;
+    return launch([&] { return f_compact(&s, lens, table, holders, table_out, holders_out, ring, out, moves, ws, stream); });
+  });
+}
+
+// (the caches: a tuple)
+PyObject* py_copy(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return call("paged_copy", n, 4, [&]() -> PyObject* {
+    Args a{args};
+    paged_shape s;
+    if (!a.shape(&s)) return nullptr;
+    const int64_t M = a.rows();
+    int32_t* moves = a.i32("moves", {M, 2});
+    PyObject* caches = *a.at++;
+    const Py_ssize_t k = a.ok ? PyTuple_Size(caches) : 0;
+    if (k < 0) return nullptr;
+    std::vector<void*> base(k);
+    std::vector<int64_t> stride(k), bytes(k);
+    for (Py_ssize_t c = 0; c < k; ++c)
+      if (!a.pages(PyTuple_GET_ITEM(caches, c), s.num_pages, &base[c], &stride[c], &bytes[c])) return nullptr;
+    const cudaStream_t stream = a.stream();
+    if (!a.ok) return nullptr;
+    const int32_t m = M > 0x7fffffff ? -1 : (int32_t)M;
+    return launch([&] { return f_copy(&s, m, moves, (int32_t)k, base.data(), stride.data(), bytes.data(), stream); });
+  });
+}
+
+// setup(PagedShape, the addresses of the library's functions in the order of `f`)
 PyObject* py_setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return call("setup", n, 5, [&]() -> PyObject* {
-    void* f[4];
-    for (int i = 0; i < 4; ++i) {
+  constexpr int F = 9;
+  return call("setup", n, 1 + F, [&]() -> PyObject* {
+    void* f[F];
+    for (int i = 0; i < F; ++i) {
       f[i] = PyLong_AsVoidPtr(args[1 + i]);
       if (!f[i]) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "setup: a null address");
@@ -248,6 +386,11 @@ PyObject* py_setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
     f_write = reinterpret_cast<decltype(f_write)>(f[1]);
     f_attention = reinterpret_cast<decltype(f_attention)>(f[2]);
     f_ws_bytes = reinterpret_cast<decltype(f_ws_bytes)>(f[3]);
+    f_fork = reinterpret_cast<decltype(f_fork)>(f[4]);
+    f_release = reinterpret_cast<decltype(f_release)>(f[5]);
+    f_compact = reinterpret_cast<decltype(f_compact)>(f[6]);
+    f_copy = reinterpret_cast<decltype(f_copy)>(f[7]);
+    f_pages_ws_bytes = reinterpret_cast<decltype(f_pages_ws_bytes)>(f[8]);
     Py_INCREF(args[0]);
     Py_XDECREF(g_shape_type);
     g_shape_type = args[0];
@@ -262,6 +405,10 @@ PyMethodDef methods[] = {{"setup", fast(py_setup), METH_FASTCALL, nullptr},
                          {"paged_plan", fast(py_plan), METH_FASTCALL, nullptr},
                          {"paged_kv_write", fast(py_write), METH_FASTCALL, nullptr},
                          {"paged_attention", fast(py_attention), METH_FASTCALL, nullptr},
+                         {"paged_fork", fast(py_fork), METH_FASTCALL, nullptr},
+                         {"paged_release", fast(py_release), METH_FASTCALL, nullptr},
+                         {"paged_compact", fast(py_compact), METH_FASTCALL, nullptr},
+                         {"paged_copy", fast(py_copy), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "rglru_binding", nullptr, -1, methods};
 

@@ -224,23 +224,6 @@ __global__ void __launch_bounds__(WRITE_THREADS) k_paged_write(const WriteArgs a
 // ---------------------------------------------------------------- host
 int elem_bytes(const paged_shape* s) { return s->io == RGLRU_BF16 ? 2 : 4; }
 
-int log2_exact(int x) {
-  int l = 0;
-  while ((1 << l) < x) ++l;
-  return l;
-}
-
-rglru_status check_cache(const paged_shape* s) {
-  if (!s || s->num_seqs < 1 || s->tokens < 0 || s->num_pages < 1 || s->page_size < 1 ||
-      s->table_width < 1)
-    return RGLRU_ERR_INVALID_ARG;
-  if ((s->page_size & (s->page_size - 1)) || s->page_size < 8 || s->page_size > 4096 ||
-      s->num_seqs > PG_MAX_SEQS || (int64_t)s->num_pages * s->page_size > 0x7fffffffLL ||
-      s->tokens > PG_MAX_TOKENS || (int64_t)s->num_seqs * s->table_width > 0x7fffffffLL)
-    return RGLRU_ERR_UNSUPPORTED;
-  return RGLRU_OK;
-}
-
 rglru_status check_heads(const paged_shape* s) {
   if (s->Hkv < 1 || s->D < 1 || (s->io != RGLRU_F32 && s->io != RGLRU_BF16))
     return RGLRU_ERR_INVALID_ARG;
@@ -266,8 +249,6 @@ int mean_rows(const paged_shape* s) {
   return (int)std::min<int64_t>(((int64_t)s->tokens + s->num_seqs - 1) / s->num_seqs * (s->Hq / s->Hkv), 1 << 30);
 }
 
-bool aligned(const void* p, size_t n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 paged_strides strides_of(const paged_shape* s, const paged_strides* given) {
   if (given) return *given;
   paged_strides t;
@@ -286,6 +267,17 @@ bool strides_ok(const paged_shape* s, std::initializer_list<int64_t> v) {
 }
 
 }  // namespace
+
+rglru_status pg_check_cache(const paged_shape* s) {
+  if (!s || s->num_seqs < 1 || s->tokens < 0 || s->num_pages < 1 || s->page_size < 1 ||
+      s->table_width < 1)
+    return RGLRU_ERR_INVALID_ARG;
+  if ((s->page_size & (s->page_size - 1)) || s->page_size < 8 || s->page_size > 4096 ||
+      s->num_seqs > PG_MAX_SEQS || (int64_t)s->num_pages * s->page_size > 0x7fffffffLL ||
+      s->tokens > PG_MAX_TOKENS || (int64_t)s->num_seqs * s->table_width > 0x7fffffffLL)
+    return RGLRU_ERR_UNSUPPORTED;
+  return RGLRU_OK;
+}
 
 cudaError_t launch_pdl(const void* f, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                        void** args, int cluster) {
@@ -318,19 +310,19 @@ extern "C" rglru_status paged_plan(const paged_shape* s, const int32_t* cached_l
                                    const int32_t* free_state, int32_t* block_table,
                                    int32_t* cu_seqlens, int32_t* kv_lens, int32_t* positions,
                                    int64_t* slots, int32_t* free_state_out, rglru_stream stream) {
-  const rglru_status st = check_cache(s);
+  const rglru_status st = pg_check_cache(s);
   if (st != RGLRU_OK) return st;
-  if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) ||
-      !aligned(free_state, 4) || !aligned(block_table, 4) || !aligned(cu_seqlens, 4) ||
-      !aligned(kv_lens, 4) || !aligned(free_state_out, 4))
+  if (!pg_aligned(cached_lens, 4) || !pg_aligned(new_lens, 4) || !pg_aligned(free_pages, 4) ||
+      !pg_aligned(free_state, 4) || !pg_aligned(block_table, 4) || !pg_aligned(cu_seqlens, 4) ||
+      !pg_aligned(kv_lens, 4) || !pg_aligned(free_state_out, 4))
     return RGLRU_ERR_INVALID_ARG;
-  if (s->tokens > 0 && (!aligned(positions, 4) || !aligned(slots, 8))) return RGLRU_ERR_INVALID_ARG;
+  if (s->tokens > 0 && (!pg_aligned(positions, 4) || !pg_aligned(slots, 8))) return RGLRU_ERR_INVALID_ARG;
   PlanArgs a;
   a.N = s->num_seqs;
   a.T = s->tokens;
   a.P = s->num_pages;
   a.s = s->page_size;
-  a.s_log2 = log2_exact(s->page_size);
+  a.s_log2 = pg_log2(s->page_size);
   a.width = s->table_width;
   a.cached = cached_lens;
   a.fresh = new_lens;
@@ -366,11 +358,11 @@ extern "C" rglru_status paged_plan(const paged_shape* s, const int32_t* cached_l
 extern "C" rglru_status paged_kv_write(const paged_shape* s, const paged_strides* strides,
                                        const void* k, const void* v, const int64_t* slots,
                                        void* k_cache, void* v_cache, rglru_stream stream) {
-  rglru_status st = check_cache(s);
+  rglru_status st = pg_check_cache(s);
   if (st == RGLRU_OK) st = check_heads(s);
   if (st != RGLRU_OK) return st;
   if (s->tokens == 0) return RGLRU_OK;
-  if (!req(k) || !req(v) || !aligned(slots, 8) || !req(k_cache) || !req(v_cache))
+  if (!req(k) || !req(v) || !pg_aligned(slots, 8) || !req(k_cache) || !req(v_cache))
     return RGLRU_ERR_INVALID_ARG;
   const paged_strides t = strides_of(s, strides);
   if (!strides_ok(s, {t.k_token, t.k_head, t.v_token, t.v_head, t.kc_page, t.kc_token, t.kc_head,
@@ -381,7 +373,7 @@ extern "C" rglru_status paged_kv_write(const paged_shape* s, const paged_strides
   a.T = s->tokens;
   a.head_pieces = s->D * es / 16;
   a.pieces = s->Hkv * a.head_pieces;
-  a.s_log2 = log2_exact(s->page_size);
+  a.s_log2 = pg_log2(s->page_size);
   a.slots_end = (int64_t)s->num_pages * s->page_size;
   a.src[0] = static_cast<const uint8_t*>(k);
   a.src[1] = static_cast<const uint8_t*>(v);
@@ -405,7 +397,7 @@ extern "C" rglru_status paged_kv_write(const paged_shape* s, const paged_strides
 }
 
 extern "C" size_t paged_attention_workspace_bytes(const paged_shape* s) {
-  if (check_cache(s) != RGLRU_OK || check_heads(s) != RGLRU_OK || check_queries(s) != RGLRU_OK)
+  if (pg_check_cache(s) != RGLRU_OK || check_heads(s) != RGLRU_OK || check_queries(s) != RGLRU_OK)
     return 0;
   const int rows = mean_rows(s);
   if (s->io == RGLRU_F32) return paged_attn_simt_ws_bytes(s, rows);
@@ -417,16 +409,16 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
                                         const int32_t* block_table, const int32_t* cu_seqlens,
                                         const int32_t* kv_lens, float scale, void* o, float* lse,
                                         void* workspace, rglru_stream stream) {
-  rglru_status st = check_cache(s);
+  rglru_status st = pg_check_cache(s);
   if (st == RGLRU_OK) st = check_heads(s);
   if (st == RGLRU_OK) st = check_queries(s);
   if (st != RGLRU_OK) return st;
   const float scale_log2 = scale * 1.4426950408889634f;
   if (!(scale > 0.0f) || !isfinite(scale_log2)) return RGLRU_ERR_INVALID_ARG;
   if (s->tokens == 0) return RGLRU_OK;
-  if (!req(q) || !req(k_cache) || !req(v_cache) || !aligned(block_table, 4) ||
-      !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) || !req(o) ||
-      (lse && !aligned(lse, 4)) || !req(workspace))
+  if (!req(q) || !req(k_cache) || !req(v_cache) || !pg_aligned(block_table, 4) ||
+      !pg_aligned(cu_seqlens, 4) || !pg_aligned(kv_lens, 4) || !req(o) ||
+      (lse && !pg_aligned(lse, 4)) || !req(workspace))
     return RGLRU_ERR_INVALID_ARG;
   const paged_strides t = strides_of(s, strides);
   if (!strides_ok(s, {t.q_token, t.q_head, t.o_token, t.o_head, t.kc_page, t.kc_token, t.kc_head,
@@ -441,7 +433,7 @@ extern "C" rglru_status paged_attention(const paged_shape* s, const paged_stride
   a.g_inv = (65536u + a.g - 1) / a.g;
   a.D = s->D;
   a.P = s->num_pages;
-  a.ps_log2 = log2_exact(s->page_size);
+  a.ps_log2 = pg_log2(s->page_size);
   a.table_width = s->table_width;
   a.window = s->window < 1 << 30 ? s->window : 0;  // (lengths are clamped to 2^30)
   a.scale_log2 = scale_log2;

@@ -358,6 +358,15 @@ size_t paged_attn_few_ws_bytes(const paged_shape* s, int rows);
 cudaError_t launch_paged_attn_simt(PagedArgs a, int rows, cudaStream_t s);
 size_t paged_attn_simt_ws_bytes(const paged_shape* s, int rows);
 
+// Host checks that every call over a paged cache makes.
+inline int pg_log2(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+inline bool pg_aligned(const void* p, size_t n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; }
+rglru_status pg_check_cache(const paged_shape* s);
+
 // One kernel on `s` with programmatic stream serialisation (and clusters of `cluster` CTAs).  Such a
 // kernel's lifetime overlaps the one before it, which may be writing what this one reads: what
 // comes after griddep_wait are ordinary loads, none through the non-coherent path (__ldg).

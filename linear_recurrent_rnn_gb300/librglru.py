@@ -1,5 +1,5 @@
-"""Thin ctypes binding of librglru (include/librglru.h, include/delta_rule.h and
-include/paged_attn.h).
+"""Thin ctypes binding of librglru (include/librglru.h, include/delta_rule.h,
+include/paged_attn.h and include/paged_pages.h).
 
 Argument marshalling only: every function here checks that its tensors are contiguous CUDA
 tensors, passes their device pointers and the current CUDA stream to the C ABI call of the same
@@ -80,6 +80,9 @@ EXPORTS = ("rglru_status_string", "rglru_saved_bytes", "rglru_workspace_bytes",
 EXPORTS_PAGED = ("paged_plan", "paged_kv_write", "paged_attention_workspace_bytes",
                  "paged_attention")
 
+EXPORTS_PAGES = ("paged_fork", "paged_pages_workspace_bytes", "paged_release", "paged_compact",
+                 "paged_copy")
+
 # Static look-back scratch of rglru_forward_noalloc, per GPU (RGLRU_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -146,7 +149,14 @@ def lib():
             L.paged_attention_workspace_bytes.argtypes = [PS]
             L.paged_attention_workspace_bytes.restype = ctypes.c_size_t
             L.paged_attention.argtypes = [PS, ST] + [P] * 6 + [ctypes.c_float] + [P] * 4
-            for n in ("paged_plan", "paged_kv_write", "paged_attention"):
+            L.paged_fork.argtypes = [PS, ctypes.c_int32] + [P] * 13
+            L.paged_pages_workspace_bytes.argtypes = [PS]
+            L.paged_pages_workspace_bytes.restype = ctypes.c_size_t
+            L.paged_release.argtypes = [PS] + [P] * 11
+            L.paged_compact.argtypes = [PS] + [P] * 10
+            L.paged_copy.argtypes = [PS, ctypes.c_int32, P, ctypes.c_int32] + [P] * 4
+            for n in ("paged_plan", "paged_kv_write", "paged_attention", "paged_fork",
+                      "paged_release", "paged_compact", "paged_copy"):
                 getattr(L, n).restype = ctypes.c_int
             L.rglru_kernel_launches.argtypes = []
             L.rglru_kernel_launches.restype = ctypes.c_uint64
@@ -394,7 +404,8 @@ def _paged_calls():
             loader.exec_module(m)
             m.setup(PagedShape, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 L.paged_plan, L.paged_kv_write, L.paged_attention,
-                L.paged_attention_workspace_bytes)))
+                L.paged_attention_workspace_bytes, L.paged_fork, L.paged_release,
+                L.paged_compact, L.paged_copy, L.paged_pages_workspace_bytes)))
             _calls = m
     return _calls
 
@@ -430,3 +441,53 @@ def paged_attention(shape, q, k_cache, v_cache, block_table, cu_seqlens, kv_lens
         _handle(stream))
     if st:
         _check("paged_attention", st)
+
+
+def paged_pages_workspace_bytes(shape: PagedShape) -> int:
+    return int(lib().paged_pages_workspace_bytes(ctypes.byref(shape)))
+
+
+def alloc_paged_pages_workspace(shape: PagedShape, device="cuda") -> torch.Tensor:
+    """Scratch of paged_release and paged_compact, zeroed as its first use wants it; one per
+    stream."""
+    return torch.zeros(max(1, paged_pages_workspace_bytes(shape)), dtype=torch.uint8,
+                       device=device)
+
+
+def paged_fork(shape, parents, children, block_table, kv_lens, holders, free_pages, free_state,
+               block_table_out, kv_lens_out, holders_out, moves, free_state_out, stream=None):
+    """parents, children int32 [M]; moves int32 [M, 2], for paged_copy."""
+    st = (_calls or _paged_calls()).paged_fork(
+        shape, parents, children, block_table, kv_lens, holders, free_pages, free_state,
+        block_table_out, kv_lens_out, holders_out, moves, free_state_out, _handle(stream))
+    if st:
+        _check("paged_fork", st)
+
+
+def paged_release(shape, first_pages, end_pages, block_table, holders, free_pages, free_state,
+                  block_table_out, holders_out, free_state_out, workspace, stream=None):
+    """workspace from alloc_paged_pages_workspace."""
+    st = (_calls or _paged_calls()).paged_release(
+        shape, first_pages, end_pages, block_table, holders, free_pages, free_state,
+        block_table_out, holders_out, free_state_out, workspace, _handle(stream))
+    if st:
+        _check("paged_release", st)
+
+
+def paged_compact(shape, kv_lens, block_table, holders, block_table_out, holders_out, free_pages,
+                  free_state_out, moves, workspace, stream=None):
+    """moves int32 [num_pages // 2, 2], for paged_copy; workspace from
+    alloc_paged_pages_workspace."""
+    st = (_calls or _paged_calls()).paged_compact(
+        shape, kv_lens, block_table, holders, block_table_out, holders_out, free_pages,
+        free_state_out, moves, workspace, _handle(stream))
+    if st:
+        _check("paged_compact", st)
+
+
+def paged_copy(shape, moves, *caches, stream=None):
+    """Each cache [num_pages, ...], of any type and strides as long as its pages lie apart; what
+    lies between a page's elements is copied with them."""
+    st = (_calls or _paged_calls()).paged_copy(shape, moves, caches, _handle(stream))
+    if st:
+        _check("paged_copy", st)
