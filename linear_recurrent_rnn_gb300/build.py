@@ -36,9 +36,10 @@ def binding_path() -> str:
 BINDING = binding_path()
 SOURCES = ["api.cu", "scan_simt.cu", "gemm_simt.cu", "noalloc.cu", "host_util.cu", "fused_fwd.cu", "fused_bwd.cu",
            "decode.cu", "varlen.cu", "delta_rule.cu", "proj_tc.cu", "paged.cu", "paged_attn_simt.cu",
-           "paged_attn_tc.cu", "paged_attn_few.cu", "paged_pages.cu"]
+           "paged_attn_tc.cu", "paged_attn_few.cu", "paged_pages.cu", "paged_q4.cu",
+           "paged_attn_q4.cu"]
 HEADERS = ["common.cuh", "internal.h", "tc.cuh", "host_util.h", "lookback.cuh",
-           "paged.cuh", "paged_tc.cuh"]
+           "paged.cuh", "paged_tc.cuh", "paged_q4.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -55,6 +56,7 @@ def _deps():
     files.append(os.path.join(ROOT, "include", "delta_rule.h"))
     files.append(os.path.join(ROOT, "include", "paged_attn.h"))
     files.append(os.path.join(ROOT, "include", "paged_pages.h"))
+    files.append(os.path.join(ROOT, "include", "paged_q4.h"))
     files.append(os.path.join(CSRC, "binding.cpp"))
     files.append(os.path.abspath(__file__))
     return files

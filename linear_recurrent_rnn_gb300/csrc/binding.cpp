@@ -20,6 +20,7 @@
 
 #include "../../include/paged_attn.h"
 #include "../../include/paged_pages.h"
+#include "../../include/paged_q4.h"
 
 namespace {
 
@@ -32,6 +33,10 @@ decltype(&paged_release) f_release;
 decltype(&paged_compact) f_compact;
 decltype(&paged_copy) f_copy;
 decltype(&paged_pages_workspace_bytes) f_pages_ws_bytes;
+decltype(&paged_q4_write) f_q4_write;
+decltype(&paged_q4_read) f_q4_read;
+decltype(&paged_q4_attention) f_q4_attention;
+decltype(&paged_q4_attention_workspace_bytes) f_q4_ws_bytes;
 PyObject* g_shape_type;  // the package's PagedShape
 
 // A call's arguments as they are taken one by one; after the first wrong one `ok` is false and a
@@ -86,7 +91,8 @@ struct Args {
     std::string w = "(";
     for (size_t i = 0; i < want.size(); ++i) w += (i ? ", " : "") + std::to_string(want[i]);
     w += want.size() == 1 ? ",)" : ")";
-    const char* tn = type == at::kInt ? "int32" : type == at::kLong ? "int64" : type == at::kFloat ? "float32" : "bfloat16";
+    const char* tn = type == at::kInt ? "int32" : type == at::kLong ? "int64" : type == at::kFloat ? "float32" :
+                     type == at::kByte ? "uint8" : type == at::ScalarType::Float8_e4m3fn ? "float8_e4m3fn" : "bfloat16";
     PyObject* n = PyObject_GetAttrString(o, "shape");
     PyObject* sizes = n ? PySequence_Tuple(n) : nullptr;
     PyObject* dtype = sizes ? PyObject_GetAttrString(o, "dtype") : nullptr;
@@ -370,9 +376,88 @@ PyObject* py_copy(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// A cache in 4 bits, as it is passed: codes and scales of keys, then of values.
+struct Q4Arrays {
+  void* at[4];
+  bool take(Args& a, const paged_shape& s, paged_q4_strides& t) {
+    static const char* const names[4] = {"k_codes", "k_scales", "v_codes", "v_scales"};
+    int64_t* const steps[4][3] = {{&t.kc_page, &t.kc_token, &t.kc_head}, {&t.ks_page, &t.ks_token, &t.ks_head},
+                                  {&t.vc_page, &t.vc_token, &t.vc_head}, {&t.vs_page, &t.vs_token, &t.vs_head}};
+    const int64_t n[3] = {s.num_pages, s.page_size, s.Hkv};
+    for (int i = 0; i < 4; ++i) {
+      const bool scales = i & 1;
+      at[i] = a.tensor(names[i], scales ? at::ScalarType::Float8_e4m3fn : at::kByte,
+                       {s.num_pages, s.page_size, s.Hkv, s.D / (scales ? 16 : 2)}, true, steps[i]);
+      for (int d = 0; d < 3; ++d)
+        if (n[d] == 1) *steps[i][d] = 16;  // (of one element: no step is taken)
+    }
+    return a.ok;
+  }
+};
+
+template <bool WRITE>
+PyObject* py_q4_rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return call(WRITE ? "paged_q4_write" : "paged_q4_read", n, 9, [&]() -> PyObject* {
+    Args a{args};
+    paged_shape s;
+    if (!a.shape(&s)) return nullptr;
+    paged_q4_strides t = {};
+    void *k = nullptr, *v = nullptr;
+    int64_t* slots = nullptr;
+    Q4Arrays c;
+    auto rows = [&] {
+      int64_t* const ks[] = {&t.k_token, &t.k_head};
+      int64_t* const vs[] = {&t.v_token, &t.v_head};
+      k = a.tensor("k", io_type(s), {s.tokens, s.Hkv, s.D}, true, ks);
+      v = a.tensor("v", io_type(s), {s.tokens, s.Hkv, s.D}, true, vs);
+    };
+    if (WRITE) rows();
+    slots = static_cast<int64_t*>(a.tensor("slots", at::kLong, {s.tokens}));
+    c.take(a, s, t);
+    if (!WRITE) rows();
+    const cudaStream_t stream = a.stream();
+    if (!a.ok) return nullptr;
+    return launch([&] {
+      return WRITE ? f_q4_write(&s, &t, k, v, slots, c.at[0], c.at[1], c.at[2], c.at[3], stream)
+                   : f_q4_read(&s, &t, slots, c.at[0], c.at[1], c.at[2], c.at[3], k, v, stream);
+    });
+  });
+}
+
+PyObject* py_q4_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return call("paged_q4_attention", n, 14, [&]() -> PyObject* {
+    Args a{args};
+    paged_shape s;
+    if (!a.shape(&s)) return nullptr;
+    paged_q4_strides t = {};
+    int64_t* const qs[] = {&t.q_token, &t.q_head};
+    int64_t* const os[] = {&t.o_token, &t.o_head};
+    void* q = a.tensor("q", io_type(s), {s.tokens, s.Hq, s.D}, true, qs);
+    Q4Arrays c;
+    c.take(a, s, t);
+    int32_t* table = a.i32("block_table", {s.num_seqs, s.table_width});
+    int32_t* cu = a.i32("cu_seqlens", {(int64_t)s.num_seqs + 1});
+    int32_t* kv = a.i32("kv_lens", {s.num_seqs});
+    const double scale = PyFloat_AsDouble(*a.at++);
+    if (a.ok && scale == -1.0 && PyErr_Occurred()) return nullptr;
+    void* o = a.tensor("o", io_type(s), {s.tokens, s.Hq, s.D}, true, os);
+    float* lse = nullptr;
+    if (*a.at == Py_None)
+      ++a.at;
+    else
+      lse = static_cast<float*>(a.tensor("lse", at::kFloat, {s.tokens, s.Hq}));
+    void* ws = a.scratch("workspace", f_q4_ws_bytes(&s));
+    const cudaStream_t stream = a.stream();
+    if (!a.ok) return nullptr;
+    return launch([&] {
+      return f_q4_attention(&s, &t, q, c.at[0], c.at[1], c.at[2], c.at[3], table, cu, kv, static_cast<float>(scale), o, lse, ws, stream);
+    });
+  });
+}
+
 // setup(PagedShape, the addresses of the library's functions in the order of `f`)
 PyObject* py_setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  constexpr int F = 9;
+  constexpr int F = 13;
   return call("setup", n, 1 + F, [&]() -> PyObject* {
     void* f[F];
     for (int i = 0; i < F; ++i) {
@@ -391,6 +476,10 @@ PyObject* py_setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
     f_compact = reinterpret_cast<decltype(f_compact)>(f[6]);
     f_copy = reinterpret_cast<decltype(f_copy)>(f[7]);
     f_pages_ws_bytes = reinterpret_cast<decltype(f_pages_ws_bytes)>(f[8]);
+    f_q4_write = reinterpret_cast<decltype(f_q4_write)>(f[9]);
+    f_q4_read = reinterpret_cast<decltype(f_q4_read)>(f[10]);
+    f_q4_attention = reinterpret_cast<decltype(f_q4_attention)>(f[11]);
+    f_q4_ws_bytes = reinterpret_cast<decltype(f_q4_ws_bytes)>(f[12]);
     Py_INCREF(args[0]);
     Py_XDECREF(g_shape_type);
     g_shape_type = args[0];
@@ -409,6 +498,9 @@ PyMethodDef methods[] = {{"setup", fast(py_setup), METH_FASTCALL, nullptr},
                          {"paged_release", fast(py_release), METH_FASTCALL, nullptr},
                          {"paged_compact", fast(py_compact), METH_FASTCALL, nullptr},
                          {"paged_copy", fast(py_copy), METH_FASTCALL, nullptr},
+                         {"paged_q4_write", fast(py_q4_rows<true>), METH_FASTCALL, nullptr},
+                         {"paged_q4_read", fast(py_q4_rows<false>), METH_FASTCALL, nullptr},
+                         {"paged_q4_attention", fast(py_q4_attention), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "rglru_binding", nullptr, -1, methods};
 

@@ -307,4 +307,49 @@ __device__ __forceinline__ uint32_t ta_pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// ---------------------------------------------------------------- keys along the lanes, few rows (tf_)
+// Or over the softmax threads, 128 of them (named barrier 1).
+__device__ __forceinline__ bool tf_any(bool x) {
+  uint32_t y;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"((uint32_t)x)
+      : "memory");
+  return y != 0;
+}
+
+// Combines NR values over a warp's lanes in halves: lane l is left with the result of value
+// tf_column(l) in v[0].
+template <int NR, class F>
+__device__ __forceinline__ void tf_combine(float (&v)[NR], F f) {
+  const int lane = threadIdx.x & 31;
+  int n = NR;
+#pragma unroll
+  for (int bit = 16; bit; bit >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+#pragma unroll
+      for (int k = 0; k < NR / 2; ++k) {
+        if (k >= n) break;
+        const float keep = lane & bit ? v[k + n] : v[k], give = lane & bit ? v[k] : v[k + n];
+        v[k] = f(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+      }
+    } else {
+      v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
+    }
+  }
+}
+template <int NR>
+__device__ __forceinline__ int tf_column() {
+  const int lane = threadIdx.x & 31;
+  return NR == 32 ? lane : lane >> 1;
+}
+
+__device__ __forceinline__ float tf_lse(float ref, float sum) {
+  return sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+}
+
 }  // namespace rglru

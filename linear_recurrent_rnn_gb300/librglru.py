@@ -1,5 +1,5 @@
 """Thin ctypes binding of librglru (include/librglru.h, include/delta_rule.h,
-include/paged_attn.h and include/paged_pages.h).
+include/paged_attn.h, include/paged_pages.h and include/paged_q4.h).
 
 Argument marshalling only: every function here checks that its tensors are contiguous CUDA
 tensors, passes their device pointers and the current CUDA stream to the C ABI call of the same
@@ -64,6 +64,13 @@ class PagedStrides(ctypes.Structure):
                  "v_head", "kc_page", "kc_token", "kc_head", "vc_page", "vc_token", "vc_head")]
 
 
+class PagedQ4Strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("q_token", "q_head", "o_token", "o_head", "k_token", "k_head", "v_token",
+                 "v_head", "kc_page", "kc_token", "kc_head", "vc_page", "vc_token", "vc_head",
+                 "ks_page", "ks_token", "ks_head", "vs_page", "vs_token", "vs_head")]
+
+
 _lock = threading.Lock()
 _lib = None
 _calls = None
@@ -82,6 +89,9 @@ EXPORTS_PAGED = ("paged_plan", "paged_kv_write", "paged_attention_workspace_byte
 
 EXPORTS_PAGES = ("paged_fork", "paged_pages_workspace_bytes", "paged_release", "paged_compact",
                  "paged_copy")
+
+EXPORTS_Q4 = ("paged_q4_write", "paged_q4_read", "paged_q4_attention_workspace_bytes",
+              "paged_q4_attention")
 
 # Static look-back scratch of rglru_forward_noalloc, per GPU (RGLRU_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -155,8 +165,14 @@ def lib():
             L.paged_release.argtypes = [PS] + [P] * 11
             L.paged_compact.argtypes = [PS] + [P] * 10
             L.paged_copy.argtypes = [PS, ctypes.c_int32, P, ctypes.c_int32] + [P] * 4
+            ST4 = ctypes.POINTER(PagedQ4Strides)
+            L.paged_q4_write.argtypes = L.paged_q4_read.argtypes = [PS, ST4] + [P] * 8
+            L.paged_q4_attention_workspace_bytes.argtypes = [PS]
+            L.paged_q4_attention_workspace_bytes.restype = ctypes.c_size_t
+            L.paged_q4_attention.argtypes = [PS, ST4] + [P] * 8 + [ctypes.c_float] + [P] * 4
             for n in ("paged_plan", "paged_kv_write", "paged_attention", "paged_fork",
-                      "paged_release", "paged_compact", "paged_copy"):
+                      "paged_release", "paged_compact", "paged_copy", "paged_q4_write",
+                      "paged_q4_read", "paged_q4_attention"):
                 getattr(L, n).restype = ctypes.c_int
             L.rglru_kernel_launches.argtypes = []
             L.rglru_kernel_launches.restype = ctypes.c_uint64
@@ -405,7 +421,9 @@ def _paged_calls():
             m.setup(PagedShape, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 L.paged_plan, L.paged_kv_write, L.paged_attention,
                 L.paged_attention_workspace_bytes, L.paged_fork, L.paged_release,
-                L.paged_compact, L.paged_copy, L.paged_pages_workspace_bytes)))
+                L.paged_compact, L.paged_copy, L.paged_pages_workspace_bytes,
+                L.paged_q4_write, L.paged_q4_read, L.paged_q4_attention,
+                L.paged_q4_attention_workspace_bytes)))
             _calls = m
     return _calls
 
@@ -491,3 +509,53 @@ def paged_copy(shape, moves, *caches, stream=None):
     st = (_calls or _paged_calls()).paged_copy(shape, moves, caches, _handle(stream))
     if st:
         _check("paged_copy", st)
+
+
+# ---------------------------------------------------------------- paged cache in 4 bits
+
+def alloc_paged_q4_cache(shape: PagedShape, device="cuda"):
+    """(k_codes, k_scales, v_codes, v_scales): all zero, head by head, rows of codes on 16 bytes and
+    rows of scales on 4."""
+    P, s, H, D = shape.num_pages, shape.page_size, shape.Hkv, shape.D
+    rows = lambda width, pad: torch.zeros(P, H, s, -(-width // pad) * pad, dtype=torch.uint8,
+                                          device=device)
+    codes = lambda: rows(D // 2, 16)[..., :D // 2].transpose(1, 2)
+    scales = lambda: rows(D // 16, 4).view(torch.float8_e4m3fn)[..., :D // 16].transpose(1, 2)
+    return codes(), scales(), codes(), scales()
+
+
+def paged_q4_attention_workspace_bytes(shape: PagedShape) -> int:
+    return int(lib().paged_q4_attention_workspace_bytes(ctypes.byref(shape)))
+
+
+def alloc_paged_q4_workspace(shape: PagedShape, device="cuda") -> torch.Tensor:
+    """Scratch of paged_q4_attention, zeroed as its first use wants it; one per stream."""
+    return torch.zeros(max(1, paged_q4_attention_workspace_bytes(shape)), dtype=torch.uint8,
+                       device=device)
+
+
+def paged_q4_write(shape, k, v, slots, k_codes, k_scales, v_codes, v_scales, stream=None):
+    """k, v [tokens, Hkv, D]; codes uint8 [num_pages, page_size, Hkv, D / 2], scales float8_e4m3fn
+    [num_pages, page_size, Hkv, D / 16], as from alloc_paged_q4_cache; all may be strided."""
+    st = (_calls or _paged_calls()).paged_q4_write(shape, k, v, slots, k_codes, k_scales, v_codes,
+                                                   v_scales, _handle(stream))
+    if st:
+        _check("paged_q4_write", st)
+
+
+def paged_q4_read(shape, slots, k_codes, k_scales, v_codes, v_scales, k, v, stream=None):
+    """k, v [tokens, Hkv, D] receive what the slots stand for (zero for slots outside the cache)."""
+    st = (_calls or _paged_calls()).paged_q4_read(shape, slots, k_codes, k_scales, v_codes,
+                                                  v_scales, k, v, _handle(stream))
+    if st:
+        _check("paged_q4_read", st)
+
+
+def paged_q4_attention(shape, q, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens,
+                       kv_lens, scale, o, lse, workspace, stream=None):
+    """As paged_attention over a cache in 4 bits; workspace from alloc_paged_q4_workspace."""
+    st = (_calls or _paged_calls()).paged_q4_attention(
+        shape, q, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, kv_lens, scale, o,
+        lse, workspace, _handle(stream))
+    if st:
+        _check("paged_q4_attention", st)
