@@ -15,7 +15,8 @@
  *
  * Arrays.  Codes: [num_pages][page_size][Hkv][D / 2] bytes, channel 2 i in the low half of byte i;
  * scales: [num_pages][page_size][Hkv][D / 16] bytes; each by strides of pages, tokens and heads.
- * Codes lie on 16 bytes and scales on 4 bytes (base and strides).  Head by head (a head's tokens
+ * Codes lie on 16 bytes and scales on 4 bytes (base and strides); strides of pages and tokens are
+ * below 2^32 bytes.  Head by head (a head's tokens
  * of a page next to one another) is the layout that reads fastest: its copies are of whole lines.
  *
  * Supported: what paged_attention supports, with 16 <= D <= 256 a multiple of 16; else

@@ -6,21 +6,30 @@
 //   S^T = K Q^T       128 keys x the rows; S^T in TMEM, float32
 //   P^T = 2^(c S^T - c m)     one key a thread, to shared memory as f16
 //   O^T += V^T P^T    D x the rows; V read transposed by the tensor core, O^T in TMEM, float32
-// What is new is the way of keys and values to the tensor core.  Codes and scales come to shared memory
-// by cp.async, a quarter of bf16's bytes, and dequantising warps write the numbers that they stand for to
-// a second ring as f16.  A code times its scale has 6 significant bits at most, so f16 holds it
-// exactly (2^-10 to 2688).  Rows that no row of the item sees, and pages that are not there, are copied
-// as zeros (cp.async with fewer source bytes), so nothing stale reaches a product.
+// What is new is the way of keys and values to the tensor core.  Codes and scales come to shared memory by
+// cp.async, a quarter of bf16's bytes; the warpgroup that copied them writes the numbers that they stand
+// for as f16, keys to TMEM (the products' A operand, a row a lane), values to shared memory.  A code times its
+// scale has 6 significant bits at most, so f16 holds it exactly (2^-10 to 2688).  Rows that no row of the
+// item sees, and pages that are not there, are copied as zeros (cp.async with fewer source bytes), so
+// nothing stale reaches a product.
 //
 // Queries are f16 too, as the tensor core takes two operands of one type: each row is multiplied by
 // the power of two that brings its largest element to [2^14, 2^15), and its scores by the inverse.
 // bf16's 8 significant bits fit f16's 11.  float32 queries and weights are split into two f16 numbers
 // (22 bits), rows of their own in the products, added in float32.  Weights are held times 2^11, so
-// that f16's range, 2^-25 to 2^15, is used from the largest weight down; the reference m is moved when a
-// weight would pass 2^15.
+// that f16's range, 2^-25 to 2^15, is used from 2^4 times the first maximum down to 2^-36 of it; the reference m
+// is moved when a weight would pass 2^15.
 //
-// Warps: 4 softmax, 2 that copy codes, MMA issuer (one thread), one that walks the items and loads
-// queries, 8 that dequantise.
+// Warpgroups: softmax; control (a thread that issues S's products, one that issues O's, a warp that walks the
+// items, one that brings queries); 2 that bring keys and 2 that bring values, a unit each in turn.
+// Bound by instructions issued: some 965 a key tile and scheduler, 1400 cycles a tile, most of them the
+// dequantising (a pair of codes a conversion, a product of two with the scale, a store).  That is 3.6 TB/s of codes on
+// long sequences where bf16's kernel reaches 6.1 TB/s of four times the bytes.
+// Measured (GB300): 256 requests of 64 to 8192 keys, 32 heads on 8 of 128, 210 us (the kernel over bf16
+// caches: 287); 64 of 4096 keys, 16 heads on 16, 172 us (314); 152 of 16384 keys on one head, 97 us.
+// Other ways that were measured: keys from shared memory (a product of 128 x 16 x 16 takes the tensor core 39
+// cycles then, from TMEM 9); TMA and bulk copies of the codes (84 cycles a copy and SM, and a page's codes
+// are 1 KB); warps that only copy, with a barrier between them and those that dequantise (420 us).
 #include <float.h>
 
 #include <algorithm>
@@ -32,148 +41,48 @@ namespace rglru {
 
 namespace {
 
-constexpr int TQ_SOFT = 128;
-constexpr int TQ_LOAD = 64;     // threads that copy
-constexpr int TQ_DEQ = 256;     // threads that dequantise
-constexpr int TQ_THREADS = TQ_SOFT + 128 + TQ_DEQ;
+// Warpgroups: softmax; scores' and outputs' MMA, walk, queries; TQ_KEYS that bring keys, a unit each in
+// turn, TQ_VALUES that bring values.
+constexpr int TQ_KEYS = 2, TQ_VALUES = 2;
+constexpr int TQ_THREADS = 128 * (2 + TQ_KEYS + TQ_VALUES);
 constexpr size_t TQ_SMEM_MAX = 232448 - 4096;  // 227 KB less the static part
 constexpr float TQ_SHIFT = 11.0f;  // weights are held times 2^TQ_SHIFT
 constexpr float TQ_TOP = 15.0f;    // and stay below 2^TQ_TOP
+constexpr uint32_t TQ_JOIN = 4096; // bytes of the weights of parts that are joined
 
 template <int DP, int R_, bool F32_>
 struct Tq {
   static constexpr int R = R_;
   static constexpr bool F32 = F32_;
-  static constexpr int NR = F32 ? 2 * R : R;          // columns of the products
-  static constexpr int SLABS = DP / 64;
-  static constexpr int UPT = DP == 256 ? 2 : 1;       // ring units of a key (or value) tile
-  static constexpr uint32_t UB = DP == 64 ? TA_SLAB : 2 * TA_SLAB;
-  static constexpr int VROWS = TA_BN / UPT;           // rows of V in a unit
-  static constexpr int MH = DP == 256 ? 2 : 1;        // products of 128 columns of V
-  static constexpr uint32_t RB = DP / 2, SP = DP / 16;  // bytes of a row's codes, of its scales
-  static constexpr uint32_t SB = 1024 * ((TA_BN * (RB + SP) + 1023) / 1024);  // a tile's
+  static constexpr int COLS = F32 ? 2 * R : R;        // columns in use of the products
+  static constexpr int NR = COLS < 16 ? 16 : COLS;    // columns
+  // Units: 128 keys (or values) of up to 128 columns; what is copied, dequantised and multiplied at once.
+  static constexpr int UNITS = DP == 256 ? 2 : 1;     // of a tile
+  static constexpr int COL = DP / UNITS;              // columns of one
+  static constexpr int KT = R == 32 ? 1 : R == 16 || DP == 256 ? 2 : 4;  // key tiles of a step
+  static constexpr uint32_t RB = COL / 2, SP = COL / 16;  // bytes of a row's codes, of its scales
+  static constexpr uint32_t SB = 1024 * ((TA_BN * (RB + SP) + 1023) / 1024);  // a unit's
+  static constexpr uint32_t VB = TA_BN * COL * 2;     // of a unit of values as f16
   static constexpr uint32_t QSLAB = NR * 128;         // 64 columns of the rows of Q
-  static constexpr uint32_t QB = SLABS * QSLAB;
-  static constexpr int QBUF = QB <= 8192 ? 4 : 2;
+  static constexpr uint32_t QB = DP / 64 * QSLAB;
+  static constexpr int QBUF = 2;
   static constexpr uint32_t PROW = NR * 2;            // a key's weights
-  static constexpr uint32_t PB = TA_BN * PROW;
+  static constexpr uint32_t PT = TA_BN * PROW;        // a tile's
+  static constexpr uint32_t PB = KT * PT;             // a step's
   static constexpr uint32_t P_LAYOUT = NR == 16 ? tc::LAYOUT_SW32 : tc::LAYOUT_SW64;
-  static constexpr int STAGES = 3;                    // units as f16
-  static constexpr int FIT = (int)((TQ_SMEM_MAX - 1024 - QBUF * QB - 2 * PB - STAGES * UB - 1024) / SB);
-  static constexpr int COPIES = FIT < 16 ? FIT : 16;  // tiles of codes on their way
-  static constexpr uint32_t S_COL = 0, O_COL = 128;   // TMEM: S^T buffers, O^T buffers
-  static constexpr size_t smem = 1024 + STAGES * UB + (size_t)COPIES * SB + QBUF * QB + 2 * PB + 1024;
-  // slabs of 64 columns, 128-byte swizzle, a slab's rows together
-  static constexpr uint32_t K_SLAB = TA_SLAB, V_SLAB = VROWS * 128;
-  static_assert(COPIES >= 4, "shared memory");
-};
-
-__device__ __forceinline__ uint32_t tq_pack(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return reinterpret_cast<const uint32_t&>(v);
-}
-// what is left of a pair after its rounding to f16
-__device__ __forceinline__ uint32_t tq_rest(float lo, float hi, uint32_t rounded) {
-  const float2 v = __half22float2(reinterpret_cast<const __half2&>(rounded));
-  return tq_pack(lo - v.x, hi - v.y);
-}
-
-// `bytes` of 16 (or 4) copied, zeros behind them; nothing is read where it is 0.
-__device__ __forceinline__ void tq_copy16(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void tq_copy4(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
-}
-// Arrives on `bar` once this thread's copies so far are done.
-__device__ __forceinline__ void tq_copies_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
-}
-
-// A row's 16-byte pieces of codes lie where neither the copies nor the dequantising threads, a row a thread,
-// meet in a bank.
-template <class C>
-__device__ __forceinline__ uint32_t tq_code(int r, int piece) {
-  const int x = C::RB == 128 ? r & 7 : C::RB == 64 ? r >> 1 & 3 : r >> 2 & 1;
-  return r * C::RB + ((piece ^ x) << 4);
-}
-
-// Copies tiles of codes and scales into the ring, by two warps, each half of a tile's rows.
-template <class C>
-struct TqLoader {
-  const PagedArgs& a;
-  const Q4Cache& c;
-  const TaAbort& ctl;
-  uint8_t* ring;
-  uint64_t* full;
-  uint64_t* empty;
-  int* kinds;
-  int half;
-  uint32_t st = 0, ph = 1;  // next stage, parity of its `empty`
-
-  // This lane's page of key tile j, for the 8 rows from row 64 half + 8 lane on (-1: zeros).
-  __device__ __forceinline__ int page_of(const TaItem& it, int j) const {
-    const int lane = threadIdx.x & 31, pos = j * TA_BN + 64 * half + 8 * lane, pg = pos >> a.ps_log2;
-    if (j >= it.j1 || lane >= 8 || pos >= it.hi || pos + 8 <= it.lo || pg >= a.table_width) return -1;
-    const int id = a.table[(int64_t)it.n * a.table_width + pg];
-    return id >= 0 && id < a.P ? id : -1;
-  }
-  __device__ __forceinline__ bool tile(bool v, int j, int id, int h, int lo, int hi) {
-    if (!ctl.wait(&empty[st], ph)) return false;
-    const int lane = threadIdx.x & 31;
-    uint8_t* dst = ring + st * C::SB;
-    const int64_t token = v ? c.vc_token : c.kc_token, s_token = v ? c.vs_token : c.ks_token;
-    const uint8_t* codes = v ? c.vc : c.kc;
-    const uint8_t* scales = v ? c.vs : c.ks;
-    // where this lane's 8 rows begin
-    const int off = (j * TA_BN + 64 * half + 8 * lane) & ((1 << a.ps_log2) - 1);
-    const int64_t at = max(id, 0) * (v ? c.vc_page : c.kc_page) + h * (v ? c.vc_head : c.kc_head) + off * token;
-    const int64_t s_at = max(id, 0) * (v ? c.vs_page : c.ks_page) + h * (v ? c.vs_head : c.ks_head) + off * s_token;
-    constexpr int CPR = C::RB / 16, RPI = 32 / CPR;  // pieces of a row, rows of an instruction
-    const int piece = lane % CPR;
-#pragma unroll
-    for (int i = 0; i < 64 / RPI; ++i) {
-      const int r = i * RPI + lane / CPR, row = 64 * half + r, pos = j * TA_BN + row;
-      const int64_t base = __shfl_sync(0xffffffffu, at, r >> 3);
-      const bool there = __shfl_sync(0xffffffffu, id, r >> 3) >= 0 && pos >= lo && pos < hi;
-      const int bytes = there ? min(max(a.D / 2 - piece * 16, 0), 16) : 0;
-      tq_copy16(dst + tq_code<C>(row, piece), bytes ? codes + base + (r & 7) * token + piece * 16 : codes, bytes);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 32 * i + lane, row = 64 * half + r, pos = j * TA_BN + row;
-      const int64_t base = __shfl_sync(0xffffffffu, s_at, r >> 3);
-      const bool there = __shfl_sync(0xffffffffu, id, r >> 3) >= 0 && pos >= lo && pos < hi;
-#pragma unroll
-      for (int w = 0; w < (int)C::SP / 4; ++w) {
-        const int bytes = there ? min(max(a.D / 16 - 4 * w, 0), 4) : 0;
-        tq_copy4(dst + TA_BN * C::RB + row * C::SP + 4 * w, bytes ? scales + base + (r & 7) * s_token + 4 * w : scales, bytes);
-      }
-    }
-    if (half == 0 && lane == 0) {
-      kinds[st] = v;
-      tc::mbar_arrive(&full[st]);
-    }
-    tq_copies_arrive(&full[st]);
-    advance();
-    return true;
-  }
-  __device__ __forceinline__ void advance() {
-    __syncwarp();
-    if (++st == C::COPIES) {
-      st = 0;
-      ph ^= 1;
-    }
-  }
-  // No more tiles.
-  __device__ __forceinline__ void end() {
-    if (!ctl.wait(&empty[st], ph)) return;
-    if (half == 0 && (threadIdx.x & 31) == 0) {
-      kinds[st] = -1;
-      tc::mbar_arrive(&full[st]);
-    }
-    tc::mbar_arrive(&full[st]);
-  }
+  static constexpr int VBUF = DP == 256 && F32 && NR == 32 ? 2 : 3;  // units of V
+  static constexpr int FIT = (int)((TQ_SMEM_MAX - 1024 - QBUF * QB - 2 * PB - VBUF * VB - TQ_JOIN - 1024) / SB);
+  // units of codes on their way: of each warpgroup that brings them
+  static constexpr int DEPTH = FIT / (TQ_KEYS + TQ_VALUES) < 6 ? FIT / (TQ_KEYS + TQ_VALUES) : 6;
+  // TMEM: S^T buffers, O^T buffers, units of keys as f16 (a row a lane).  A step's tiles lie COLS columns
+  // apart in S^T: a product's columns beyond those in use are overwritten by the next tile's.
+  static constexpr uint32_t S_WIDTH = 64;  // of a buffer
+  static constexpr uint32_t S_COL = 0, O_COL = 128, K_COL = 256;
+  static constexpr int KBUF = 4;
+  static constexpr uint32_t V_SLAB = TA_SLAB;         // 64 columns, 128-byte swizzle
+  static constexpr size_t smem = 1024 + VBUF * VB + (size_t)(TQ_KEYS + TQ_VALUES) * DEPTH * SB + QBUF * QB + 2 * PB + TQ_JOIN + 1024;
+  static_assert(KT * COLS + NR - COLS <= S_WIDTH && 2 * UNITS * NR <= 128 && KBUF * COL / 2 <= 256, "TMEM");
+  static_assert(DEPTH >= 2, "shared memory");
 };
 
 template <int DP, int R, bool F32>
@@ -183,19 +92,21 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
   constexpr int NR = C::NR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* s_ring = smem;
-  uint8_t* s_copy = s_ring + (size_t)C::STAGES * C::UB;
-  uint8_t* s_q = s_copy + (size_t)C::COPIES * C::SB;
+  uint8_t* s_v = smem;
+  uint8_t* s_copy = s_v + (size_t)C::VBUF * C::VB;
+  uint8_t* s_q = s_copy + (size_t)(TQ_KEYS + TQ_VALUES) * C::DEPTH * C::SB;
   uint8_t* s_p = s_q + C::QBUF * C::QB;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_p + 2 * C::PB);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* c_full = empty + C::STAGES;    // [COPIES] a tile's codes are there
-  uint64_t* c_empty = c_full + C::COPIES;  // [COPIES] and have been read
-  uint64_t* q_full = c_empty + C::COPIES;  // [QBUF]
+  float2* s_join = reinterpret_cast<float2*>(s_p + 2 * C::PB);
+  uint64_t* v_full = reinterpret_cast<uint64_t*>(s_p + 2 * C::PB + TQ_JOIN);
+  uint64_t* v_empty = v_full + C::VBUF;    // [VBUF] units of V
+  uint64_t* k_full = v_empty + C::VBUF;    // [KBUF] units of K in TMEM
+  uint64_t* k_empty = k_full + C::KBUF;
+  uint64_t* q_full = k_empty + C::KBUF;    // [QBUF]
   uint64_t* q_empty = q_full + C::QBUF;    // [QBUF]
   uint64_t* s_full = q_empty + C::QBUF;    // [2] S^T of buffer b complete
-  uint64_t* p_full = s_full + 2;           // [2] P^T of buffer b written (and O^T scaled)
-  uint64_t* pv_done = p_full + 2;          // [2] the product with P^T of buffer b complete
+  uint64_t* s_empty = s_full + 2;          // [2] and read
+  uint64_t* p_full = s_empty + 2;          // [2] P^T of buffer b written (and O^T scaled)
+  uint64_t* pv_done = p_full + 2;          // [2] the products with P^T of buffer b complete
   uint64_t* o_empty = pv_done + 2;         // [2] O^T buffer read
   uint64_t* i_full = o_empty + 2;          // [TA_ITEMS] item records
   uint64_t* i_empty = i_full + TA_ITEMS;
@@ -204,24 +115,22 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
   __shared__ int64_t scratch[33];
   __shared__ TaItem s_item[TA_ITEMS];
   __shared__ uint32_t tmem_holder, s_flag, s_last;
-  __shared__ int s_kind[C::COPIES];                          // of a tile: 0 keys, 1 values, -1 no more
-  __shared__ float s_red[4][R];                              // a value a softmax warp and row
+  __shared__ __align__(16) float s_red[4][R];                // a value a softmax warp and row
   __shared__ __align__(16) float s_ref[R], s_scale[R];       // the rows' references; factors of a change
   __shared__ __align__(16) float s_factor[TA_ITEMS][R];      // of the rows' scores
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // < 0: softmax; 0, 1: copies, 2: MMA, 3: walk and queries, 4 and on: dequantising
-  const int role = warp - TQ_SOFT / 32;
-  const TaAbort ctl{&s_flag, reinterpret_cast<uint32_t*>(a.ws), a.wait_ns};
+  const int group = warp >> 2, role = warp - 4;  // warpgroup; of the second: 0, 2: MMA, 1: walk, 3: queries
+  const TqAbort ctl{&s_flag, reinterpret_cast<uint32_t*>(a.ws), (uint32_t)(a.wait_ns >> 10) + 1};
 
   // up to griddep_wait nothing touches global memory
   if (tid == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
-      tc::mbar_init(&full[i], TQ_DEQ / 32);
-      tc::mbar_init(&empty[i], 1);
+    for (int i = 0; i < C::VBUF; ++i) {
+      tc::mbar_init(&v_full[i], 4);
+      tc::mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < C::COPIES; ++i) {
-      tc::mbar_init(&c_full[i], TQ_LOAD + 1);
-      tc::mbar_init(&c_empty[i], TQ_DEQ / 32);
+    for (int i = 0; i < C::KBUF; ++i) {
+      tc::mbar_init(&k_full[i], 4);
+      tc::mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < C::QBUF; ++i) {
       tc::mbar_init(&q_full[i], 1);
@@ -229,35 +138,39 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&s_full[i], 1);
-      tc::mbar_init(&p_full[i], TQ_SOFT / 32);
+      tc::mbar_init(&s_empty[i], 4);
+      tc::mbar_init(&p_full[i], 4);
       tc::mbar_init(&pv_done[i], 1);
-      tc::mbar_init(&o_empty[i], TQ_SOFT / 32);
+      tc::mbar_init(&o_empty[i], 4);
     }
     for (int i = 0; i < TA_ITEMS; ++i) {
       tc::mbar_init(&i_full[i], 1);
-      tc::mbar_init(&i_empty[i], TQ_SOFT / 32 + 3);
+      tc::mbar_init(&i_empty[i], 4 * (1 + TQ_KEYS + TQ_VALUES) + 3);
       tc::mbar_init(&r_full[i], 1);
     }
-    tc::mbar_init(drain, 1);
+    tc::mbar_init(drain, 2);
     s_flag = 0u;
     tc::fence_barrier_init();
   }
-  if (role == 2) {
+  if (role == 0) {
     tc::tmem_alloc(&tmem_holder, 512);
     tc::tmem_relinquish();
   }
+  // columns that no row uses stay zero, of queries and of weights
+  for (uint32_t i = tid; i < (C::QBUF * C::QB + 2 * C::PB) / 16; i += TQ_THREADS)
+    reinterpret_cast<uint4*>(s_q)[i] = make_uint4(0u, 0u, 0u, 0u);
   tc::griddep_wait();
   // By the warp that holds the TMEM, not before: a CTA of the next grid that takes TMEM keeps it until
   // this grid has ended.
-  if (role == 2) tc::griddep_launch_dependents();
+  if (role == 0) tc::griddep_launch_dependents();
   PgWalk w;
   PgWalk::Found start;
   if (a.N <= PG_WARP_SEQS) {
-    if (role == 3) start = w.find_warp(a);
+    if (role == 1) start = w.find_warp(a);
   } else {
-    int64_t* prefix = reinterpret_cast<int64_t*>(s_ring);  // before the ring is in use
+    int64_t* prefix = reinterpret_cast<int64_t*>(s_v);  // before the rings are in use
     pg_scan(a, prefix, scratch);
-    if (role == 3) start = w.find(a, prefix);
+    if (role == 1) start = w.find(a, prefix);
   }
   tc::fence_proxy_async_smem();
   tc::tc_fence_before();
@@ -265,10 +178,12 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
   tc::tc_fence_after();
   const uint32_t tmem = tmem_holder;
 
-  if (role < 0) {
-    // ------------------------------------------------------------ softmax, one key a thread
+  // Registers: 768 threads x 80 at launch = 128 x (144 + 80 + 4 x 64).
+  if (group == 0) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    // ------------------------------------------------------------ softmax, a key of each tile a thread
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    uint32_t step = 0, no = 0;  // key tiles, items with an O^T so far
+    uint32_t step = 0, no = 0;  // steps, items with an O^T so far
     bool ok = true;
     for (uint32_t ni = 0;; ++ni) {
       ok = ctl.wait(&i_full[ni % TA_ITEMS], ni / TA_ITEMS & 1);
@@ -278,54 +193,87 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
       const int j0 = it.j0, j1 = it.j1;
       const int rows = min(a.tb, it.q - it.tok) * a.g;
       const int p_first = it.kv - it.q + it.tok, p_last = p_first + min(a.tb, it.q - it.tok) - 1;
-      const uint32_t ob = no & 1, t_o = lanes + C::O_COL + ob * (C::MH * NR);
-      float ref[R], l[R];  // the rows' references (scores in log2 units), this thread's sums
-#pragma unroll
-      for (int c = 0; c < R; ++c) l[c] = ref[c] = 0.0f;
-      const float* factor = s_factor[ni % TA_ITEMS];
+      const uint32_t ob = no & 1, t_o = lanes + C::O_COL + ob * (C::UNITS * NR);
+      // the rows' factors, references (scores in log2 units), this thread's sums; in pairs of rows.  Of 32
+      // rows only the sums are kept in registers.
+      constexpr bool KEEP = R <= 16;
+      float2 factors[KEEP ? R / 2 : 1], refs[KEEP ? R / 2 : 1], l[R / 2];
       ok = ctl.wait(&r_full[ni % TA_ITEMS], ni / TA_ITEMS & 1);
+      const float2* s_f2 = reinterpret_cast<const float2*>(s_factor[ni % TA_ITEMS]);
+      if (!KEEP) {
+        if (tid < R) s_ref[tid] = 0.0f;
+        tf_any(false);
+      }
+#pragma unroll
+      for (int c = 0; c < R / 2; ++c) {
+        if (KEEP) factors[c] = s_f2[c];
+        if (KEEP) refs[c] = make_float2(0.0f, 0.0f);
+        l[c] = make_float2(0.0f, 0.0f);
+      }
+      auto factor = [&](int c) { return KEEP ? factors[KEEP ? c : 0] : s_f2[c]; };
+      auto ref = [&](int c) { return KEEP ? refs[KEEP ? c : 0] : reinterpret_cast<const float2*>(s_ref)[c]; };
       bool out = false;
-      for (int j = j0; j < j1; ++j, ++step) {
+      for (int j = j0; j < j1; j += C::KT, ++step) {
         const uint32_t b = step & 1;
         ok = ctl.wait(&s_full[b], step >> 1 & 1) && ok;
         tc::tc_fence_after();
-        float x[NR];
+        float x[C::KT * C::COLS];
 #pragma unroll
-        for (int c = 0; c < NR; c += 16)
-          tc::tmem_ld16(lanes + C::S_COL + b * NR + c, *reinterpret_cast<float(*)[16]>(x + c));
+        for (int c = 0; c < C::KT * C::COLS; c += 16)
+          tc::tmem_ld16(lanes + C::S_COL + b * C::S_WIDTH + c, *reinterpret_cast<float(*)[16]>(x + c));
         tc::tmem_ld_wait();
         tc::reg_fence(x);
-        if (F32)
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s_empty[b]);
+        // scores, and those times their factors less the references (rounded once)
+        float2 z[C::KT][R / 2], y[C::KT][R / 2];
 #pragma unroll
-          for (int c = 0; c < R; ++c) x[c] += x[NR - R + c];
-        const int k0 = j * TA_BN;
-        float worst = -INFINITY;
+        for (int t = 0; t < C::KT; ++t)
 #pragma unroll
-        for (int c = 0; c < R; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(factor + c);
-          x[c] *= f.x;
-          x[c + 1] *= f.y;
-          x[c + 2] *= f.z;
-          x[c + 3] *= f.w;
-        }
-        if (k0 + TA_BN - 1 > p_first || (a.window && k0 < p_last - a.window + 1)) {
-          int p = p_first, h = 0;  // row c's position
+          for (int c = 0; c < R / 2; ++c) {
+            z[t][c] = make_float2(x[t * C::COLS + 2 * c], x[t * C::COLS + 2 * c + 1]);
+            if (F32)
+              z[t][c] = ta_add2(z[t][c], make_float2(x[t * C::COLS + (C::COLS - R) + 2 * c], x[t * C::COLS + (C::COLS - R) + 2 * c + 1]));
+            y[t][c] = ta_fma2(z[t][c], factor(c), make_float2(-ref(c).x, -ref(c).y));
+          }
+        // positions that rows do not see, and tiles past the part's last (their scores are stale)
+        const int k0 = j * TA_BN, k1 = j1 * TA_BN;
+        if (k0 + C::KT * TA_BN > min(p_first + 1, k1) || (a.window && k0 < p_last - a.window + 1)) {
+          int p = p_first, h = 0;  // the row's position
 #pragma unroll
           for (int c = 0; c < R; ++c) {
-            if (k0 + tid > p || (a.window && k0 + tid <= p - a.window)) x[c] = -INFINITY;
+            const int lo = a.window ? p - k0 - tid - a.window : -1, hi = min(p, k1 - 1) - k0 - tid;  // lo < 128 t <= hi
+#pragma unroll
+            for (int t = 0; t < C::KT; ++t) {
+              float& w = c & 1 ? y[t][c / 2].y : y[t][c / 2].x;
+              if (t * TA_BN > hi || t * TA_BN <= lo) w = -INFINITY;
+            }
             if (++h == a.g) {
               h = 0;
               ++p;
             }
           }
         }
+        float worst = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < R; ++c) worst = fmaxf(worst, x[c] - ref[c]);
-        if (tf_any(!ok || j == j0 || worst > TQ_TOP)) {
+        for (int t = 0; t < C::KT; ++t)
+#pragma unroll
+          for (int c = 0; c < R / 2; ++c) worst = ta_max3(worst, y[t][c].x, y[t][c].y);
+        if (j == j0 || tf_any(!ok || worst > TQ_TOP)) {
           // new references: the rows' maxima so far, less the shift
+          // (from the scores themselves: y has lost them where the reference was far off)
+          auto score = [&](float w, float p, float f, float m) { return w == -INFINITY ? w : fmaf(p, f, -m); };
           float v[R];
 #pragma unroll
-          for (int c = 0; c < R; ++c) v[c] = x[c];
+          for (int c = 0; c < R / 2; ++c) {
+            v[2 * c] = v[2 * c + 1] = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < C::KT; ++t) {
+              v[2 * c] = fmaxf(v[2 * c], score(y[t][c].x, z[t][c].x, factor(c).x, 0.0f));
+              v[2 * c + 1] = fmaxf(v[2 * c + 1], score(y[t][c].y, z[t][c].y, factor(c).y, 0.0f));
+            }
+          }
           tf_combine<R>(v, [](float p, float q) { return fmaxf(p, q); });
           s_red[warp][tf_column<R>()] = v[0];
           if (j > j0) ok = ctl.wait(&pv_done[b ^ 1], (step - 1) >> 1 & 1) && ok;
@@ -333,54 +281,101 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
             out = true;
             break;
           }
-          if (tid < R) {
-            // the lowest finite number: no score is below it, and a key that is not seen (-inf) weighs 0
-            const float m0 = j == j0 ? -FLT_MAX : s_ref[tid];
-            const float seen = fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid]));
-            // Rows that the tile has to spare see stale keys' zeros: with an infinite reference they weigh
-            // nothing and never ask for a change.
-            const float m = tid < rows ? fmaxf(seen - TQ_SHIFT, m0) : INFINITY;
-            s_scale[tid] = m0 == m ? 1.0f : ta_ex2(m0 - m);
-            s_ref[tid] = m;
-          }
-          tf_any(false);
+          // the lowest finite number: no score is below it, and a key that is not seen (-inf) weighs 0.
+          // Rows that the tile has to spare: with an infinite reference they weigh nothing and never ask
+          // for a change.
+          auto moved = [&](int c, float seen, float m0) { return c < rows ? fmaxf(seen - TQ_SHIFT, m0) : INFINITY; };
+          constexpr bool ALL = R <= 8;  // more rows would cost the registers that the steps need
+          float2 scale[ALL ? R / 2 : 1] = {};
+          if constexpr (ALL) {  // each thread all rows: one barrier
 #pragma unroll
-          for (int c = 0; c < R; c += 4)
-            *reinterpret_cast<float4*>(ref + c) = *reinterpret_cast<const float4*>(s_ref + c);
+            for (int c = 0; c < R; c += 4) {
+              float4 t4 = *reinterpret_cast<const float4*>(&s_red[0][c]);
+#pragma unroll
+              for (int w = 1; w < 4; ++w) {
+                const float4 u = *reinterpret_cast<const float4*>(&s_red[w][c]);
+                t4 = make_float4(fmaxf(t4.x, u.x), fmaxf(t4.y, u.y), fmaxf(t4.z, u.z), fmaxf(t4.w, u.w));
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float2 m0 = j == j0 ? make_float2(-FLT_MAX, -FLT_MAX) : refs[c / 2 + e];
+                const float2 m = make_float2(moved(c + 2 * e, e ? t4.z : t4.x, m0.x), moved(c + 2 * e + 1, e ? t4.w : t4.y, m0.y));
+                scale[c / 2 + e] = make_float2(m0.x == m.x ? 1.0f : ta_ex2(m0.x - m.x), m0.y == m.y ? 1.0f : ta_ex2(m0.y - m.y));
+                refs[c / 2 + e] = m;
+              }
+            }
+          } else {
+            if (tid < R) {
+              const float m0 = j == j0 ? -FLT_MAX : s_ref[tid];
+              const float m = moved(tid, fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), m0);
+              s_scale[tid] = m0 == m ? 1.0f : ta_ex2(m0 - m);
+              s_ref[tid] = m;
+            }
+            tf_any(false);
+            if constexpr (KEEP)
+#pragma unroll
+              for (int c = 0; c < R / 2; ++c) refs[c] = reinterpret_cast<const float2*>(s_ref)[c];
+          }
+          auto factor_of = [&](int c) { return ALL ? scale[ALL ? c : 0] : reinterpret_cast<const float2*>(s_scale)[c]; };
+#pragma unroll
+          for (int c = 0; c < R / 2; ++c)
+#pragma unroll
+            for (int t = 0; t < C::KT; ++t)
+              y[t][c] = make_float2(score(y[t][c].x, z[t][c].x, factor(c).x, ref(c).x), score(y[t][c].y, z[t][c].y, factor(c).y, ref(c).y));
           if (j > j0) {
             tc::tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < R; ++c) l[c] *= s_scale[c];
-#pragma unroll 1
-            for (int c = 0; c < C::MH * NR; c += 4) {
+            for (int c = 0; c < R / 2; ++c) l[c] = make_float2(l[c].x * factor_of(c).x, l[c].y * factor_of(c).y);
+            auto rescale = [&](uint32_t at, float2 f0, float2 f1) {
               float o[4];
-              tc::tmem_ld4(t_o + c, o);
+              tc::tmem_ld4(at, o);
               tc::tmem_ld_wait();
               tc::reg_fence(o);
+              o[0] *= f0.x;
+              o[1] *= f0.y;
+              o[2] *= f1.x;
+              o[3] *= f1.y;
+              tc::tmem_st4(at, o);
+            };
+#pragma unroll 1
+            for (int hm = 0; hm < C::UNITS; ++hm) {
+              if constexpr (ALL) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] *= s_scale[c % R + e];
-              tc::tmem_st4(t_o + c, o);
+                for (int c = 0; c < C::COLS; c += 4) rescale(t_o + hm * NR + c, factor_of(c % R / 2), factor_of(c % R / 2 + 1));
+              } else {
+#pragma unroll 1
+                for (int c = 0; c < C::COLS; c += 4) {
+                  const float2* f = reinterpret_cast<const float2*>(s_scale) + c % R / 2;
+                  rescale(t_o + hm * NR + c, f[0], f[1]);
+                }
+              }
             }
             tc::tmem_st_wait();
           }
         }
-        uint32_t pk[NR / 2];
-#pragma unroll
-        for (int c = 0; c < R; c += 2) {
-          const float p0 = ta_ex2(x[c] - ref[c]), p1 = ta_ex2(x[c + 1] - ref[c + 1]);
-          l[c] += p0;
-          l[c + 1] += p1;
-          pk[c / 2] = tq_pack(p0, p1);
-          if (F32) pk[(NR - R + c) / 2] = tq_rest(p0, p1, pk[c / 2]);
-        }
         ok = ctl.wait(&pv_done[b], (step >> 1 & 1) ^ 1) && ok;  // P^T of two steps ago is used up
-        // key tid's row of P^T: 16-byte pieces where the tensor core's swizzle has them
-        uint8_t* row = s_p + b * C::PB + tid * C::PROW;
-        const int sw = NR == 16 ? tid >> 2 & 1 : tid >> 1 & 3;
 #pragma unroll
-        for (int c = 0; c < NR / 8; ++c)
-          *reinterpret_cast<uint4*>(row + ((c ^ sw) << 4)) =
-              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        for (int t = 0; t < C::KT; ++t) {
+          uint32_t pk[C::COLS / 2];
+#pragma unroll
+          for (int c = 0; c < R / 2; ++c) {
+            const float2 w = make_float2(ta_ex2(y[t][c].x), ta_ex2(y[t][c].y));
+            l[c] = ta_add2(l[c], w);
+            pk[c] = tq_pack(w.x, w.y);
+            if (F32) pk[(C::COLS - R) / 2 + c] = tq_rest(w.x, w.y, pk[c]);
+          }
+          // the key's row of P^T: 16-byte pieces where the tensor core's swizzle has them
+          uint8_t* row = s_p + b * C::PB + t * C::PT + tid * C::PROW;
+          const int sw = NR == 16 ? tid >> 2 & 1 : tid >> 1 & 3;
+          if constexpr (C::COLS == 4) {
+            *reinterpret_cast<uint2*>(row + (sw << 4)) = make_uint2(pk[0], pk[1]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < C::COLS / 8; ++c)
+              *reinterpret_cast<uint4*>(row + ((c ^ sw) << 4)) =
+                  make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          }
+        }
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
         __syncwarp();
@@ -389,8 +384,19 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
       if (out) break;
       const bool any = j1 > j0;
       // the rows' sums over the threads
-      tf_combine<R>(l, [](float p, float q) { return p + q; });
-      s_red[warp][tf_column<R>()] = l[0];
+      {
+        float v[R];
+#pragma unroll
+        for (int c = 0; c < R / 2; ++c) {
+          v[2 * c] = l[c].x;
+          v[2 * c + 1] = l[c].y;
+        }
+        tf_combine<R>(v, [](float p, float q) { return p + q; });
+        s_red[warp][tf_column<R>()] = v[0];
+        if (R <= 8 && tid == 0)
+#pragma unroll
+          for (int c = 0; c < R / 2; ++c) reinterpret_cast<float2*>(s_ref)[c] = ref(c);
+      }
       if (any) {
         ok = ctl.wait(&pv_done[(step - 1) & 1], (step - 1) >> 1 & 1) && ok;
         tc::tc_fence_after();
@@ -415,15 +421,15 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < rows; c += 4) {
           __syncwarp();  // (TMEM is read by whole warps)
-          float o[C::MH][4], o2[C::MH][4];
+          float o[C::UNITS][4], o2[C::UNITS][4];
 #pragma unroll
-          for (int hm = 0; hm < C::MH; ++hm) {
+          for (int hm = 0; hm < C::UNITS; ++hm) {
             if (any) tc::tmem_ld4(t_o + hm * NR + c, o[hm]);
-            if (any && F32) tc::tmem_ld4(t_o + hm * NR + R + c, o2[hm]);
+            if (any && F32) tc::tmem_ld4(t_o + hm * NR + (C::COLS - R) + c, o2[hm]);
           }
           if (any) tc::tmem_ld_wait();
 #pragma unroll
-          for (int hm = 0; hm < C::MH; ++hm) {
+          for (int hm = 0; hm < C::UNITS; ++hm) {
             tc::reg_fence(o[hm]);
             if (F32) {
               tc::reg_fence(o2[hm]);
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
             if (whole) {
               const float sum = row_sum(c + e), inv = __fdividef(1.0f, sum);
 #pragma unroll
-              for (int hm = 0; hm < C::MH; ++hm) {
+              for (int hm = 0; hm < C::UNITS; ++hm) {
                 const float y = sum == 0.0f ? 0.0f : o[hm][e] * inv;
                 if (hm * 128 + tid >= a.D) continue;
                 if (F32)
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
               }
             } else if (any) {
 #pragma unroll
-              for (int hm = 0; hm < C::MH; ++hm)
+              for (int hm = 0; hm < C::UNITS; ++hm)
                 if (hm * 128 + tid < DP) po[(c + e) * DP + hm * 128] = o[hm][e];
             }
           }
@@ -470,14 +476,13 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
         }
         tf_any(false);
         if (s_last) {
-          // The item's last CTA joins its parts, up to PARTS at a time: first their weights (in the
-          // buffers of P^T, which nothing uses now), then the sums, a thread four columns of every
-          // RP-th row.
+          // The item's last CTA joins its parts, up to PARTS at a time: first their weights, then the
+          // sums, a thread four columns of every RP-th row.
           __threadfence();
-          float2* wt = reinterpret_cast<float2*>(s_p);  // [part][row]
-          constexpr int PARTS = 2 * C::PB / (R * 8), RP = 512 / DP, PASSES = R / RP;
+          float2* wt = s_join;  // [part][row]
+          constexpr int PARTS = TQ_JOIN / (R * 8), RP = 512 / DP, PASSES = R < RP ? 1 : R / RP;
           constexpr int BATCH = PASSES >= 16 ? 1 : 16 / PASSES;  // parts loaded at once
-          const int col = tid % (DP / 4) * 4, r0 = tid / (DP / 4);
+          const int col = tid % (DP / 4) * 4, r0 = min(tid / (DP / 4), R - 1);
           float4 o[PASSES];
 #pragma unroll
           for (int k = 0; k < PASSES; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
             };
             load(0);
 #pragma unroll 1
-            for (int i = tid; i < nq * R; i += TQ_SOFT)
+            for (int i = tid; i < nq * R; i += 128)
               wt[i] = i % R < rows ? __ldcg(reinterpret_cast<const float2*>(a.ws + a.part_ml) +
                                             (size_t)PgWalk::slot(q0 + i / R, it.c0) * R + i % R)
                                    : make_float2(0.0f, 0.0f);
@@ -546,7 +551,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
 #pragma unroll
           for (int k = 0; k < PASSES; ++k) {
             const int r = r0 + k * RP;
-            if (r >= rows || col >= a.D) continue;
+            if (r >= rows || col >= a.D || tid / (DP / 4) >= R) continue;
             const float sum_r = s_ref[r], inv = sum_r == 0.0f ? 0.0f : __fdividef(1.0f, sum_r);
             const int tok = pg_token(a, r);
             const int64_t dst = (int64_t)(tok0 + tok) * a.o_token + (int64_t)(it.h * a.g + r - tok * a.g) * a.o_head + col;
@@ -564,93 +569,65 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
         tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
       }
     }
-  } else if (role < 2) {
-    // ------------------------------------------------------------ codes and scales
-    TqLoader<C> ld{a, cache, ctl, s_copy, c_full, c_empty, s_kind, role};
-    bool ok = true, pend = false;
-    int pj = 0, pid = 0, ph = 0, plo = 0, phi = 0;  // the values still to be loaded
-    for (uint32_t ni = 0; ok; ++ni) {
-      ok = ctl.wait(&i_full[ni % TA_ITEMS], ni / TA_ITEMS & 1);
-      if (!ok) break;
-      TaItem it = s_item[ni % TA_ITEMS];
-      if (it.n < 0) break;
-      it.h /= cache.split;
+  } else if (group >= 2 && group < 2 + TQ_KEYS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // ------------------------------------------------------------ keys: a row a thread, to its lane of TMEM
+    const int r = tid & 127, g = group - 2;
+    const uint32_t lanes = tmem + ((uint32_t)(r & ~31) << 16) + C::K_COL;
+    TqStream<C, TQ_KEYS, 0> str{a, cache, ctl, s_item, i_full, i_empty, s_copy + g * C::DEPTH * C::SB, (uint32_t)g};
+    uint32_t s = g;  // unit
+    for (int st = 0; str.issue(st); st = st + 1 == C::DEPTH ? 0 : st + 1) {
+      if (!str.come()) continue;
+      const uint32_t kb = s % C::KBUF;
+      if (!ctl.wait(&k_empty[kb], (s / C::KBUF & 1) ^ 1)) break;
+      tc::tc_fence_after();
+      const uint8_t* src = s_copy + (g * C::DEPTH + (st + 1 == C::DEPTH ? 0 : st + 1)) * C::SB;
+      tq_row<C>(src, r, [&](int p, const uint32_t (&y)[16]) {
+        tc::tmem_st16(lanes + kb * (C::COL / 2) + p * 16, *reinterpret_cast<const float(*)[16]>(y));
+      });
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
-      if (it.j1 <= it.j0 && pend) {  // (as the MMA issuer does)
-        ok = ld.tile(true, pj, pid, ph, plo, phi);
-        pend = false;
-      }
-      int id = ld.page_of(it, it.j0);
-      for (int j = it.j0; j < it.j1 && ok; ++j) {
-        const int id_next = ld.page_of(it, j + 1);
-        ok = ld.tile(false, j, id, it.h, it.lo, it.hi);
-        if (pend) ok = ok && ld.tile(true, pj, pid, ph, plo, phi);
-        pend = true;
-        pj = j;
-        pid = id;
-        ph = it.h;
-        plo = it.lo;
-        phi = it.hi;
-        id = id_next;
-      }
+      if (lane == 0) tc::mbar_arrive(&k_full[kb]);
+      s += TQ_KEYS;
     }
-    if (pend && ok) ok = ld.tile(true, pj, pid, ph, plo, phi);
-    if (ok) ld.end();
     asm volatile("cp.async.wait_all;" ::: "memory");  // none is in flight when the CTA leaves
-  } else if (role == 2) {
-    // ------------------------------------------------------------ MMA issuer: one thread
+  } else if (group >= 2 + TQ_KEYS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // ------------------------------------------------------------ values: to shared memory
+    const int r = tid & 127, g = group - 2 - TQ_KEYS;
+    uint8_t* ring = s_copy + (TQ_KEYS + g) * C::DEPTH * C::SB;
+    uint32_t o[4];  // where the row's 16-byte pieces lie
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] = (c ^ (r & 7)) << 4;
+    TqStream<C, TQ_VALUES, 1> str{a, cache, ctl, s_item, i_full, i_empty, ring, (uint32_t)g};
+    uint32_t s = g;  // unit
+    for (int st = 0; str.issue(st); st = st + 1 == C::DEPTH ? 0 : st + 1) {
+      if (!str.come()) continue;
+      const uint32_t vb = s % C::VBUF;
+      if (!ctl.wait(&v_empty[vb], (s / C::VBUF & 1) ^ 1)) break;
+      const uint8_t* src = ring + (st + 1 == C::DEPTH ? 0 : st + 1) * C::SB;
+      uint8_t* line = s_v + vb * C::VB + r * 128;
+      tq_row<C>(src, r, [&](int p, const uint32_t (&y)[16]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(line + p / 2 * C::V_SLAB + (o[c] ^ (p & 1) << 6)) = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+      });
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&v_full[vb]);
+      s += TQ_VALUES;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (role == 0) {
+    // ------------------------------------------------------------ S^T = K Q^T: one thread
+    // The two kinds of products have a thread each, which sleeps where what it needs is not there: one
+    // thread that looked for either took a quarter of the SM's issue slots.
     if (tc::elect_one()) {
       constexpr uint32_t id_s = tc::idesc_f16(128, NR, 0, 0);
-      constexpr uint32_t id_o = tc::idesc_f16(128, NR, 1, 1);
-      const uint64_t d_k = tc::smem_desc(tc::smem_u32(s_ring), 16, 1024, tc::LAYOUT_SW128);
       const uint64_t d_q = tc::smem_desc(tc::smem_u32(s_q), 16, 1024, tc::LAYOUT_SW128);
-      // V^T: 64 columns a slab; D <= 64 has one, read twice for the 128 rows of the product
-      const uint64_t d_v = tc::smem_desc(tc::smem_u32(s_ring), DP == 64 ? 0 : C::V_SLAB, 1024, tc::LAYOUT_SW128);
-      const uint64_t d_p = tc::smem_desc(tc::smem_u32(s_p), 16, 8 * C::PROW, C::P_LAYOUT);
-      uint32_t st = 0, par = 0;   // next ring unit, parity of its `full`
-      uint32_t step = 0, nq = 0;  // S^T begun; items with keys
-      bool ok = true, pend = false;
-      struct {
-        uint32_t step, item;
-        bool first;
-      } pv = {};
-      // (a unit's arrival is waited for where it is used)
-      auto take = [&](uint32_t (&at)[C::UPT], uint32_t (&arr)[C::UPT]) {
-#pragma unroll
-        for (int u = 0; u < C::UPT; ++u) {
-          at[u] = st;
-          arr[u] = par;
-          if (++st == C::STAGES) {
-            st = 0;
-            par ^= 1;
-          }
-        }
-      };
-      auto product = [&] {  // O^T += V^T P^T of the step before
-        uint32_t at[C::UPT], arr[C::UPT];
-        take(at, arr);
-        const uint32_t b = pv.step & 1, ob = pv.item & 1;
-        ok = ok && ctl.wait1(&p_full[b], pv.step >> 1 & 1);
-        if (pv.first) ok = ok && ctl.wait1(&o_empty[ob], (pv.item >> 1 & 1) ^ 1);
-        if (!ok) return;
-        tc::tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < TA_BN / 16; ++k) {
-          if (k * 16 % C::VROWS == 0) {
-            ok = ctl.wait1(&full[at[k * 16 / C::VROWS]], arr[k * 16 / C::VROWS]);
-            if (!ok) return;
-            tc::tc_fence_after();
-          }
-#pragma unroll
-          for (int hm = 0; hm < C::MH; ++hm)
-            tc::mma_bf16(tmem + C::O_COL + (ob * C::MH + hm) * NR,
-                         d_v + ((at[k * 16 / C::VROWS] * C::UB + 2 * hm * C::V_SLAB + k % (C::VROWS / 16) * 2048) >> 4),
-                         d_p + ((b * C::PB + k * 16 * C::PROW) >> 4), id_o, k > 0 ? 1u : (uint32_t)!pv.first);
-          if ((k + 1) * 16 % C::VROWS == 0) tc::mma_commit(&empty[at[k * 16 / C::VROWS]]);
-        }
-        tc::mma_commit(&pv_done[b]);
-      };
+      uint32_t ks = 0, step = 0, nq = 0;  // units of K used, steps, items with keys
+      bool ok = true;
       for (uint32_t ni = 0; ok; ++ni) {
         ok = ctl.wait1(&i_full[ni % TA_ITEMS], ni / TA_ITEMS & 1);
         if (!ok) break;
@@ -658,47 +635,81 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
         if (it.n < 0) break;
         const int j0 = it.j0, j1 = it.j1;
         tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
-        if (j1 <= j0 && pend) {  // no step to wait for: items without keys may follow one another
-          product();
-          pend = false;
-        }
+        if (j1 <= j0) continue;
         const uint32_t qb = nq % C::QBUF;
-        for (int j = j0; j < j1 && ok; ++j, ++step) {
-          uint32_t at[C::UPT], arr[C::UPT];
-          take(at, arr);
-          if (j == j0) ok = ok && ctl.wait1(&q_full[qb], nq / C::QBUF & 1);
-          if (!ok) break;
-          tc::tc_fence_after();
+        ok = ctl.wait1(&q_full[qb], nq / C::QBUF & 1);
+        ++nq;
+        for (int j = j0; j < j1 && ok; j += C::KT, ++step) {
           const uint32_t b = step & 1;
+          ok = ctl.wait1(&s_empty[b], (step >> 1 & 1) ^ 1);
+          const int kt = min(C::KT, j1 - j);
+#pragma unroll 1
+          for (int t = 0; t < kt && ok; ++t)
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            if (k % 8 == 0) {
-              ok = ctl.wait1(&full[at[k / 8]], arr[k / 8]);
+            for (int u = 0; u < C::UNITS; ++u, ++ks) {
+              const uint32_t kb = ks % C::KBUF;
+              ok = ok && ctl.wait1(&k_full[kb], ks / C::KBUF & 1);
               if (!ok) break;
               tc::tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < C::COL / 16; ++k)
+                tc::mma_ts(tmem + C::S_COL + b * C::S_WIDTH + t * C::COLS, tmem + C::K_COL + kb * (C::COL / 2) + k * 8,
+                           d_q + ((qb * C::QB + (u * C::COL / 64 + k / 4) * C::QSLAB + k % 4 * 32) >> 4), id_s, u > 0 || k > 0);
+              tc::mma_commit(&k_empty[kb]);
             }
-            tc::mma_bf16(tmem + C::S_COL + b * NR,
-                         d_k + ((at[k / 8] * C::UB + k % 8 / 4 * C::K_SLAB + k % 4 * 32) >> 4),
-                         d_q + ((qb * C::QB + k / 4 * C::QSLAB + k % 4 * 32) >> 4), id_s, k > 0);
-            if (k % 8 == 7 || k == DP / 16 - 1) tc::mma_commit(&empty[at[k / 8]]);
-          }
           if (!ok) break;
           tc::mma_commit(&s_full[b]);
-          if (j == j1 - 1) tc::mma_commit(&q_empty[qb]);
-          if (pend) product();
-          pend = true;
-          pv.step = step;
-          pv.item = nq;
-          pv.first = j == j0;
+          if (j + C::KT >= j1) tc::mma_commit(&q_empty[qb]);
         }
-        nq += j1 > j0;
       }
-      if (pend && ok) product();
-      tc::mma_commit(drain);  // arrives when all MMAs are done
+      tc::mma_commit(drain);  // arrives when all of this thread's products are done
     }
-  } else if (role == 3) {
-    // ------------------------------------------------------------ walk, and queries
-    uint32_t n = 0;  // items with keys
+  } else if (role == 2) {
+    // ------------------------------------------------------------ O^T += V^T P^T: one thread
+    if (tc::elect_one()) {
+      constexpr uint32_t id_o = tc::idesc_f16(128, NR, 1, 1);
+      // V^T: 64 columns a slab; D <= 64 has one, read twice for the 128 rows of the product
+      const uint64_t d_v = tc::smem_desc(tc::smem_u32(s_v), DP == 64 ? 0 : C::V_SLAB, 1024, tc::LAYOUT_SW128);
+      const uint64_t d_p = tc::smem_desc(tc::smem_u32(s_p), 16, 8 * C::PROW, C::P_LAYOUT);
+      uint32_t vn = 0, step = 0, no = 0;  // units of V used, steps, items with keys
+      bool ok = true;
+      for (uint32_t ni = 0; ok; ++ni) {
+        ok = ctl.wait1(&i_full[ni % TA_ITEMS], ni / TA_ITEMS & 1);
+        if (!ok) break;
+        const TaItem& it = s_item[ni % TA_ITEMS];
+        if (it.n < 0) break;
+        const int j0 = it.j0, j1 = it.j1;
+        tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
+        if (j1 <= j0) continue;
+        const uint32_t ob = no & 1;
+        ok = ctl.wait1(&o_empty[ob], (no >> 1 & 1) ^ 1);
+        ++no;
+        uint32_t more = 0;  // not the item's first product
+        for (int j = j0; j < j1 && ok; j += C::KT, ++step) {
+          const uint32_t b = step & 1;
+          ok = ctl.wait1(&p_full[b], step >> 1 & 1);
+          const int kt = min(C::KT, j1 - j);
+#pragma unroll 1
+          for (int t = 0; t < kt && ok; ++t, more = 1)
+#pragma unroll
+            for (int u = 0; u < C::UNITS; ++u, ++vn) {
+              const uint32_t vb = vn % C::VBUF;
+              ok = ok && ctl.wait1(&v_full[vb], vn / C::VBUF & 1);
+              if (!ok) break;
+              tc::tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < TA_BN / 16; ++k)
+                tc::mma_bf16(tmem + C::O_COL + (ob * C::UNITS + u) * NR, d_v + ((vb * C::VB + k * 2048) >> 4),
+                             d_p + ((b * C::PB + t * C::PT + k * 16 * C::PROW) >> 4), id_o, k > 0 ? 1u : more);
+              tc::mma_commit(&v_empty[vb]);
+            }
+          if (ok) tc::mma_commit(&pv_done[b]);
+        }
+      }
+      tc::mma_commit(drain);
+    }
+  } else if (role == 1) {
+    // ------------------------------------------------------------ walk
     bool more = w.enter(a, start);
     bool ok = true;
     for (uint32_t ni = 0; ok; ++ni) {
@@ -725,12 +736,23 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
       }
       __syncwarp();
       if (!more) break;
+      more = w.next(a);
+    }
+  } else if (role == 3) {
+    // ------------------------------------------------------------ queries
+    uint32_t n = 0;  // items with keys
+    bool ok = true;
+    for (uint32_t ni = 0; ok; ++ni) {
+      ok = ctl.wait(&i_full[ni % TA_ITEMS], ni / TA_ITEMS & 1);
+      if (!ok) break;
+      const TaItem x = s_item[ni % TA_ITEMS];
+      if (x.n < 0) break;
       if (x.j1 > x.j0) {
         // Queries: LPR lanes a row, 8 channels a lane.
         const uint32_t qb = n % C::QBUF;
         ok = ctl.wait(&q_empty[qb], (n / C::QBUF & 1) ^ 1);
         if (!ok) break;
-        constexpr int LPR = DP / 8, RPP = 32 / LPR, PASSES = R / RPP, BATCH = PASSES < 4 ? PASSES : 4;
+        constexpr int LPR = DP / 8, RPP = 32 / LPR, PASSES = R < RPP ? 1 : R / RPP, BATCH = PASSES < 4 ? PASSES : 4;
         const int c0 = lane % LPR * 8, rows = min(a.tb, x.q - x.tok) * a.g;
         uint8_t* dst = s_q + qb * C::QB + c0 / 64 * C::QSLAB;
 #pragma unroll 1
@@ -774,9 +796,10 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
               hi[k] = tq_pack(y0, y1);
               lo[k] = F32 ? tq_rest(y0, y1, hi[k]) : 0u;
             }
-            uint8_t* at = dst + r * 128 + ((c0 / 8 % 8 ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (F32) *reinterpret_cast<uint4*>(at + R * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (r >= R) continue;
+            *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 / 8 % 8 ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (F32)
+              *reinterpret_cast<uint4*>(dst + (r + R) * 128 + ((c0 / 8 % 8 ^ ((r + R) & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (lane % LPR == 0)
               s_factor[ni % TA_ITEMS][r] = fminf(a.scale_log2 * __uint_as_float((uint32_t)max(ex - 14 + 127, 1) << 23), FLT_MAX);
           }
@@ -786,69 +809,10 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
         if (lane == 0) tc::mbar_arrive(&q_full[qb]);
         ++n;
       }
-      if (lane == 0) tc::mbar_arrive(&r_full[ni % TA_ITEMS]);
       __syncwarp();
-      more = w.next(a);
-    }
-  } else {
-    // ------------------------------------------------------------ dequantising, a row a thread
-    const int t = tid - TQ_SOFT - 128;
-    uint32_t cst = 0, cpar = 0;  // next tile of codes, parity of its `full`
-    uint32_t st = 0, par = 1;    // next unit, parity of its `empty`
-    for (bool ok = true; ok;) {
-      ok = ctl.wait_long(&c_full[cst], cpar);
-      if (!ok) break;
-      const int v = s_kind[cst];
-      if (v < 0) break;
-      const uint8_t* src = s_copy + cst * C::SB;
-#pragma unroll 1
-      for (int u = 0; u < C::UPT && ok; ++u) {
-        // this thread's row, and its pieces of 32 channels
-        constexpr int PPT = DP == 64 ? 1 : 2;
-        const bool deep = C::UPT == 2 && v;
-        const int r = deep ? 64 * u + (t & 63) : t & 127;
-        const int p0 = deep ? (t >> 6) * 2 : (t >> 7) * PPT + (C::UPT == 2 ? 4 * u : 0);
-        uint4 codes[PPT];
-        uint32_t two[PPT];
-#pragma unroll
-        for (int e = 0; e < PPT; ++e) {
-          codes[e] = *reinterpret_cast<const uint4*>(src + tq_code<C>(r, p0 + e));
-          two[e] = *reinterpret_cast<const uint16_t*>(src + TA_BN * C::RB + r * C::SP + (p0 + e) * 2);
-        }
-        ok = ctl.wait(&empty[st], par);
-        if (!ok) break;
-        uint8_t* dst = s_ring + st * C::UB;
-#pragma unroll
-        for (int e = 0; e < PPT; ++e) {
-          const int p = p0 + e - (!deep && C::UPT == 2 ? 4 * u : 0);  // within the unit
-          const int row = deep ? r - 64 * u : r;
-          uint8_t* line = dst + p / 2 * (deep ? C::V_SLAB : C::K_SLAB) + row * 128;
-          const uint32_t s2 = q4_scales(two[e]);
-          const uint32_t s_lo = __byte_perm(s2, s2, 0x1010), s_hi = __byte_perm(s2, s2, 0x3232);
-          const uint32_t word[4] = {codes[e].x, codes[e].y, codes[e].z, codes[e].w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t y[4];
-            q4_pairs(word[c], y);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = q4_mul2(y[k], c < 2 ? s_lo : s_hi);
-            *reinterpret_cast<uint4*>(line + ((((p & 1) * 4 + c) ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(&full[st]);
-          if (u == C::UPT - 1) tc::mbar_arrive(&c_empty[cst]);
-        }
-        if (++st == C::STAGES) {
-          st = 0;
-          par ^= 1;
-        }
-      }
-      if (++cst == C::COPIES) {
-        cst = 0;
-        cpar ^= 1;
+      if (lane == 0) {
+        tc::mbar_arrive(&r_full[ni % TA_ITEMS]);
+        tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
       }
     }
   }
@@ -856,7 +820,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
   __syncthreads();
   if (s_flag && tid < 32) tc::mbar_wait(drain, 0, a.wait_ns);  // a wait ran out: products in flight end
   __syncthreads();
-  if (role == 2) {
+  if (role == 0) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
@@ -867,26 +831,35 @@ cudaError_t run(PagedArgs& a, const Q4Cache& c, cudaStream_t s, int sms) {
   using C = Tq<DP, R, F32>;
   const void* f = reinterpret_cast<const void*>(k_paged_attn_q4<DP, R, F32>);
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = ta_prepare(f, C::smem, 0, ready);
+  // the register split draws on what the launch gives
+  const cudaError_t e = ta_prepare(f, C::smem, 80, ready);
   if (e != cudaSuccess) return e;
   a.tb = R / a.g;
   const PagedWs L = paged_ws(sms, R, DP);
   a.part_ml = L.ml;
   a.part_o = L.o;
   a.rows = R;
-  pg_division(a, sms, 128, 192, 256);
+  pg_division(a, sms, 640, 192, 256);
   Q4Cache cache = c;
   void* args[] = {&a, &cache};
   return launch_pdl(f, dim3(sms), dim3(TQ_THREADS), C::smem, s, args, 1);
 }
 
-// Rows of a tile: 16, or 32 where a request has more in the mean.
-int tile_rows(bool f32, int rows) { return f32 || rows <= 16 ? 16 : 32; }
+// Rows of a tile: no more than a request's in the mean ask for.
+int tile_rows(bool f32, int rows) {
+  if (f32) return rows <= 8 ? 8 : 16;
+  return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
 
 template <int DP>
 cudaError_t run_rows(PagedArgs& a, const Q4Cache& c, bool f32, int rows, cudaStream_t s, int sms) {
-  if (f32) return run<DP, 16, true>(a, c, s, sms);
-  return rows == 16 ? run<DP, 16, false>(a, c, s, sms) : run<DP, 32, false>(a, c, s, sms);
+  if (f32) return rows == 8 ? run<DP, 8, true>(a, c, s, sms) : run<DP, 16, true>(a, c, s, sms);
+  switch (rows) {
+    case 4: return run<DP, 4, false>(a, c, s, sms);
+    case 8: return run<DP, 8, false>(a, c, s, sms);
+    case 16: return run<DP, 16, false>(a, c, s, sms);
+    default: return run<DP, 32, false>(a, c, s, sms);
+  }
 }
 
 }  // namespace
@@ -901,6 +874,7 @@ cudaError_t launch_paged_attn_q4(PagedArgs a, const Q4Cache& cache, bool f32, in
   int g = std::min(a.g, R);
   while (a.g % g) --g;
   c.split = a.g / g;
+  c.s_whole = q4_whole_scales(a, c);
   if ((int64_t)a.Hkv * c.split > 0x7fffffff) return cudaErrorNotSupported;
   a.Hkv *= c.split;
   a.g = g;

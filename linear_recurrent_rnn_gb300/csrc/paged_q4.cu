@@ -221,6 +221,8 @@ bool strides_ok(int64_t size, int64_t n, std::initializer_list<int64_t> v) {
 }
 
 bool cache_strides_ok(const paged_q4_strides& t) {
+  for (int64_t x : {t.kc_page, t.kc_token, t.vc_page, t.vc_token, t.ks_page, t.ks_token, t.vs_page, t.vs_token})
+    if (x >= (int64_t)1 << 32) return false;  // (multiplied in 32 bits, to 64)
   return strides_ok(1, 16, {t.kc_page, t.kc_token, t.kc_head, t.vc_page, t.vc_token, t.vc_head}) &&
          strides_ok(1, 4, {t.ks_page, t.ks_token, t.ks_head, t.vs_page, t.vs_token, t.vs_head});
 }
@@ -345,6 +347,6 @@ extern "C" rglru_status paged_q4_attention(const paged_shape* s, const paged_q4_
   a.wait_ns = a.drop_cta >= 0 ? (uint64_t)debug_spin_limit() * 100 : TA_WAIT_NS;
   const Q4Cache c = {static_cast<const uint8_t*>(k_codes), static_cast<const uint8_t*>(k_scales), static_cast<const uint8_t*>(v_codes),
                      static_cast<const uint8_t*>(v_scales), t.kc_page, t.kc_token, t.kc_head, t.vc_page, t.vc_token, t.vc_head,
-                     t.ks_page, t.ks_token, t.ks_head, t.vs_page, t.vs_token, t.vs_head, 1};
+                     t.ks_page, t.ks_token, t.ks_head, t.vs_page, t.vs_token, t.vs_head, 0, 1};
   return cuda_status(launch_paged_attn_q4(a, c, s->io == RGLRU_F32, mean_rows(s), stream));
 }

@@ -307,16 +307,107 @@ __device__ __forceinline__ uint32_t ta_pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// ---------------------------------------------------------------- rows along the lanes, many rows
+constexpr int TA_HERE = 4;  // parts that are joined without handing over the last one
+
+// Row tile t of an item and its key tiles within the CTA's part.
+struct TaTile {
+  int tok, rows, ja, jb;
+};
+__device__ __forceinline__ TaTile ta_tile(const PagedArgs& a, const TaItem& it, int t, int tb1) {
+  TaTile x;
+  x.tok = it.tok + t * tb1;
+  const int nt = min(tb1, it.q - x.tok);
+  x.rows = max(nt, 0) * a.g;
+  const int base = it.kv - it.q + x.tok;
+  const int hi = max(base + nt, 0);
+  const int lo = a.window && base >= a.window ? base - a.window + 1 : 0;
+  x.ja = max(it.j0, lo / TA_BN);
+  x.jb = min(it.j1, (hi + TA_BN - 1) / TA_BN);
+  if (x.rows == 0 || x.jb < x.ja) x.jb = x.ja;
+  return x;
+}
+
+__device__ __forceinline__ void ta_store32(bf16* p, const uint32_t* u) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+               "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+
+// Bits 0 to h, none for a negative h.
+__device__ __forceinline__ uint32_t ta_bits(int h) { return h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1; }
+
+// One row's results joined over the CTAs [c0, c1] of an item, by all softmax threads: a thread
+// takes one row and a run of columns.
+template <int DP>
+__device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int tb1, int tid) {
+  const int c0 = it.c0, c1 = it.c1;
+  constexpr int NT = DP == 256 ? 1 : 2, SOFT = NT * 128;  // row tiles, threads
+  const float2* ml = reinterpret_cast<const float2*>(a.ws + a.part_ml);
+  const float* po = reinterpret_cast<const float*>(a.ws + a.part_o);
+  const int R = NT * 128;
+  // rows in use: of tile 0, and past 128 of tile 1
+  const int n1 = min(it.q - it.tok, tb1) * a.g;
+  const int n2 = NT == 2 ? max(min(it.q - it.tok - tb1, tb1), 0) * a.g : 0;
+  const int used = n2 > 0 ? 128 + n2 : n1;
+  int rp = SOFT * 16 / DP;
+  while (rp < used) rp <<= 1;
+  const int groups = SOFT / rp, cols = DP / groups;
+  const int row = tid & (rp - 1), col0 = tid / rp * cols;
+  if (row >= used || (row < 128 && row >= n1)) return;
+  float m = -INFINITY;
+  for (int c = c0; c <= c1; ++c) {
+    const float2 x = __ldcg(ml + (size_t)PgWalk::slot(c, c0) * R + row);
+    if (x.y != 0.0f) m = fmaxf(m, x.x);
+  }
+  float l = 0.0f;
+  for (int c = c0; c <= c1; ++c) {
+    const float2 x = __ldcg(ml + (size_t)PgWalk::slot(c, c0) * R + row);
+    if (x.y != 0.0f) l = fmaf(x.y, ta_ex2(x.x - m), l);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int t = row >> 7, r = row & 127;
+  const int64_t tok = it.first + it.tok + t * tb1 + pg_token(a, r);
+  const int hq = it.h * a.g + r - pg_token(a, r) * a.g;
+  bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
+  constexpr int W = 16;  // columns at a time: with two parts, 32 loads in flight
+#pragma unroll 1
+  for (int k = col0; k < col0 + cols && k < a.D; k += W) {
+    float acc[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) acc[e] = 0.0f;
+#pragma unroll 2
+    for (int c = c0; c <= c1; ++c) {
+      const size_t s = (size_t)PgWalk::slot(c, c0);
+      const float2 x = __ldcg(ml + s * R + row);
+      float v[W];
+#pragma unroll
+      for (int e = 0; e < W; ++e) v[e] = __ldcg(po + (s * DP + k + e) * R + row);
+      const float f = x.y == 0.0f ? 0.0f : ta_ex2(x.x - m);  // a part that saw nothing did not write its sums
+#pragma unroll
+      for (int e = 0; e < W; ++e) acc[e] = f != 0.0f ? fmaf(v[e], f, acc[e]) : acc[e];
+    }
+#pragma unroll
+    for (int e = 0; e < W; e += 8)
+      if (k + e < a.D && k + e < col0 + cols)
+        *reinterpret_cast<uint4*>(o + k + e) =
+            make_uint4(ta_pack(acc[e] * inv, acc[e + 1] * inv), ta_pack(acc[e + 2] * inv, acc[e + 3] * inv),
+                       ta_pack(acc[e + 4] * inv, acc[e + 5] * inv), ta_pack(acc[e + 6] * inv, acc[e + 7] * inv));
+  }
+  if (a.lse && col0 == 0)
+    a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 // ---------------------------------------------------------------- keys along the lanes, few rows (tf_)
-// Or over the softmax threads, 128 of them (named barrier 1).
-__device__ __forceinline__ bool tf_any(bool x) {
+// Or over the 128 softmax threads of a group (a named barrier each).
+__device__ __forceinline__ bool tf_any(bool x, int bar = 1) {
   uint32_t y;
   __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(y)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "r"(bar)
       : "memory");
   return y != 0;
 }
@@ -344,8 +435,7 @@ __device__ __forceinline__ void tf_combine(float (&v)[NR], F f) {
 }
 template <int NR>
 __device__ __forceinline__ int tf_column() {
-  const int lane = threadIdx.x & 31;
-  return NR == 32 ? lane : lane >> 1;
+  return (threadIdx.x & 31) / (32 / NR);
 }
 
 __device__ __forceinline__ float tf_lse(float ref, float sum) {
