@@ -37,7 +37,7 @@ BINDING = binding_path()
 SOURCES = ["api.cu", "scan_simt.cu", "gemm_simt.cu", "noalloc.cu", "host_util.cu", "fused_fwd.cu", "fused_bwd.cu",
            "decode.cu", "varlen.cu", "delta_rule.cu", "proj_tc.cu", "paged.cu", "paged_attn_simt.cu",
            "paged_attn_tc.cu", "paged_attn_few.cu", "paged_pages.cu", "paged_q4.cu",
-           "paged_attn_q4.cu"]
+           "paged_attn_q4.cu", "paged_attn_q4_tc.cu"]
 HEADERS = ["common.cuh", "internal.h", "tc.cuh", "host_util.h", "lookback.cuh",
            "paged.cuh", "paged_tc.cuh", "paged_q4.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

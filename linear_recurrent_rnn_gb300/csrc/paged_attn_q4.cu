@@ -576,13 +576,12 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
     const uint32_t lanes = tmem + ((uint32_t)(r & ~31) << 16) + C::K_COL;
     TqStream<C, TQ_KEYS, 0> str{a, cache, ctl, s_item, i_full, i_empty, s_copy + g * C::DEPTH * C::SB, (uint32_t)g};
     uint32_t s = g;  // unit
-    for (int st = 0; str.issue(st); st = st + 1 == C::DEPTH ? 0 : st + 1) {
-      if (!str.come()) continue;
+    while (str.issue()) {
+      if (__builtin_expect(!str.come(), 0)) continue;
       const uint32_t kb = s % C::KBUF;
       if (!ctl.wait(&k_empty[kb], (s / C::KBUF & 1) ^ 1)) break;
       tc::tc_fence_after();
-      const uint8_t* src = s_copy + (g * C::DEPTH + (st + 1 == C::DEPTH ? 0 : st + 1)) * C::SB;
-      tq_row<C>(src, r, [&](int p, const uint32_t (&y)[16]) {
+      tq_row<C>(str.ring + str.stage, r, [&](int p, const uint32_t (&y)[16]) {
         tc::tmem_st16(lanes + kb * (C::COL / 2) + p * 16, *reinterpret_cast<const float(*)[16]>(y));
       });
       tc::tmem_st_wait();
@@ -601,14 +600,12 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[c] = (c ^ (r & 7)) << 4;
     TqStream<C, TQ_VALUES, 1> str{a, cache, ctl, s_item, i_full, i_empty, ring, (uint32_t)g};
-    uint32_t s = g;  // unit
-    for (int st = 0; str.issue(st); st = st + 1 == C::DEPTH ? 0 : st + 1) {
-      if (!str.come()) continue;
-      const uint32_t vb = s % C::VBUF;
-      if (!ctl.wait(&v_empty[vb], (s / C::VBUF & 1) ^ 1)) break;
-      const uint8_t* src = ring + (st + 1 == C::DEPTH ? 0 : st + 1) * C::SB;
+    uint32_t vb = g, par = 1;  // (C::VBUF >= TQ_VALUES)
+    while (str.issue()) {
+      if (__builtin_expect(!str.come(), 0)) continue;
+      if (!ctl.wait(&v_empty[vb], par)) break;
       uint8_t* line = s_v + vb * C::VB + r * 128;
-      tq_row<C>(src, r, [&](int p, const uint32_t (&y)[16]) {
+      tq_row<C>(ring + str.stage, r, [&](int p, const uint32_t (&y)[16]) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<uint4*>(line + p / 2 * C::V_SLAB + (o[c] ^ (p & 1) << 6)) = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
@@ -616,7 +613,11 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&v_full[vb]);
-      s += TQ_VALUES;
+      vb += TQ_VALUES;
+      if (vb >= C::VBUF) {
+        vb -= C::VBUF;
+        par ^= 1;
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (role == 0) {

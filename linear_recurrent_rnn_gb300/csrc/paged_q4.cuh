@@ -17,7 +17,7 @@ struct Q4Cache {
   const uint8_t* vs;
   int64_t kc_page, kc_token, kc_head, vc_page, vc_token, vc_head;
   int64_t ks_page, ks_token, ks_head, vs_page, vs_token, vs_head;
-  int s_whole;  // rows of scales lie on boundaries of their size
+  int s_whole;  // nothing of a row is cut off: its scales lie on boundaries of their size, D fills its columns, pages of 16 and more
   int split;  // heads of the attention's work division a key/value head
 };
 
@@ -105,10 +105,12 @@ __device__ __forceinline__ uint32_t tq_code(int r, int piece) {
 
 // The units of codes that a warpgroup brings: every G-th of the CTA's stream of keys (KIND 0) or of values
 // (1), or all of both in the order in which a kernel uses them: the values of a tile after its keys (2), or
-// after the next tile's (3).  Each of its warps copies its own 32 rows, waits for them and dequantises them, so that no other warp is asked: units in flight are the
-// warp's own groups of cp.async, one an iteration (an empty one where there is no unit to copy).
+// after the next tile's (3).  Each of its warps copies its own 32 rows, waits for them and dequantises
+// them, so that no other warp is asked: units in flight are the warp's own groups of cp.async, one an iteration
+// (an empty one where there is no unit to copy).
 template <class C, int G, int KIND>
 struct TqStream {
+  static constexpr int CPR = C::RB / 16, RPI = 32 / CPR;  // 16-byte pieces of a row, rows of an instruction
   const PagedArgs& a;
   const Q4Cache& c;
   const TqAbort& ctl;
@@ -117,9 +119,11 @@ struct TqStream {
   uint64_t* i_empty;
   uint8_t* ring;  // this warpgroup's
   uint32_t g;     // which of the G it is
+  uint32_t stage = 0;  // offset of the stage that is copied to next, and of the oldest copy
   uint32_t ni = 0, next = 0;  // item; number of its first unit
   int q = 0, part = 0, end = 0, j0 = 0, lo = 0, hi = 0;  // the place in the item's stream of what is copied next (q < end), its keys
-  const int32_t* table = nullptr;  // the item's row of the table, its head's codes and scales
+  int pos = 0;                 // its first position of this warp's rows
+  const int32_t* table = nullptr;  // the item's row of the table
   int h = 0;
   int id[2] = {-1, -1};        // the pages of the first and the last 16 of the warp's rows (-1: zeros)
   bool more = true, ok = true; // there are items left
@@ -132,17 +136,22 @@ struct TqStream {
   }
   // (read an iteration before they are used)
   __device__ __forceinline__ void page() {
-    const int j = tile();
+    pos = tile() * TA_BN + (threadIdx.x & 96);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int pos = j * TA_BN + (threadIdx.x & 96) + 16 * e;
-      id[e] = q < end && pos < hi && pos + 16 > lo ? table[pos >> a.ps_log2] : -1;
+      const int at = pos + 16 * e;
+      id[e] = -1;
+      if ((q < end) & (at < hi) & (at + 16 > lo)) id[e] = table[at >> a.ps_log2];
     }
   }
   __device__ __forceinline__ void forward(uint32_t units) {
-    part += units;
-    q += part / C::UNITS;
-    part %= C::UNITS;
+    if (C::UNITS == 1) {
+      q += units;
+    } else {
+      part += units;
+      q += part / C::UNITS;
+      part %= C::UNITS;
+    }
   }
   // The next item, if its record is there (or waiting for it); its first unit that is this group's.
   __device__ __forceinline__ void item(bool wait) {
@@ -157,6 +166,7 @@ struct TqStream {
     const TaItem& it = items[ni % TA_ITEMS];
     more = it.n >= 0;
     if (!more) return;
+    const int lane = threadIdx.x & 31;
     h = it.h / c.split;
     table = a.table + (int64_t)it.n * a.table_width;
     j0 = it.j0;
@@ -165,7 +175,7 @@ struct TqStream {
     lo = it.lo;
     hi = (int)min((int64_t)it.hi, (int64_t)a.table_width << a.ps_log2);  // (beyond the table: zeros)
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
+    if (lane == 0) tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
     ++ni;
     const uint32_t skip = (g + G - next % G) % G;
     next += end * C::UNITS;
@@ -173,68 +183,86 @@ struct TqStream {
     forward(skip);
     page();
   }
-  // One iteration: copies the next unit to stage `st`; false once nothing is left to copy or on its way.
-  __device__ __forceinline__ bool issue(int st) {
+  // One iteration: copies the next unit; false once nothing is left to copy or on its way.
+  __device__ __forceinline__ bool issue() {
     real <<= 1;
-    while (q >= end && more && ok) {
+    while (__builtin_expect((q >= end) & more & ok, 0)) {
       const uint32_t had = ni;
       item((real & ((1u << C::DEPTH) - 1)) == 0);
       if (ni == had) break;
     }
-    if (!ok) return false;
-    if (q < end) {
-      copy(ring + st * C::SB);
+    if (__builtin_expect(!ok, 0)) return false;
+    if (__builtin_expect(q < end, 1)) {
+      // whole rows of pages of 16 and more, as nearly all are: nothing to cut off
+      const bool v = values();
+      if (__builtin_expect(((uint32_t)id[0] < (uint32_t)a.P) & ((uint32_t)id[1] < (uint32_t)a.P) & (pos >= lo) & (pos + 32 <= hi) & c.s_whole, 1)) {
+        if (v) whole<true>();
+        else whole<false>();
+      } else {
+        cut(v);
+      }
       real |= 1u;
       forward(G);
       page();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    return more || q < end || (real & ((1u << C::DEPTH) - 1)) != 0;
+    stage = stage + C::SB == C::DEPTH * C::SB ? 0u : stage + C::SB;
+    return more | (q < end) | ((real & ((1u << C::DEPTH) - 1)) != 0);
   }
-  __device__ __forceinline__ void copy(uint8_t* dst) {
-    constexpr int CPR = C::RB / 16, RPI = 32 / CPR;  // pieces of a row, rows of an instruction
+  template <bool V>
+  __device__ __forceinline__ void whole() {
+    const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96, in = (1 << a.ps_log2) - 1;
+    const uint32_t token = V ? c.vc_token : c.kc_token, s_token = V ? c.vs_token : c.ks_token;
+    uint8_t* dst = ring + stage;
+    const uint32_t o[2] = {(uint32_t)(pos & in), (uint32_t)((pos + 16) & in)};
+    const uint8_t* codes = (V ? c.vc + h * c.vc_head : c.kc + h * c.kc_head) + part * C::RB + lane % CPR * 16;
+    const uint8_t* scales = (V ? c.vs + h * c.vs_head : c.ks + h * c.ks_head) + part * C::SP;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint8_t* row = codes + (uint64_t)(uint32_t)id[e] * (uint32_t)(V ? c.vc_page : c.kc_page) + (uint64_t)(o[e] + lane / CPR) * token;
+      uint8_t* to = dst + r0 * C::RB + tq_code<C>(lane / CPR, lane % CPR);
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        tq_copy16(to + (16 * e + i * RPI) * C::RB, row);
+        row += (uint64_t)RPI * token;
+      }
+    }
+    tq_copy_row<C::SP>(dst + TA_BN * C::RB + (r0 + lane) * C::SP,
+                       scales + (uint64_t)(uint32_t)(lane < 16 ? id[0] : id[1]) * (uint32_t)(V ? c.vs_page : c.ks_page) +
+                           (uint64_t)((lane < 16 ? o[0] : o[1]) + (lane & 15)) * s_token);
+  }
+  __device__ __forceinline__ void cut(bool v) {
     const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96, piece = lane % CPR;
-    const bool v = values();
-    const int pos = tile() * TA_BN + r0, in = (1 << a.ps_log2) - 1, left = a.D - part * C::COL;  // columns
+    uint8_t* dst = ring + stage;
+    const int in = (1 << a.ps_log2) - 1, left = a.D - part * C::COL;  // columns
     const uint32_t page = v ? c.vc_page : c.kc_page, token = v ? c.vc_token : c.kc_token;
     const uint32_t s_page = v ? c.vs_page : c.ks_page, s_token = v ? c.vs_token : c.ks_token;
     const uint8_t* from = (v ? c.vc : c.kc) + h * (v ? c.vc_head : c.kc_head) + part * C::RB + piece * 16;
     const uint8_t* s_from = (v ? c.vs : c.ks) + h * (v ? c.vs_head : c.ks_head) + part * C::SP;
     uint8_t* to = dst + TA_BN * C::RB + (r0 + lane) * C::SP;
-    // whole rows of pages of 16 and more, as nearly all are: nothing to cut off
-    if ((uint32_t)id[0] < (uint32_t)a.P && (uint32_t)id[1] < (uint32_t)a.P && pos >= lo && pos + 32 <= hi && left >= C::COL &&
-        c.s_whole && a.ps_log2 >= 4) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint8_t* row = from + (uint64_t)(uint32_t)id[e] * page + (uint64_t)(uint32_t)(((pos + 16 * e) & in) + lane / CPR) * token;
-#pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) tq_copy16(dst + tq_code<C>(r0 + 16 * e + i * RPI + lane / CPR, piece), row + i * RPI * (uint64_t)token);
-      }
-      tq_copy_row<C::SP>(to, s_from + (uint64_t)(uint32_t)(lane < 16 ? id[0] : id[1]) * s_page + (uint64_t)(uint32_t)((pos + lane) & in) * s_token);
-    } else {
-      // a row a lane: its page, read here where pages are smaller
-      int mine = lane < 16 ? id[0] : id[1];
-      const bool seen = pos + lane >= lo && pos + lane < hi;
-      if (a.ps_log2 < 4) mine = seen ? table[(pos + lane) >> a.ps_log2] : -1;
-      const bool there = seen && (uint32_t)mine < (uint32_t)a.P;
-      const uint64_t off = (uint32_t)((pos + lane) & in);
-      const uint64_t row = (uint64_t)(uint32_t)mine * page + off * token;
+    // a row a lane: its page, read here where pages are smaller
+    int mine = lane < 16 ? id[0] : id[1];
+    const bool seen = pos + lane >= lo && pos + lane < hi;
+    if (a.ps_log2 < 4) mine = seen ? table[(pos + lane) >> a.ps_log2] : -1;
+    const bool there = seen && (uint32_t)mine < (uint32_t)a.P;
+    const uint64_t off = (uint32_t)((pos + lane) & in);
+    const uint64_t row = (uint64_t)(uint32_t)mine * page + off * token;
 #pragma unroll 1
-      for (int i = 0; i < 32 / RPI; ++i) {
-        const int r = i * RPI + lane / CPR;
-        const uint64_t at = __shfl_sync(0xffffffffu, row, r);
-        const int bytes = __shfl_sync(0xffffffffu, there, r) ? min(max(left / 2 - piece * 16, 0), 16) : 0;
-        tq_copy16(dst + tq_code<C>(r0 + r, piece), bytes ? from + at : c.kc, bytes);
-      }
-      s_from += (uint64_t)(uint32_t)mine * s_page + off * s_token;
+    for (int i = 0; i < 32 / RPI; ++i) {
+      const int r = i * RPI + lane / CPR;
+      const uint64_t at = __shfl_sync(0xffffffffu, row, r);
+      const int bytes = __shfl_sync(0xffffffffu, there, r) ? min(max(left / 2 - piece * 16, 0), 16) : 0;
+      tq_copy16(dst + tq_code<C>(r0 + r, piece), bytes ? from + at : c.kc, bytes);
+    }
+    s_from += (uint64_t)(uint32_t)mine * s_page + off * s_token;
 #pragma unroll
-      for (int w = 0; w < (int)C::SP / 4; ++w) {
-        const int bytes = there ? min(max(left / 16 - 4 * w, 0), 4) : 0;
-        tq_copy4(to + 4 * w, bytes ? s_from + 4 * w : c.ks, bytes);
-      }
+    for (int w = 0; w < (int)C::SP / 4; ++w) {
+      const int bytes = there ? min(max(left / 16 - 4 * w, 0), 4) : 0;
+      tq_copy4(to + 4 * w, bytes ? s_from + 4 * w : c.ks, bytes);
     }
   }
-  // Waits for the unit that was copied DEPTH - 1 iterations ago; false if there was none.
+  // Waits for the unit that was copied DEPTH - 1 iterations ago, at `ring + stage` (issue() has moved it on);
+  // false if there was none.
   __device__ __forceinline__ bool come() const {
     asm volatile("cp.async.wait_group %0;" ::"n"(C::DEPTH - 1) : "memory");
     __syncwarp();
@@ -283,14 +311,20 @@ __device__ __forceinline__ void tq_row(const uint8_t* src, int r, F f) {
   }
 }
 
-// Attention over the cache in 4 bits, `rows` a request in the mean (paged_attn_q4.cu).
+// Attention over the cache in 4 bits: few rows a request, `rows` in the mean (paged_attn_q4.cu; float32 always),
+// many rows (paged_attn_q4_tc.cu; bf16).
+// Rows up to which the first is taken, where bf16 queries let choose.  Measured (64 requests of 500 to 4096 keys, 32
+// heads on 8 of 128; few against many): 20 rows 120 and 138 us, 32 rows 132 and 138, 48 rows 242 and 145.
+constexpr int TQ_FEW_ROWS = 32;
 cudaError_t launch_paged_attn_q4(PagedArgs a, const Q4Cache& c, bool f32, int rows, cudaStream_t s);
 size_t paged_attn_q4_ws_bytes(const paged_shape* s, int rows);
-// Whether rows of scales lie on boundaries of their size, to be copied at once.
+cudaError_t launch_paged_attn_q4_tc(PagedArgs a, const Q4Cache& c, cudaStream_t s);
+size_t paged_attn_q4_tc_ws_bytes(const paged_shape* s);
+// Q4Cache::s_whole (a row that is cut off is copied piece by piece, with what lies behind it as zeros).
 inline int q4_whole_scales(const PagedArgs& a, const Q4Cache& c) {
   const uint64_t on = reinterpret_cast<uintptr_t>(c.ks) | reinterpret_cast<uintptr_t>(c.vs) | c.ks_page | c.ks_token | c.ks_head |
                       c.vs_page | c.vs_token | c.vs_head;
-  return on % 8 == 0 || (a.D <= 64 && on % 4 == 0);
+  return on % (a.D <= 64 ? 4 : 8) == 0 && (a.D == 64 || a.D == 128 || a.D == 256) && a.ps_log2 >= 4;
 }
 
 }  // namespace rglru
