@@ -12,12 +12,17 @@ namespace rglru {
 namespace {
 
 // ---------------------------------------------------------------- write and read
-// A lane takes a group: 16 channels of a token's head, keys' groups first, then values'.  A token's
-// groups are spread over the lanes of a warp, or of a part of one where it has few.  Bound by memory
-// bandwidth, and by latency for few tokens.
+// A lane has a group, 16 channels of a head of the keys or of the values, and takes it of several tokens at
+// once: where the group lies is worked out once, and the tokens' loads are in flight together.  A token's
+// groups are spread over the lanes of a warp, or of a part of one where it has few; more than 32 of them, and keys
+// and values, are blocks of their own (blockIdx.y).
+// Measured (GB300): 16384 tokens of 8 heads of 128 in bf16, written and read back, 33.9 us, 5.1 TB/s of what must
+// move (with a lane's place worked out anew for each group, 16-byte loads and a division: 50.6).  Bound by memory
+// bandwidth; by latency for few tokens: 64 of 1 head 5.4 us.
 struct Q4RowArgs {
-  int T, Hkv, groups, s_log2, lanes_log2;  // groups of a token's keys; lanes of a token
-  uint32_t head_groups;                    // groups of a head
+  int T, groups, s_log2, lanes_log2;  // groups of a token's keys; lanes of a token
+  int head_groups, units;             // groups of a head; blocks of lanes for a token's keys and values
+  int wide;                           // rows lie on 32 bytes
   int64_t slots_end;
   const int64_t* slots;
   uint8_t* row[2];  // k and v
@@ -40,130 +45,167 @@ __device__ __forceinline__ float q4_get(const Q4Group<bf16>& g, int i) {
 }
 __device__ __forceinline__ float q4_get(const Q4Group<float>& g, int i) { return __uint_as_float((&g.w[i / 4].x)[i % 4]); }
 
-// A group's codes and scale.  The largest is found among the bits without signs: an infinity's are
-// above all finite ones', a NaN's above those.  x / s is needed to the last bit only near a border
-// between two codes, s times a number of at most 3 bits, which x may equal; so it is rounded
-// correctly, by one step of Newton's method on the product with 1 / s (Markstein, 1990).
-template <class T>
-__device__ __forceinline__ uint2 q4_quantise(const Q4Group<T>& g, uint8_t& scale) {
+__device__ __forceinline__ void q4_put(Q4Group<bf16>& g, int i, float lo, float hi) { (&g.w[i / 8].x)[i / 2 % 4] = ta_pack(lo, hi); }
+__device__ __forceinline__ void q4_put(Q4Group<float>& g, int i, float lo, float hi) {
+  (&g.w[i / 4].x)[i % 4] = __float_as_uint(lo);
+  (&g.w[i / 4].x)[i % 4 + 1] = __float_as_uint(hi);
+}
+// The largest of the group, without its sign, as bits: an infinity's are above all finite ones', a NaN's above those.
+__device__ __forceinline__ uint32_t q4_top(const Q4Group<bf16>& g) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(q4_get(g, i)) & 0x7fffffffu);
-  if (top >= 0x7f800000u) {
+  for (int i = 0; i < 8; ++i) top = __vmaxu2(top, (&g.w[i / 4].x)[i % 4] & 0x7fff7fffu);
+  return max(top & 0xffff0000u, top << 16);
+}
+__device__ __forceinline__ uint32_t q4_top(const Q4Group<float>& g) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, (&g.w[i / 4].x)[i % 4] & 0x7fffffffu);
+  return top;
+}
+// Whole sectors an instruction: half as many passes through L1.
+__device__ __forceinline__ void q4_load32(uint4* u, const uint8_t* p) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(u[0].x), "=r"(u[0].y), "=r"(u[0].z), "=r"(u[0].w), "=r"(u[1].x), "=r"(u[1].y), "=r"(u[1].z), "=r"(u[1].w)
+               : "l"(p)
+               : "memory");
+}
+
+// A group's codes and scale.  x / s is needed to the last bit only near a border between two codes, s times
+// a number b of at most 3 bits.  With r the reciprocal of s cut to 16 bits (never above it, so that a zero keeps its
+// sign) and d = (1 - r s) / s, where r s is exact: x / s = x r + x d.  That sum, rounded once, is off by less than
+// 2^-37 of it before its rounding; where x = s b it rounds to b, and the next float32 x on either side is
+// at least 2^-24 / 1.875 of b away from it, more than half of the last bit by 2^-28: the code is that of the exact
+// quotient.  The same for the largest by 6, of which no float32 quotient lies within 2^-27 of a rounding's border.
+template <class T>
+__device__ __forceinline__ uint2 q4_quantise(const Q4Group<T>& g, uint8_t& scale) {
+  const uint32_t bits = q4_top(g);
+  if (bits >= 0x7f800000u) {
     scale = 0x7f;  // NaN
     return make_uint2(0u, 0u);
   }
+  const float top = __uint_as_float(bits);
+  constexpr float SIXTH = 0x1.5554p-3f, REST = 0x1.555556p-19f;  // 1/6 in 16 bits, and what is left of it
   uint16_t two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(__fdiv_rn(__uint_as_float(top), 6.0f)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(fmaf(top, SIXTH, top * REST)));
   const uint32_t code = max((uint32_t)two & 0xffu, 1u);  // 1: 2^-9
   const uint32_t h = q4_scales(code);
-  const float s = __half2float(reinterpret_cast<const __half2&>(h).x), r = __frcp_rn(s);
+  const float s = __half2float(reinterpret_cast<const __half2&>(h).x);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  const float cut = __uint_as_float(__float_as_uint(r) & 0xffffff00u), d = fmaf(-cut, s, 1.0f) * r;
   scale = (uint8_t)code;
-  uint32_t out[2] = {0u, 0u};
+  uint32_t out[2];
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    float q[2];
+  for (int w = 0; w < 2; ++w) {
+    float2 q[4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float x = q4_get(g, i + e), y = x * r;
-      q[e] = copysignf(fmaf(fmaf(-y, s, x), r, y), x);  // (a zero keeps its sign)
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = make_float2(q4_get(g, 8 * w + 2 * k), q4_get(g, 8 * w + 2 * k + 1));
+      q[k] = make_float2(fmaf(x.x, cut, x.x * d), fmaf(x.y, cut, x.y * d));
     }
-    uint32_t b;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(b) : "f"(q[1]), "f"(q[0]));
-    out[i / 8] |= b << i % 8 * 4;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(out[w])
+        : "f"(q[0].x), "f"(q[0].y), "f"(q[1].x), "f"(q[1].y), "f"(q[2].x), "f"(q[2].y), "f"(q[3].x), "f"(q[3].y));
   }
   return make_uint2(out[0], out[1]);
 }
 
-// Where group i of a token lies: keys or values, its row's bytes, its code's and scale's in the slot.
+// The lane's group of token 0 and slot 0: `kv` keys or values, its row, its codes and its scale.
 struct Q4Place {
-  int kv, b;
-  int64_t row, code, scale;
+  int kv;
+  bool in;
+  uint8_t *row, *codes, *scale;
 };
 template <class T>
-__device__ __forceinline__ Q4Place q4_place(const Q4RowArgs& a, int64_t t, int64_t page, int64_t off, int i) {
+__device__ __forceinline__ Q4Place q4_place(const Q4RowArgs& a, int unit) {
   Q4Place p;
-  p.kv = i >= a.groups;
-  const int c = p.kv ? i - a.groups : i, h = c / a.head_groups, b = c - h * a.head_groups;
-  p.b = b;
-  p.row = t * a.row_token[p.kv] + h * a.row_head[p.kv] + b * (16 * (int)sizeof(T));
-  p.code = page * a.c_page[p.kv] + off * a.c_token[p.kv] + h * a.c_head[p.kv] + b * 8;
-  p.scale = page * a.s_page[p.kv] + off * a.s_token[p.kv] + h * a.s_head[p.kv] + b;
+  p.kv = unit & 1;
+  const int lanes = 1 << a.lanes_log2, c = (unit >> 1) * lanes + (threadIdx.x & (lanes - 1)), h = c / a.head_groups, b = c - h * a.head_groups;
+  p.in = c < a.groups;
+  p.row = a.row[p.kv] + h * a.row_head[p.kv] + b * (16 * (int)sizeof(T));
+  p.codes = a.codes[p.kv] + h * a.c_head[p.kv] + b * 8;
+  p.scale = a.scales[p.kv] + h * a.s_head[p.kv] + b;
   return p;
 }
+// tokens of a lane in flight
+template <class T>
+constexpr int Q4_BATCH = sizeof(T) == 2 ? 4 : 2;
 
 template <class T>
 __global__ void __launch_bounds__(Q4_THREADS) k_paged_q4_write(const __grid_constant__ Q4RowArgs a) {
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  constexpr int BATCH = sizeof(T) == 2 ? 4 : 2;  // groups of a lane in flight
-  const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
+  constexpr int BATCH = Q4_BATCH<T>;
   const int64_t step = (int64_t)gridDim.x * Q4_THREADS >> a.lanes_log2;
-  for (int64_t t = ((int64_t)blockIdx.x * Q4_THREADS + threadIdx.x) >> a.lanes_log2; t < a.T; t += step) {
-    const int64_t slot = a.slots[t];
-    if (slot < 0 || slot >= a.slots_end) continue;
-    const int64_t page = slot >> a.s_log2, off = slot & ((1 << a.s_log2) - 1);
-    for (int i0 = lane; i0 < 2 * a.groups; i0 += lanes * BATCH) {
+  for (int unit = blockIdx.y; unit < a.units; unit += gridDim.y) {
+    const Q4Place p = q4_place<T>(a, unit);
+    if (!p.in) continue;
+    for (int64_t t0 = ((int64_t)blockIdx.x * Q4_THREADS + threadIdx.x) >> a.lanes_log2; t0 < a.T; t0 += step * BATCH) {
       Q4Group<T> g[BATCH];
-      Q4Place p[BATCH];
+      int64_t slot[BATCH];
 #pragma unroll
       for (int e = 0; e < BATCH; ++e) {
-        const int i = i0 + lanes * e;
-        if (i >= 2 * a.groups) continue;
-        p[e] = q4_place<T>(a, t, page, off, i);
-        const uint4* src = reinterpret_cast<const uint4*>(a.row[p[e].kv] + p[e].row);
+        const int64_t t = t0 + e * step;
+        slot[e] = -1;
+        if (t >= a.T) continue;
+        slot[e] = a.slots[t];
+        const uint8_t* src = p.row + t * a.row_token[p.kv];
+        if (a.wide) {
 #pragma unroll
-        for (int w = 0; w < Q4Group<T>::WORDS; ++w) g[e].w[w] = src[w];
+          for (int w = 0; w < Q4Group<T>::WORDS; w += 2) q4_load32(g[e].w + w, src + 16 * w);
+        } else {
+#pragma unroll
+          for (int w = 0; w < Q4Group<T>::WORDS; ++w) g[e].w[w] = reinterpret_cast<const uint4*>(src)[w];
+        }
       }
 #pragma unroll
       for (int e = 0; e < BATCH; ++e) {
-        if (i0 + lanes * e >= 2 * a.groups) continue;
+        if (slot[e] < 0 || slot[e] >= a.slots_end) continue;
+        const int64_t page = slot[e] >> a.s_log2, off = slot[e] & ((1 << a.s_log2) - 1);
         uint8_t scale;
         const uint2 codes = q4_quantise(g[e], scale);
-        *reinterpret_cast<uint2*>(a.codes[p[e].kv] + p[e].code) = codes;
-        a.scales[p[e].kv][p[e].scale] = scale;
+        *reinterpret_cast<uint2*>(p.codes + page * a.c_page[p.kv] + off * a.c_token[p.kv]) = codes;
+        p.scale[page * a.s_page[p.kv] + off * a.s_token[p.kv]] = scale;
       }
     }
   }
-}
-
-__device__ __forceinline__ void q4_put(Q4Group<bf16>& g, int i, float lo, float hi) { (&g.w[i / 8].x)[i / 2 % 4] = ta_pack(lo, hi); }
-__device__ __forceinline__ void q4_put(Q4Group<float>& g, int i, float lo, float hi) {
-  (&g.w[i / 4].x)[i % 4] = __float_as_uint(lo);
-  (&g.w[i / 4].x)[i % 4 + 1] = __float_as_uint(hi);
 }
 
 template <class T>
 __global__ void __launch_bounds__(Q4_THREADS) k_paged_q4_read(const __grid_constant__ Q4RowArgs a) {
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  constexpr int BATCH = 4;
-  const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
+  constexpr int BATCH = Q4_BATCH<T>;
   const int64_t step = (int64_t)gridDim.x * Q4_THREADS >> a.lanes_log2;
-  for (int64_t t = ((int64_t)blockIdx.x * Q4_THREADS + threadIdx.x) >> a.lanes_log2; t < a.T; t += step) {
-    const int64_t slot = a.slots[t];
-    const bool there = slot >= 0 && slot < a.slots_end;
-    const int64_t page = there ? slot >> a.s_log2 : 0, off = there ? slot & ((1 << a.s_log2) - 1) : 0;
-    for (int i0 = lane; i0 < 2 * a.groups; i0 += lanes * BATCH) {
+  for (int unit = blockIdx.y; unit < a.units; unit += gridDim.y) {
+    const Q4Place p = q4_place<T>(a, unit);
+    if (!p.in) continue;
+    for (int64_t t0 = ((int64_t)blockIdx.x * Q4_THREADS + threadIdx.x) >> a.lanes_log2; t0 < a.T; t0 += step * BATCH) {
+      int64_t slot[BATCH];
+#pragma unroll
+      for (int e = 0; e < BATCH; ++e) slot[e] = t0 + e * step < a.T ? a.slots[t0 + e * step] : -1;
       uint2 codes[BATCH];
       uint32_t scale[BATCH];
-      Q4Place p[BATCH];
 #pragma unroll
       for (int e = 0; e < BATCH; ++e) {
-        const int i = i0 + lanes * e;
         codes[e] = make_uint2(0u, 0u);
         scale[e] = 0u;
-        if (i >= 2 * a.groups) continue;
-        p[e] = q4_place<T>(a, t, page, off, i);
-        if (!there) continue;
-        codes[e] = *reinterpret_cast<const uint2*>(a.codes[p[e].kv] + p[e].code);
-        scale[e] = a.scales[p[e].kv][p[e].scale];
+        if (slot[e] < 0 || slot[e] >= a.slots_end) continue;
+        const int64_t page = slot[e] >> a.s_log2, off = slot[e] & ((1 << a.s_log2) - 1);
+        codes[e] = *reinterpret_cast<const uint2*>(p.codes + page * a.c_page[p.kv] + off * a.c_token[p.kv]);
+        scale[e] = p.scale[page * a.s_page[p.kv] + off * a.s_token[p.kv]];
       }
 #pragma unroll
       for (int e = 0; e < BATCH; ++e) {
-        if (i0 + lanes * e >= 2 * a.groups) continue;
-        const uint32_t h = q4_scales(scale[e]);
-        const float s = __half2float(reinterpret_cast<const __half2&>(h).x);
+        const int64_t t = t0 + e * step;
+        if (t >= a.T) continue;
+        const uint32_t s = q4_scales(scale[e]), s2 = __byte_perm(s, s, 0x1010);
         Q4Group<T> g;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
@@ -171,13 +213,19 @@ __global__ void __launch_bounds__(Q4_THREADS) k_paged_q4_read(const __grid_const
           q4_pairs(w ? codes[e].y : codes[e].x, r);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 v = __half22float2(reinterpret_cast<const __half2&>(r[k]));
-            q4_put(g, 8 * w + 2 * k, v.x * s, v.y * s);
+            const uint32_t y = q4_mul2(r[k], s2);  // (exact)
+            const float2 v = __half22float2(reinterpret_cast<const __half2&>(y));
+            q4_put(g, 8 * w + 2 * k, v.x, v.y);
           }
         }
-        uint4* dst = reinterpret_cast<uint4*>(a.row[p[e].kv] + p[e].row);
+        uint8_t* dst = p.row + t * a.row_token[p.kv];
+        if (a.wide) {
 #pragma unroll
-        for (int w = 0; w < Q4Group<T>::WORDS; ++w) dst[w] = g.w[w];
+          for (int w = 0; w < Q4Group<T>::WORDS; w += 2) ta_store32(reinterpret_cast<bf16*>(dst + 16 * w), &g.w[w].x);
+        } else {
+#pragma unroll
+          for (int w = 0; w < Q4Group<T>::WORDS; ++w) reinterpret_cast<uint4*>(dst)[w] = g.w[w];
+        }
       }
     }
   }
@@ -248,12 +296,13 @@ rglru_status rows_call(const paged_shape* s, const paged_q4_strides* strides, co
   if (!strides_ok(es, 16, {t.k_token, t.k_head, t.v_token, t.v_head}) || !cache_strides_ok(t)) return RGLRU_ERR_UNSUPPORTED;
   Q4RowArgs a;
   a.T = s->tokens;
-  a.Hkv = s->Hkv;
   a.head_groups = s->D / 16;
   if ((int64_t)s->Hkv * a.head_groups > 1 << 24) return RGLRU_ERR_UNSUPPORTED;  // (groups are counted in 32 bits)
   a.groups = s->Hkv * (int)a.head_groups;
   a.s_log2 = pg_log2(s->page_size);
-  a.lanes_log2 = std::min(5, pg_log2(2 * a.groups));
+  for (a.lanes_log2 = 0; a.lanes_log2 < 5 && 1 << a.lanes_log2 < a.groups;) ++a.lanes_log2;
+  a.units = 2 * ((a.groups + (1 << a.lanes_log2) - 1) >> a.lanes_log2);
+  a.wide = 1;
   a.slots_end = (int64_t)s->num_pages * s->page_size;
   a.slots = slots;
   const void* ptr[2][3] = {{k, kc, ks}, {v, vc, vs}};
@@ -263,6 +312,7 @@ rglru_status rows_call(const paged_shape* s, const paged_q4_strides* strides, co
     a.row[i] = const_cast<uint8_t*>(static_cast<const uint8_t*>(ptr[i][0]));
     a.codes[i] = const_cast<uint8_t*>(static_cast<const uint8_t*>(ptr[i][1]));
     a.scales[i] = const_cast<uint8_t*>(static_cast<const uint8_t*>(ptr[i][2]));
+    a.wide = a.wide && (reinterpret_cast<uintptr_t>(ptr[i][0]) | str[i][0] * es | str[i][1] * es) % 32 == 0;
     a.row_token[i] = str[i][0] * es;
     a.row_head[i] = str[i][1] * es;
     a.c_page[i] = str[i][2];
@@ -272,12 +322,15 @@ rglru_status rows_call(const paged_shape* s, const paged_q4_strides* strides, co
     a.s_token[i] = str[i][6];
     a.s_head[i] = str[i][7];
   }
-  const int per = Q4_THREADS >> a.lanes_log2;
-  const int blocks = (int)std::min<int64_t>(((int64_t)a.T + per - 1) / per, 1 << 16);
+  // few tokens: one a lane, over many SMs
+  const int64_t per = Q4_THREADS >> a.lanes_log2, batch = es == 2 ? Q4_BATCH<bf16> : Q4_BATCH<float>;
+  const int y = std::min(a.units, 1 << 15);
+  const int64_t most = (a.T + per - 1) / per, least = (a.T + per * batch - 1) / (per * batch);
+  const int blocks = (int)std::max(least, std::min<int64_t>(most, (608 + y - 1) / y));
   const void* f = write ? (es == 2 ? reinterpret_cast<const void*>(k_paged_q4_write<bf16>) : reinterpret_cast<const void*>(k_paged_q4_write<float>))
                         : (es == 2 ? reinterpret_cast<const void*>(k_paged_q4_read<bf16>) : reinterpret_cast<const void*>(k_paged_q4_read<float>));
   void* args[] = {&a};
-  return cuda_status(launch_pdl(f, dim3(blocks), dim3(Q4_THREADS), 0, stream, args, 1));
+  return cuda_status(launch_pdl(f, dim3(blocks, y), dim3(Q4_THREADS), 0, stream, args, 1));
 }
 
 }  // namespace
