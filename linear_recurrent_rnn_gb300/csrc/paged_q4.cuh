@@ -125,7 +125,7 @@ struct TqStream {
   int pos = 0;                 // its first position of this warp's rows
   const int32_t* table = nullptr;  // the item's row of the table
   int h = 0;
-  int id[2] = {-1, -1};        // the pages of the first and the last 16 of the warp's rows (-1: zeros)
+  int mine = -1;               // the page of the lane's row (-1: zeros)
   bool more = true, ok = true; // there are items left
   uint32_t real = 0;           // a bit an iteration: a unit was copied (the last one: bit 0)
 
@@ -137,12 +137,9 @@ struct TqStream {
   // (read an iteration before they are used)
   __device__ __forceinline__ void page() {
     pos = tile() * TA_BN + (threadIdx.x & 96);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int at = pos + 16 * e;
-      id[e] = -1;
-      if ((q < end) & (at < hi) & (at + 16 > lo)) id[e] = table[at >> a.ps_log2];
-    }
+    const int at = pos + (threadIdx.x & 31);
+    mine = -1;
+    if ((q < end) & (at < hi) & (at >= lo)) mine = table[at >> a.ps_log2];
   }
   __device__ __forceinline__ void forward(uint32_t units) {
     if (C::UNITS == 1) {
@@ -195,7 +192,7 @@ struct TqStream {
     if (__builtin_expect(q < end, 1)) {
       // whole rows of pages of 16 and more, as nearly all are: nothing to cut off
       const bool v = values();
-      if (__builtin_expect(((uint32_t)id[0] < (uint32_t)a.P) & ((uint32_t)id[1] < (uint32_t)a.P) & (pos >= lo) & (pos + 32 <= hi) & c.s_whole, 1)) {
+      if (__builtin_expect(__all_sync(0xffffffffu, (uint32_t)mine < (uint32_t)a.P) & c.s_whole, 1)) {
         if (v) whole<true>();
         else whole<false>();
       } else {
@@ -214,12 +211,13 @@ struct TqStream {
     const int lane = threadIdx.x & 31, r0 = threadIdx.x & 96, in = (1 << a.ps_log2) - 1;
     const uint32_t token = V ? c.vc_token : c.kc_token, s_token = V ? c.vs_token : c.ks_token;
     uint8_t* dst = ring + stage;
+    const uint32_t id[2] = {__shfl_sync(0xffffffffu, (uint32_t)mine, 0), __shfl_sync(0xffffffffu, (uint32_t)mine, 16)};
     const uint32_t o[2] = {(uint32_t)(pos & in), (uint32_t)((pos + 16) & in)};
     const uint8_t* codes = (V ? c.vc + h * c.vc_head : c.kc + h * c.kc_head) + part * C::RB + lane % CPR * 16;
     const uint8_t* scales = (V ? c.vs + h * c.vs_head : c.ks + h * c.ks_head) + part * C::SP;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint8_t* row = codes + (uint64_t)(uint32_t)id[e] * (uint32_t)(V ? c.vc_page : c.kc_page) + (uint64_t)(o[e] + lane / CPR) * token;
+      const uint8_t* row = codes + (uint64_t)id[e] * (uint32_t)(V ? c.vc_page : c.kc_page) + (uint64_t)(o[e] + lane / CPR) * token;
       uint8_t* to = dst + r0 * C::RB + tq_code<C>(lane / CPR, lane % CPR);
 #pragma unroll
       for (int i = 0; i < 16 / RPI; ++i) {
@@ -228,7 +226,7 @@ struct TqStream {
       }
     }
     tq_copy_row<C::SP>(dst + TA_BN * C::RB + (r0 + lane) * C::SP,
-                       scales + (uint64_t)(uint32_t)(lane < 16 ? id[0] : id[1]) * (uint32_t)(V ? c.vs_page : c.ks_page) +
+                       scales + (uint64_t)(uint32_t)mine * (uint32_t)(V ? c.vs_page : c.ks_page) +
                            (uint64_t)((lane < 16 ? o[0] : o[1]) + (lane & 15)) * s_token);
   }
   __device__ __forceinline__ void cut(bool v) {
@@ -240,18 +238,15 @@ struct TqStream {
     const uint8_t* from = (v ? c.vc : c.kc) + h * (v ? c.vc_head : c.kc_head) + part * C::RB + piece * 16;
     const uint8_t* s_from = (v ? c.vs : c.ks) + h * (v ? c.vs_head : c.ks_head) + part * C::SP;
     uint8_t* to = dst + TA_BN * C::RB + (r0 + lane) * C::SP;
-    // a row a lane: its page, read here where pages are smaller
-    int mine = lane < 16 ? id[0] : id[1];
-    const bool seen = pos + lane >= lo && pos + lane < hi;
-    if (a.ps_log2 < 4) mine = seen ? table[(pos + lane) >> a.ps_log2] : -1;
-    const bool there = seen && (uint32_t)mine < (uint32_t)a.P;
+    const bool there = (uint32_t)mine < (uint32_t)a.P;
     const uint64_t off = (uint32_t)((pos + lane) & in);
-    const uint64_t row = (uint64_t)(uint32_t)mine * page + off * token;
-#pragma unroll 1
+    const uint64_t row = there ? (uint64_t)(uint32_t)mine * page + off * token : ~0ull;  // of the lane's own row
+    const int wide = min(max(left / 2 - piece * 16, 0), 16);
+#pragma unroll
     for (int i = 0; i < 32 / RPI; ++i) {
       const int r = i * RPI + lane / CPR;
       const uint64_t at = __shfl_sync(0xffffffffu, row, r);
-      const int bytes = __shfl_sync(0xffffffffu, there, r) ? min(max(left / 2 - piece * 16, 0), 16) : 0;
+      const int bytes = at == ~0ull ? 0 : wide;
       tq_copy16(dst + tq_code<C>(r0 + r, piece), bytes ? from + at : c.kc, bytes);
     }
     s_from += (uint64_t)(uint32_t)mine * s_page + off * s_token;
