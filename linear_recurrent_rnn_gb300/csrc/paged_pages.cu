@@ -163,7 +163,8 @@ struct PagesArgs {
 };
 
 // One bit for every page that the entries free (RELEASE) or use.  A warp takes a row and PP_COLS
-// entries.  A page without other holders is free at once; the others count down, and the one that
+// entries, one such task where the GPU holds as many warps (1024 requests of up to 1000 pages: 15.2 us a release; with a
+// CTA an SM, and three tasks a warp one after another, 19.0).  A page without other holders is free at once; the others count down, and the one that
 // finds none left frees the page: which of them does not matter, as the ring's order is the pages' own.
 template <bool RELEASE>
 __global__ void __launch_bounds__(PP_THREADS) k_paged_mark(const PagesArgs a) {
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(COPY_THREADS) k_paged_copy(const __grid_consta
 }
 
 // ---------------------------------------------------------------- host
-int ctas_for(int64_t work, int per) { return (int)std::min<int64_t>(std::max<int64_t>((work + per - 1) / per, 1), PP_MAX_CTAS); }
+int ctas_for(int64_t work, int per, int most = PP_MAX_CTAS) { return (int)std::min<int64_t>(std::max<int64_t>((work + per - 1) / per, 1), most); }
 
 // holders_out = holders, where they are two
 cudaError_t copy_counts(const int32_t* from, int32_t* to, int n, cudaStream_t stream) {
@@ -521,7 +522,7 @@ extern "C" rglru_status paged_release(const paged_shape* s, const int32_t* first
   a.bits = a.counter + 64;
   cudaError_t e = copy_counts(holders, holders_out, a.P, stream);
   const int64_t tasks = (int64_t)a.N * ((a.width + PP_COLS - 1) / PP_COLS);
-  if (e == cudaSuccess) e = launch(k_paged_mark<true>, ctas_for(tasks, PP_WARPS), a, stream);
+  if (e == cudaSuccess) e = launch(k_paged_mark<true>, ctas_for(tasks, PP_WARPS, 4 * PP_MAX_CTAS), a, stream);
   if (e == cudaSuccess) e = launch(k_paged_freed, ctas_for(a.words, PP_WARPS), a, stream);
   return cuda_status(e);
 }
@@ -554,9 +555,9 @@ extern "C" rglru_status paged_compact(const paged_shape* s, const int32_t* kv_le
   a.bits = a.counter + 64;
   a.rank = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + pages_ws(a.P).rank);
   const int64_t tasks = (int64_t)a.N * ((a.width + PP_COLS - 1) / PP_COLS);
-  cudaError_t e = launch(k_paged_mark<false>, ctas_for(tasks, PP_WARPS), a, stream);
+  cudaError_t e = launch(k_paged_mark<false>, ctas_for(tasks, PP_WARPS, 4 * PP_MAX_CTAS), a, stream);
   if (e == cudaSuccess) e = launch(k_paged_moves, ctas_for(a.words, PP_WARPS), a, stream);
-  if (e == cudaSuccess) e = launch(k_paged_renumber, ctas_for(tasks, PP_WARPS), a, stream);
+  if (e == cudaSuccess) e = launch(k_paged_renumber, ctas_for(tasks, PP_WARPS, 4 * PP_MAX_CTAS), a, stream);
   return cuda_status(e);
 }
 
