@@ -802,7 +802,8 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
             if (F32)
               *reinterpret_cast<uint4*>(dst + (r + R) * 128 + ((c0 / 8 % 8 ^ ((r + R) & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (lane % LPR == 0)
-              s_factor[ni % TA_ITEMS][r] = fminf(a.scale_log2 * __uint_as_float((uint32_t)max(ex - 14 + 127, 1) << 23), FLT_MAX);
+              s_factor[ni % TA_ITEMS][r] =
+                  fminf(fmaxf(a.scale_log2 * __uint_as_float((uint32_t)max(ex - 14 + 127, 1) << 23), FLT_MIN), FLT_MAX);  // (0 times infinity is none)
           }
         }
         tc::fence_proxy_async_smem();

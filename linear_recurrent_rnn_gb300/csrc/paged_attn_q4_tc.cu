@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
             }
             *at(c) = v;
           }
-          s_factor[t * 128 + r] = fminf(a.scale_log2 * __uint_as_float((uint32_t)max(ex - 14 + 127, 1) << 23), FLT_MAX);
+          s_factor[t * 128 + r] =
+              fminf(fmaxf(a.scale_log2 * __uint_as_float((uint32_t)max(ex - 14 + 127, 1) << 23), FLT_MIN), FLT_MAX);  // (0 times infinity is none)
         }
         tc::fence_proxy_async_smem();
         __syncwarp();

@@ -304,6 +304,19 @@ def test_queries_of_any_size(size, io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[(3, 400), (1, 290)], [(300, 900)]])
+def test_scales_that_leave_nothing_of_the_scores(lens, io):
+    """Queries of zero (and tiny ones) with a tiny scale: every key that a row sees weighs the same, behind tiles
+    of which it sees nothing (the rows of a tile see windows that begin in several of them)."""
+    x = build(lens, 4, 2, 64, 16, io, 9)
+    x["q"][:, 0] = 0
+    x["q"][:, 1:] *= 1e-30
+    for scale in (1e-12, 1e-37):
+        o, L, _ = attend(x, scale, 70)
+        compare(o, L, expect(x, scale, 70), io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_attention_repeats_bitwise_and_keeps_its_workspace(io):
     """Many CTAs share a request's keys: a second run on the same workspace, and one on another stream with its
     own, give the same bits."""
