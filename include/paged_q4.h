@@ -16,8 +16,8 @@
  * Arrays.  Codes: [num_pages][page_size][Hkv][D / 2] bytes, channel 2 i in the low half of byte i;
  * scales: [num_pages][page_size][Hkv][D / 16] bytes; each by strides of pages, tokens and heads.
  * Codes lie on 16 bytes and scales on 4 bytes (base and strides); strides of pages and tokens are
- * below 2^32 bytes.  Head by head (a head's tokens
- * of a page next to one another) is the layout that reads fastest: its copies are of whole lines.
+ * below 2^32 bytes.  Head by head (a head's tokens of a page next to one another) is the layout that
+ * reads fastest: its copies are of whole lines.
  *
  * Supported: what paged_attention supports, with 16 <= D <= 256 a multiple of 16; else
  * RGLRU_ERR_UNSUPPORTED.  shape.io is the type of q, k, v and o (bf16 or float32).
@@ -66,9 +66,9 @@ size_t paged_q4_attention_workspace_bytes(const paged_shape *shape);
  * waits that run out.
  * Numerics: keys and values enter the products exactly.  Queries enter as f16, each row times a
  * power of two: exact for bf16 but for elements below 2^-29 of their row's largest; float32 ones as
- * a sum of two (relative 2^-22).  Weights enter as f16 (relative 2^-11; weights below 2^-25 of the row's
- * largest may be lost), float32 ones as a sum of two (2^-22).  Scores, softmax and sums are held in
- * float32. */
+ * a sum of two (relative 2^-22).  Weights enter as f16, off by 2^-11 of themselves or 2^-32 of the
+ * row's largest (2^-36 with up to 32 rows a request), float32 ones as a sum of two (2^-22).  Scores,
+ * softmax and sums are held in float32. */
 rglru_status paged_q4_attention(const paged_shape *shape, const paged_q4_strides *strides,
                                 const void *q, const void *k_codes, const void *k_scales,
                                 const void *v_codes, const void *v_scales,

@@ -22,11 +22,12 @@
 //
 // Warpgroups: softmax; control (a thread that issues S's products, one that issues O's, a warp that walks the
 // items, one that brings queries); 2 that bring keys and 2 that bring values, a unit each in turn.
-// Bound by instructions issued: some 965 a key tile and scheduler, 1400 cycles a tile, most of them the
-// dequantising (a pair of codes a conversion, a product of two with the scale, a store).  That is 3.6 TB/s of codes on
-// long sequences where bf16's kernel reaches 6.1 TB/s of four times the bytes.
-// Measured (GB300): 256 requests of 64 to 8192 keys, 32 heads on 8 of 128, 210 us (the kernel over bf16
-// caches: 287); 64 of 4096 keys, 16 heads on 16, 172 us (314); 152 of 16384 keys on one head, 97 us.
+// Bound by the warps that dequantise: 1390 cycles a key tile of one head of 128, in which a scheduler issues some 800
+// instructions (57 % of its slots); each of its six warps issues in order, ten cycles an instruction, and more warps
+// have no registers.  That is 3.8 TB/s of codes on long sequences, where bf16's kernel reaches 6.1 TB/s of 3.6 times
+// the bytes.
+// Measured (GB300): 256 requests of 64 to 8192 keys, 32 heads on 8 of 128, 197 us (the kernel over bf16
+// caches: 287); 64 of 4096 keys, 16 heads on 16, 164 us (314); 152 of 16384 keys on one head, 94 us.
 // Other ways that were measured: keys from shared memory (a product of 128 x 16 x 16 takes the tensor core 39
 // cycles then, from TMEM 9); TMA and bulk copies of the codes (84 cycles a copy and SM, and a page's codes
 // are 1 KB); warps that only copy, with a barrier between them and those that dequantise (420 us).

@@ -10,11 +10,11 @@
 // held times 2^7; the maximum is moved when a weight would pass 2^15.
 //
 // Width D <= 128: two row tiles a CTA and one warpgroup that brings keys and values; D <= 256: one row tile, two
-// such warpgroups (one: 590 us where two take 390, of 8 chunks of 2048 tokens in 8192, 10 heads on 1, window 2048).
+// such warpgroups (one: 590 us where two take 378, of 8 chunks of 2048 tokens in 8192, 10 heads on 1, window 2048).
 // A second one for D <= 128 needs registers that softmax has: reading the scores twice, so as not to hold 128 of
-// them, took 2161 us where this takes 1825 (8 chunks of 2048 tokens in 8192, 32 heads on 8 of 128).
+// them, took 2161 us where this takes 1823 (8 chunks of 2048 tokens in 8192, 32 heads on 8 of 128).
 // Measured (GB300): that is 1.05 PFLOP/s (1.41 over bf16 caches); 20 decode rows and 4 chunks of 300 to 777 tokens
-// in up to 8192, 117 us.  What bounds it: the one warpgroup's 2250 cycles a unit, of which a key tile has two, against
+// in up to 8192, 116 us.  What bounds it: the one warpgroup's 2250 cycles a unit, of which a key tile has two, against
 // 2048 of products; a lone warp a scheduler issues in order, ten cycles an instruction.
 #include <float.h>
 

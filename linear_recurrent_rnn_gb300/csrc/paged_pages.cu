@@ -163,9 +163,10 @@ struct PagesArgs {
 };
 
 // One bit for every page that the entries free (RELEASE) or use.  A warp takes a row and PP_COLS
-// entries, one such task where the GPU holds as many warps (1024 requests of up to 1000 pages: 15.2 us a release; with a
-// CTA an SM, and three tasks a warp one after another, 19.0).  A page without other holders is free at once; the others count down, and the one that
-// finds none left frees the page: which of them does not matter, as the ring's order is the pages' own.
+// entries, one such task where the GPU holds as many warps (1024 requests of up to 1000 pages: 15.2 us a
+// release; with a CTA an SM, and three tasks a warp one after another, 19.0).  A page without other holders is
+// free at once; the others count down, and the one that finds none left frees the page: which of them does not
+// matter, as the ring's order is the pages' own.
 template <bool RELEASE>
 __global__ void __launch_bounds__(PP_THREADS) k_paged_mark(const PagesArgs a) {
   tc::griddep_wait();
