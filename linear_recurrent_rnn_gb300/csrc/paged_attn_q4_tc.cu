@@ -1,24 +1,28 @@
-// Attention over the paged cache held in 4 bits (include/paged_q4.h), many rows a request (bf16 I/O).
+// Attention over the paged cache held in 4 bits (include/paged_q4.h), many rows a request.
 //
 // The products and the softmax are those of the kernel for many rows over a bf16 cache (paged_attn_tc.cu):
 //   S = Q K^T, P = 2^(c S - c m), O += P V, rows along the 128 lanes, one thread a row.
 // What is new: a warpgroup copies codes and scales (cp.async, its own 32 rows a warp) and writes the
 // numbers that they stand for to the ring of key and value tiles as f16, which holds them exactly; rows that no
-// row of the item sees, and pages that are not there, are zeros there.  Queries come by TMA as bf16 and are
-// rewritten in place as f16, each row times the power of two that brings its largest element to [2^14, 2^15)
-// (bf16's 8 significant bits fit f16's 11); its scores are multiplied by the inverse.  Weights are f16 and
-// held times 2^7; the maximum is moved when a weight would pass 2^15.
+// row of the item sees, and pages that are not there, are zeros there.  Queries come by TMA and are rewritten in
+// place as f16, each row times the power of two that brings its largest element to [2^14, 2^15) (bf16's 8
+// significant bits fit f16's 11); its scores are multiplied by the inverse.  Weights are f16 and held times a
+// power of two; the maximum is moved when a weight would pass 2^15.  float32 queries and weights are sums of two f16
+// (22 bits): each of the two is multiplied with the same keys or values into the same sums, twice the products.
 //
-// Width D <= 128: two row tiles a CTA and one warpgroup that brings keys and values; D <= 256: one row tile, two
-// such warpgroups (one: 590 us where two take 378, of 8 chunks of 2048 tokens in 8192, 10 heads on 1, window 2048).
-// A second one for D <= 128 needs registers that softmax has: reading the scores twice, so as not to hold 128 of
-// them, took 2161 us where this takes 1823 (8 chunks of 2048 tokens in 8192, 32 heads on 8 of 128).
+// bf16 and width D <= 128: two row tiles a CTA and one warpgroup that brings keys and values; else one row tile and two
+// such warpgroups (bf16, one: 590 us where two take 378, of 8 chunks of 2048 tokens in 8192, 10 heads on 1 of 256, window
+// 2048), or one where float32 queries of 256 columns take the shared memory.  A second one beside two row tiles needs
+// registers that softmax has: reading the scores twice, so as not to hold 128 of them, took 2161 us where this takes
+// 1823 (8 chunks of 2048 tokens in 8192, 32 heads on 8 of 128).
 // Measured (GB300): that is 1.05 PFLOP/s (1.41 over bf16 caches); 20 decode rows and 4 chunks of 300 to 777 tokens
 // in up to 8192, 116 us.  What bounds it: the one warpgroup's 2250 cycles a unit, of which a key tile has two, against
-// 2048 of products; a lone warp a scheduler issues in order, ten cycles an instruction.
+// 2048 of products; a lone warp a scheduler issues in order, ten cycles an instruction.  float32, 4 chunks of 700
+// tokens in up to 4096, 16 heads on 4 of 128: 129 us (the kernel for few rows: 510), 10 on 1 of 256: 148 (844).
 #include <float.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "host_util.h"
 #include "paged_q4.cuh"
@@ -27,21 +31,23 @@ namespace rglru {
 
 namespace {
 
-constexpr float TM_SHIFT = 7.0f;  // weights are held times 2^TM_SHIFT, and may grow by 2^8
-
-template <int DP>
+template <int DP, bool F32>
 struct Tm {
-  static constexpr int NT = DP == 256 ? 1 : 2;        // row tiles
-  static constexpr int SLABS = DP / 64;
+  static constexpr int NT = DP == 256 || F32 ? 1 : 2; // row tiles
+  // weights are held times 2^SHIFT, and may grow to 2^15 before a row's sums are scaled anew: rarer with 7, but the
+  // numbers then end at 2^-32 of the largest, with 11 at 2^-36
+  static constexpr float SHIFT = F32 ? 11.0f : 7.0f;
+  static constexpr int NUM = F32 ? 2 : 1;             // f16 numbers for one of a query or weight
+  static constexpr int SLABS = NUM * DP / 64;         // 64 columns of f16, of either number in turn
   // Units: 128 keys (or values) of up to 128 columns; what is copied, dequantised and multiplied at once.
   static constexpr int UNITS = DP == 256 ? 2 : 1;     // of a tile
   static constexpr int COL = DP / UNITS;              // columns of one
   static constexpr uint32_t RB = COL / 2, SP = COL / 16;  // bytes of a row's codes, of its scales
   static constexpr uint32_t SB = 1024 * ((TA_BN * (RB + SP) + 1023) / 1024);  // a unit's
   static constexpr uint32_t UB = TA_BN * COL * 2;     // of a unit as f16
-  static constexpr int STAGES = DP == 64 ? 6 : 3;     // units as f16
+  static constexpr int STAGES = DP == 64 ? 6 : DP == 256 && F32 ? 2 : 3;  // units as f16
   static constexpr int SOFT = NT * 128;               // softmax threads
-  static constexpr int GROUPS = NT == 2 ? 1 : 2;      // warpgroups that bring keys and values, a unit each in turn
+  static constexpr int GROUPS = NT == 2 || (DP == 256 && F32) ? 1 : 2;  // warpgroups that bring keys and values, a unit each in turn
   static constexpr int THREADS = SOFT + 128 + GROUPS * 128;
   static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P buffers b at 128 b, O tiles
   static constexpr size_t Q_BYTES = (size_t)NT * SLABS * TA_SLAB;
@@ -51,11 +57,12 @@ struct Tm {
   static_assert(DEPTH >= 2 && GROUPS <= STAGES, "shared memory");
 };
 
-template <int DP>
-__global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
+template <int DP, bool F32>
+__global__ void __launch_bounds__(Tm<DP, F32>::THREADS, 1)
     k_paged_attn_q4_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ PagedArgs a,
                        const __grid_constant__ Q4Cache cache) {
-  using C = Tm<DP>;
+  using C = Tm<DP, F32>;
+  using IO = std::conditional_t<F32, float, bf16>;
   constexpr int NT = C::NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -157,7 +164,8 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
     if (lane == 0) tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
     ++ni;
   };
-  // Registers: 512 threads x 128 at launch = 256 x 184 + 256 x 72 (one row tile: 128 x 224 + 384 x 96)
+  // Registers: 512 threads x 128 at launch = 256 x 184 + 256 x 72 (one row tile: 128 x 224 + 384 x 96, or 384
+  // threads x 168 = 128 x 224 + 256 x 136)
   // after the warpgroups of softmax have taken what the others give up.
   if (role < 0) {
     if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
@@ -220,7 +228,7 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
                                     fmaxf(mx[2], mx[3]));
           if (j == tl.ja) {
             m = top;
-          } else if (__any_sync(0xffffffffu, r < tl.rows && (top - m) * sc > 8.0f)) {  // (of rows in use)
+          } else if (__any_sync(0xffffffffu, r < tl.rows && (top - m) * sc > 15.0f - C::SHIFT)) {  // (of rows in use)
             const float f = top == m ? 1.0f : ta_ex2((top - m) * -sc);
             l *= f;
             m = top;
@@ -241,20 +249,23 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
               tc::tmem_st16(t_o + c, o);
             }
           }
-          const float off = m == -INFINITY ? 0.0f : fmaf(-m, sc, TM_SHIFT);
+          const float off = m == -INFINITY ? 0.0f : fmaf(-m, sc, C::SHIFT);
           float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
           for (int c = 0; c < 128; c += 32) {
-            float pk[16];
+            float pk[16], pl[16];  // and what is left of float32 ones
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 x = ta_fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), make_float2(sc, sc),
                                        make_float2(off, off));
               const float2 p = make_float2(ta_ex2(x.x), ta_ex2(x.y));
               sum[e & 1] = ta_add2(sum[e & 1], p);
-              pk[e] = __uint_as_float(tq_pack(p.x, p.y));
+              const uint32_t hi = tq_pack(p.x, p.y);
+              pk[e] = __uint_as_float(hi);
+              if (F32) pl[e] = __uint_as_float(tq_rest(p.x, p.y, hi));
             }
             tc::tmem_st16(t_s + c / 2, pk);
+            if (F32) tc::tmem_st16(t_s + 64 + c / 2, pl);
           }
           const float2 s2 = ta_add2(sum[0], sum[1]);
           l += s2.x + s2.y;
@@ -302,12 +313,12 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
       const float2* g_ml = reinterpret_cast<const float2*>(a.ws + a.part_ml);
       const float* g_o = reinterpret_cast<const float*>(a.ws + a.part_o);
       // (rounded here as in memory, whichever of the two it is joined from)
-      const float2 own = make_float2(m == -INFINITY ? m : fmaf(m, sc, -TM_SHIFT), l);
+      const float2 own = make_float2(m == -INFINITY ? m : fmaf(m, sc, -C::SHIFT), l);
       if (here) {
         if (live) {
           const int64_t tok = it.first + tl.tok + my_tok;
           const int hq = it.h * a.g + min(r, tl.rows - 1) - my_tok * a.g;
-          bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
+          IO* o = static_cast<IO*>(a.o) + tok * a.o_token + hq * a.o_head;
           float top = own.x, sum = l;
           auto part = [&](int q) { return q == (int)blockIdx.x ? own : __ldcg(g_ml + (size_t)PgWalk::slot(q, it.c0) * R + row); };
           if (parts > 1) {
@@ -353,20 +364,29 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[e] = acc[e];
             }
-            uint32_t u[16];
+            if constexpr (F32) {
+              if (mine)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              u[e] = sum == 0.0f ? 0u : ta_pack(v[2 * e] * inv, v[2 * e + 1] * inv);
-            if (mine) {
-              if (a.o_32) {  // whole 32-byte sectors a store: half as many passes through L1
-                ta_store32(o + c, u);
-                if (c + 16 < a.D) ta_store32(o + c + 16, u + 8);
-              } else {
+                for (int e = 0; e < 32; e += 4)
+                  if (c + e < a.D)
+                    *reinterpret_cast<float4*>(o + c + e) = sum == 0.0f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                                        : make_float4(v[e] * inv, v[e + 1] * inv, v[e + 2] * inv, v[e + 3] * inv);
+            } else {
+              uint32_t u[16];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (c + 8 * e < a.D)
-                    *reinterpret_cast<uint4*>(o + c + 8 * e) =
-                        make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+              for (int e = 0; e < 16; ++e)
+                u[e] = sum == 0.0f ? 0u : ta_pack(v[2 * e] * inv, v[2 * e + 1] * inv);
+              if (mine) {
+                if (a.o_32) {  // whole 32-byte sectors a store: half as many passes through L1
+                  ta_store32(o + c, u);
+                  if (c + 16 < a.D) ta_store32(o + c + 16, u + 8);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    if (c + 8 * e < a.D)
+                      *reinterpret_cast<uint4*>(o + c + 8 * e) =
+                          make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+                }
               }
             }
           }
@@ -422,14 +442,15 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
         ++nj;
         if (*reinterpret_cast<volatile uint32_t*>(s_last)) {
           __threadfence();
-          ta_join<DP>(a, it, tb1, tid);
+          ta_join<DP, IO, NT>(a, it, tb1, tid);
         }
       }
       done_item();
     }
   } else {
     if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    else if (C::GROUPS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
     if (role == 3) {
       // ------------------------------------------------------------ walk, and queries
       uint32_t n[NT] = {};  // query loads
@@ -469,7 +490,7 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
             if (lane == 0) {
               tc::mbar_expect_tx(&q_full[t], bytes);
               for (int s = 0; s < C::SLABS; ++s)
-                tc::tma_load_3d(s_q + (t * C::SLABS + s) * TA_SLAB, &tm_q, &q_full[t], s * 64, x.h * a.g,
+                tc::tma_load_3d(s_q + (t * C::SLABS + s) * TA_SLAB, &tm_q, &q_full[t], s * (F32 ? 32 : 64), x.h * a.g,
                                 x.first + tl.tok);
             }
             ++n[t];
@@ -497,28 +518,48 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
         for (int r = first + lane; r < first + rows; r += 32) {
           uint8_t* row = s_q + (size_t)t * C::SLABS * TA_SLAB + r * 128;
           auto at = [&](int c) { return reinterpret_cast<uint4*>(row + c / 8 * TA_SLAB + ((c % 8 ^ (r & 7)) << 4)); };
-          uint32_t top = 0;
+          uint32_t top = 0;  // the largest, as a float's bits without the sign
 #pragma unroll 4
           for (int c = 0; c < C::SLABS * 8; ++c) {
             const uint4 v = *at(c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t x = (&v.x)[e] & 0x7fff7fffu;
-              top = max(top, max(x & 0xffffu, x >> 16));
+              const uint32_t x = (&v.x)[e] & (F32 ? 0x7fffffffu : 0x7fff7fffu);
+              top = max(top, F32 ? x : max(x << 16, x & 0xffff0000u));
             }
           }
           // the row's power of two, within what float32 holds; 1 where the row is not finite
-          const int ex = top >= 0x7f80u ? 14 : max((int)(top >> 7) - 127, -112);
+          const int ex = top >= 0x7f800000u ? 14 : max((int)(top >> 23) - 127, -112);
           const float f = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-#pragma unroll 4
-          for (int c = 0; c < C::SLABS * 8; ++c) {
-            uint4 v = *at(c);
+          if constexpr (F32) {
+            // 64 columns: two slabs of float32 become one of f16 numbers and one of what is left of them
+#pragma unroll 1
+            for (int c0 = 0; c0 < C::SLABS * 8; c0 += 16) {
+              uint32_t y[64];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t& x = (&v.x)[e];
-              x = tq_pack(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+              for (int c = 0; c < 16; ++c) {
+                const uint4 v = *at(c0 + c);
+                const float x[4] = {__uint_as_float(v.x) * f, __uint_as_float(v.y) * f, __uint_as_float(v.z) * f, __uint_as_float(v.w) * f};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  y[2 * c + e] = tq_pack(x[2 * e], x[2 * e + 1]);
+                  y[32 + 2 * c + e] = tq_rest(x[2 * e], x[2 * e + 1], y[2 * c + e]);
+                }
+              }
+#pragma unroll
+              for (int c = 0; c < 16; ++c) *at(c0 + c) = make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
             }
-            *at(c) = v;
+          } else {
+#pragma unroll 4
+            for (int c = 0; c < C::SLABS * 8; ++c) {
+              uint4 v = *at(c);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t& x = (&v.x)[e];
+                x = tq_pack(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+              }
+              *at(c) = v;
+            }
           }
           s_factor[t * 128 + r] =
               fminf(fmaxf(a.scale_log2 * __uint_as_float((uint32_t)max(ex - 14 + 127, 1) << 23), FLT_MIN), FLT_MAX);  // (0 times infinity is none)
@@ -586,17 +627,20 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
               ++cs[t];
               tc::tc_fence_after();
 #pragma unroll
-              for (int k = 0; k < DP / 16; ++k) {
-                if (NT == 1 && k % 8 == 0) {
-                  ok = ctl.wait1(&full[k_st[k / 8]], k_par[k / 8]);
+              for (int u = 0; u < C::UNITS; ++u) {
+                if (NT == 1) {
+                  ok = ctl.wait1(&full[k_st[u]], k_par[u]);
                   if (!ok) return;
                   tc::tc_fence_after();
                 }
-                tc::mma_bf16(tmem + C::S_COL + b * 128,
-                             d_q + (((t * C::SLABS + k / 4) * TA_SLAB + k % 4 * 32) >> 4),
-                             d_k + ((k_st[k / 8] * C::UB + k % 8 / 4 * TA_SLAB + k % 4 * 32) >> 4),
-                             id_qk, k > 0);
-                if (NT == 1 && k % 8 == 7) tc::mma_commit(&empty[k_st[k / 8]]);  // a unit is free once read
+#pragma unroll
+                for (int k = 0; k < C::COL / 16; ++k)
+#pragma unroll
+                  for (int x = 0; x < C::NUM; ++x)
+                    tc::mma_bf16(tmem + C::S_COL + b * 128,
+                                 d_q + (((t * C::SLABS + (u * C::COL / 64 + k / 4) * C::NUM + x) * TA_SLAB + k % 4 * 32) >> 4),
+                                 d_k + ((k_st[u] * C::UB + k / 4 * TA_SLAB + k % 4 * 32) >> 4), id_qk, u + k + x > 0);
+                if (NT == 1) tc::mma_commit(&empty[k_st[u]]);  // a unit is free once read
               }
               tc::mma_commit(&s_full[b]);
               if (j == tl[t].jb - 1) tc::mma_commit(&q_empty[t]);
@@ -619,8 +663,10 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
                 }
 #pragma unroll
                 for (int k = 0; k < TA_BN / 16; ++k)
-                  tc::mma_ts(tmem + C::O_COL + t * DP + u * C::COL, tmem + C::S_COL + b * 128 + k * 8,
-                             d_v + ((v_st[u] * C::UB + k * 2048) >> 4), id_pv, k > 0 ? 1u : more);
+#pragma unroll
+                  for (int x = 0; x < C::NUM; ++x)
+                    tc::mma_ts(tmem + C::O_COL + t * DP + u * C::COL, tmem + C::S_COL + b * 128 + x * 64 + k * 8,
+                               d_v + ((v_st[u] * C::UB + k * 2048) >> 4), id_pv, k + x > 0 ? 1u : more);
                 if (NT == 1) tc::mma_commit(&empty[v_st[u]]);
               }
               tc::mma_commit(&pv_done[t]);
@@ -693,20 +739,21 @@ __global__ void __launch_bounds__(Tm<DP>::THREADS, 1)
   }
 }
 
-template <int DP>
+template <int DP, bool F32>
 cudaError_t run(PagedArgs& a, const Q4Cache& c, cudaStream_t s, int sms) {
-  using C = Tm<DP>;
+  using C = Tm<DP, F32>;
   const int tb1 = std::max(1, 128 / a.g);
   CUtensorMap mq;
   const uint64_t dq[3] = {(uint64_t)a.D, (uint64_t)a.Hq, (uint64_t)a.T};
-  const uint64_t sq[2] = {(uint64_t)a.q_head * 2, (uint64_t)a.q_token * 2};
-  const uint32_t bq[3] = {64, (uint32_t)a.g, (uint32_t)tb1};
-  cudaError_t e = encode_tmap(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B);
+  constexpr uint64_t size = F32 ? 4 : 2;
+  const uint64_t sq[2] = {(uint64_t)a.q_head * size, (uint64_t)a.q_token * size};
+  const uint32_t bq[3] = {F32 ? 32 : 64, (uint32_t)a.g, (uint32_t)tb1};
+  cudaError_t e = encode_tmap(&mq, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  const void* f = reinterpret_cast<const void*>(k_paged_attn_q4_tc<DP>);
+  const void* f = reinterpret_cast<const void*>(k_paged_attn_q4_tc<DP, F32>);
   static std::atomic<uint64_t> ready{0};
   // the register split draws on what the launch gives
-  e = ta_prepare(f, C::smem, 128, ready);
+  e = ta_prepare(f, C::smem, C::THREADS == 384 ? 166 : 128, ready);
   if (e != cudaSuccess) return e;
   const PagedWs L = paged_ws(sms, C::NT * 128, DP);
   a.part_ml = L.ml;
@@ -724,19 +771,19 @@ cudaError_t run(PagedArgs& a, const Q4Cache& c, cudaStream_t s, int sms) {
 
 }  // namespace
 
-cudaError_t launch_paged_attn_q4_tc(PagedArgs a, const Q4Cache& c, cudaStream_t s) {
+cudaError_t launch_paged_attn_q4_tc(PagedArgs a, const Q4Cache& c, bool f32, cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1 || sms > PG_MAX_CTAS) return cudaErrorNotSupported;
   switch (ta_width(a.D)) {
-    case 64: return run<64>(a, c, s, sms);
-    case 128: return run<128>(a, c, s, sms);
-    default: return run<256>(a, c, s, sms);
+    case 64: return f32 ? run<64, true>(a, c, s, sms) : run<64, false>(a, c, s, sms);
+    case 128: return f32 ? run<128, true>(a, c, s, sms) : run<128, false>(a, c, s, sms);
+    default: return f32 ? run<256, true>(a, c, s, sms) : run<256, false>(a, c, s, sms);
   }
 }
 
 size_t paged_attn_q4_tc_ws_bytes(const paged_shape* s) {
   const int sms = sm_count(), dp = ta_width(s->D);
-  return paged_ws(sms > 0 ? sms : 256, dp == 256 ? 128 : 256, dp).total;
+  return paged_ws(sms > 0 ? sms : 256, dp == 256 || s->io == RGLRU_F32 ? 128 : 256, dp).total;
 }
 
 }  // namespace rglru

@@ -279,8 +279,10 @@ int mean_rows(const paged_shape* s) {
   return (int)std::min<int64_t>(((int64_t)s->tokens + s->num_seqs - 1) / s->num_seqs * (s->Hq / s->Hkv), 1 << 30);
 }
 
-// Which of the two kernels (paged_attention's rule for a bf16 cache, at half as many rows).
-bool many_rows(const paged_shape* s) { return s->io == RGLRU_BF16 && mean_rows(s) > TQ_FEW_ROWS; }
+// Which of the two kernels.
+bool many_rows(const paged_shape* s) {
+  return mean_rows(s) > (s->io == RGLRU_BF16 ? TQ_FEW_ROWS : s->D > 128 ? TQ_FEW_ROWS_F32_WIDE : TQ_FEW_ROWS_F32);
+}
 
 // Write (k and v read) and read (k and v written).
 rglru_status rows_call(const paged_shape* s, const paged_q4_strides* strides, const void* k, const void* v, const int64_t* slots,
@@ -404,6 +406,6 @@ extern "C" rglru_status paged_q4_attention(const paged_shape* s, const paged_q4_
   const Q4Cache c = {static_cast<const uint8_t*>(k_codes), static_cast<const uint8_t*>(k_scales), static_cast<const uint8_t*>(v_codes),
                      static_cast<const uint8_t*>(v_scales), t.kc_page, t.kc_token, t.kc_head, t.vc_page, t.vc_token, t.vc_head,
                      t.ks_page, t.ks_token, t.ks_head, t.vs_page, t.vs_token, t.vs_head, 0, 1};
-  if (many_rows(s)) return cuda_status(launch_paged_attn_q4_tc(a, c, stream));
+  if (many_rows(s)) return cuda_status(launch_paged_attn_q4_tc(a, c, s->io == RGLRU_F32, stream));
   return cuda_status(launch_paged_attn_q4(a, c, s->io == RGLRU_F32, mean_rows(s), stream));
 }

@@ -339,10 +339,10 @@ __device__ __forceinline__ uint32_t ta_bits(int h) { return h < 0 ? 0u : h >= 31
 
 // One row's results joined over the CTAs [c0, c1] of an item, by all softmax threads: a thread
 // takes one row and a run of columns.
-template <int DP>
+template <int DP, class IO = bf16, int NT = DP == 256 ? 1 : 2>
 __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int tb1, int tid) {
   const int c0 = it.c0, c1 = it.c1;
-  constexpr int NT = DP == 256 ? 1 : 2, SOFT = NT * 128;  // row tiles, threads
+  constexpr int SOFT = NT * 128;  // threads (NT: row tiles)
   const float2* ml = reinterpret_cast<const float2*>(a.ws + a.part_ml);
   const float* po = reinterpret_cast<const float*>(a.ws + a.part_o);
   const int R = NT * 128;
@@ -369,7 +369,7 @@ __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int t
   const int t = row >> 7, r = row & 127;
   const int64_t tok = it.first + it.tok + t * tb1 + pg_token(a, r);
   const int hq = it.h * a.g + r - pg_token(a, r) * a.g;
-  bf16* o = static_cast<bf16*>(a.o) + tok * a.o_token + hq * a.o_head;
+  IO* o = static_cast<IO*>(a.o) + tok * a.o_token + hq * a.o_head;
   constexpr int W = 16;  // columns at a time: with two parts, 32 loads in flight
 #pragma unroll 1
   for (int k = col0; k < col0 + cols && k < a.D; k += W) {
@@ -389,10 +389,16 @@ __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int t
     }
 #pragma unroll
     for (int e = 0; e < W; e += 8)
-      if (k + e < a.D && k + e < col0 + cols)
+      if (k + e < a.D && k + e < col0 + cols) {
+        if constexpr (sizeof(IO) == 4) {
+          reinterpret_cast<float4*>(o + k + e)[0] = make_float4(acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
+          reinterpret_cast<float4*>(o + k + e)[1] = make_float4(acc[e + 4] * inv, acc[e + 5] * inv, acc[e + 6] * inv, acc[e + 7] * inv);
+          continue;
+        }
         *reinterpret_cast<uint4*>(o + k + e) =
             make_uint4(ta_pack(acc[e] * inv, acc[e + 1] * inv), ta_pack(acc[e + 2] * inv, acc[e + 3] * inv),
                        ta_pack(acc[e + 4] * inv, acc[e + 5] * inv), ta_pack(acc[e + 6] * inv, acc[e + 7] * inv));
+      }
   }
   if (a.lse && col0 == 0)
     a.lse[tok * a.Hq + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;

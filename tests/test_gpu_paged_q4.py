@@ -252,6 +252,10 @@ CASES = {
     "group-64": ([(3, 140), (1, 500)], 64, 1, 128, 16, 0),
     "group-33": ([(1, 140), (2, 300)], 66, 2, 64, 16, 0),
     "group-17-long": ([(60, 200), (2, 300)], 17, 1, 256, 16, 40),
+    "group-12": ([(1, 500), (1, 33), (1, 1)], 12, 1, 128, 16, 0),
+    "group-12-64": ([(1, 500), (1, 129)], 24, 2, 64, 32, 200),
+    "group-20-256": ([(1, 300), (1, 40)], 20, 1, 256, 16, 0),
+    "group-40-192": ([(1, 700), (0, 9), (1, 127)], 40, 1, 192, 8, 0),
     "page-4096": ([(3, 5000)], 2, 1, 64, 4096, 0),
     "mixed": ([(1, 350)] * 6 + [(160, 320), (1, 1), (77, 900)], 8, 1, 128, 16, 256),
 }
