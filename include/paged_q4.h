@@ -67,7 +67,7 @@ size_t paged_q4_attention_workspace_bytes(const paged_shape *shape);
  * Numerics: keys and values enter the products exactly.  Queries enter as f16, each row times a
  * power of two: exact for bf16 but for elements below 2^-29 of their row's largest; float32 ones as
  * a sum of two (relative 2^-22).  Weights enter as f16, off by 2^-11 of themselves or 2^-32 of the
- * row's largest (2^-36 with up to 32 rows a request), float32 ones as a sum of two (2^-22, or 2^-36
+ * row's largest (2^-36 with up to 16 rows a request), float32 ones as a sum of two (2^-22, or 2^-36
  * of the row's largest).  Scores, softmax and sums are held in float32. */
 rglru_status paged_q4_attention(const paged_shape *shape, const paged_q4_strides *strides,
                                 const void *q, const void *k_codes, const void *k_scales,

@@ -857,12 +857,9 @@ int tile_rows(bool f32, int rows) {
 template <int DP>
 cudaError_t run_rows(PagedArgs& a, const Q4Cache& c, bool f32, int rows, cudaStream_t s, int sms) {
   if (f32) return rows == 8 ? run<DP, 8, true>(a, c, s, sms) : run<DP, 16, true>(a, c, s, sms);
-  switch (rows) {
-    case 4: return run<DP, 4, false>(a, c, s, sms);
-    case 8: return run<DP, 8, false>(a, c, s, sms);
-    case 16: return run<DP, 16, false>(a, c, s, sms);
-    default: return run<DP, 32, false>(a, c, s, sms);
-  }
+  if constexpr (DP == 256)  // (narrower heads have their many rows elsewhere)
+    if (rows == 32) return run<DP, 32, false>(a, c, s, sms);
+  return rows == 4 ? run<DP, 4, false>(a, c, s, sms) : rows == 8 ? run<DP, 8, false>(a, c, s, sms) : run<DP, 16, false>(a, c, s, sms);
 }
 
 }  // namespace

@@ -10,15 +10,16 @@
 // power of two; the maximum is moved when a weight would pass 2^15.  float32 queries and weights are sums of two f16
 // (22 bits): each of the two is multiplied with the same keys or values into the same sums, twice the products.
 //
-// bf16 and width D <= 128: two row tiles a CTA and one warpgroup that brings keys and values; else one row tile and two
-// such warpgroups (bf16, one: 590 us where two take 378, of 8 chunks of 2048 tokens in 8192, 10 heads on 1 of 256, window
-// 2048), or one where float32 queries of 256 columns take the shared memory.  A second one beside two row tiles needs
-// registers that softmax has: reading the scores twice, so as not to hold 128 of them, took 2161 us where this takes
-// 1823 (8 chunks of 2048 tokens in 8192, 32 heads on 8 of 128).
-// Measured (GB300): that is 1.05 PFLOP/s (1.41 over bf16 caches); 20 decode rows and 4 chunks of 300 to 777 tokens
-// in up to 8192, 116 us.  What bounds it: the one warpgroup's 2250 cycles a unit, of which a key tile has two, against
-// 2048 of products; a lone warp a scheduler issues in order, ten cycles an instruction.  float32, 4 chunks of 700
-// tokens in up to 4096, 16 heads on 4 of 128: 129 us (the kernel for few rows: 510), 10 on 1 of 256: 148 (844).
+// Widths up to 128: one row tile a CTA and two warpgroups that bring keys and values, or, for long prompts in bf16, two
+// row tiles and one (row_tiles below; a second beside two tiles needs registers that softmax has: reading the
+// scores twice, so as not to hold 128 of them, took 2161 us where this takes 1822, of 8 chunks of 2048 tokens in 8192, 32
+// heads on 8 of 128).  Width 256: one row tile and three (8 chunks of 2048 tokens in 8192, 10 heads on 1, window 2048:
+// 590 us with one, 377 with two, 340 with three), or one where float32 queries take the shared memory.
+// Measured (GB300): those chunks 1.05 PFLOP/s (1.41 over bf16 caches), with heads of 256 1.01; 20 decode rows and 4
+// chunks of 300 to 777 tokens in up to 8192, 104 us.  What bounds it: a warpgroup's 2250 cycles a unit, of which a key
+// tile has two, against 1024 of products a row tile; a lone warp a scheduler issues in order, ten cycles an
+// instruction.  float32, 4 chunks of 700 tokens in up to 4096, 16 heads on 4 of 128: 129 us (the kernel for few rows: 510),
+// 10 on 1 of 256: 148 (844).
 #include <float.h>
 
 #include <algorithm>
@@ -31,9 +32,9 @@ namespace rglru {
 
 namespace {
 
-template <int DP, bool F32>
+template <int DP, bool F32, int NT_>
 struct Tm {
-  static constexpr int NT = DP == 256 || F32 ? 1 : 2; // row tiles
+  static constexpr int NT = NT_;                      // row tiles
   // weights are held times 2^SHIFT, and may grow to 2^15 before a row's sums are scaled anew: rarer with 7, but the
   // numbers then end at 2^-32 of the largest, with 11 at 2^-36
   static constexpr float SHIFT = F32 ? 11.0f : 7.0f;
@@ -47,8 +48,13 @@ struct Tm {
   static constexpr uint32_t UB = TA_BN * COL * 2;     // of a unit as f16
   static constexpr int STAGES = DP == 64 ? 6 : DP == 256 && F32 ? 2 : 3;  // units as f16
   static constexpr int SOFT = NT * 128;               // softmax threads
-  static constexpr int GROUPS = NT == 2 || (DP == 256 && F32) ? 1 : 2;  // warpgroups that bring keys and values, a unit each in turn
+  // warpgroups that bring keys and values, a unit each in turn
+  static constexpr int GROUPS = NT == 2 || (DP == 256 && F32) ? 1 : DP == 256 ? 3 : 2;
   static constexpr int THREADS = SOFT + 128 + GROUPS * 128;
+  // Registers of a thread: at launch, and after the softmax's warpgroups have taken what the others give up.
+  static constexpr int REGS = 65536 / THREADS / 8 * 8;
+  static constexpr int SOFT_REGS = NT == 2 ? 184 : GROUPS == 3 ? 192 : 224;
+  static constexpr int OTHER_REGS = (REGS * THREADS - SOFT_REGS * SOFT) / (THREADS - SOFT) / 8 * 8;
   static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P buffers b at 128 b, O tiles
   static constexpr size_t Q_BYTES = (size_t)NT * SLABS * TA_SLAB;
   static constexpr int FIT = (int)((232448 - 4096 - 1024 - Q_BYTES - STAGES * UB - 1024) / SB);
@@ -57,11 +63,11 @@ struct Tm {
   static_assert(DEPTH >= 2 && GROUPS <= STAGES, "shared memory");
 };
 
-template <int DP, bool F32>
-__global__ void __launch_bounds__(Tm<DP, F32>::THREADS, 1)
+template <int DP, bool F32, int NT_>
+__global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
     k_paged_attn_q4_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ PagedArgs a,
                        const __grid_constant__ Q4Cache cache) {
-  using C = Tm<DP, F32>;
+  using C = Tm<DP, F32, NT_>;
   using IO = std::conditional_t<F32, float, bf16>;
   constexpr int NT = C::NT;
   extern __shared__ uint8_t smem_raw[];
@@ -164,12 +170,8 @@ __global__ void __launch_bounds__(Tm<DP, F32>::THREADS, 1)
     if (lane == 0) tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
     ++ni;
   };
-  // Registers: 512 threads x 128 at launch = 256 x 184 + 256 x 72 (one row tile: 128 x 224 + 384 x 96, or 384
-  // threads x 168 = 128 x 224 + 256 x 136)
-  // after the warpgroups of softmax have taken what the others give up.
   if (role < 0) {
-    if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFT_REGS));
     // ------------------------------------------------------------ softmax, one row a thread
     const int t = NT == 2 ? warp >> 2 : 0, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
@@ -448,9 +450,7 @@ __global__ void __launch_bounds__(Tm<DP, F32>::THREADS, 1)
       done_item();
     }
   } else {
-    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else if (C::GROUPS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (role == 3) {
       // ------------------------------------------------------------ walk, and queries
       uint32_t n[NT] = {};  // query loads
@@ -739,9 +739,9 @@ __global__ void __launch_bounds__(Tm<DP, F32>::THREADS, 1)
   }
 }
 
-template <int DP, bool F32>
+template <int DP, bool F32, int NT>
 cudaError_t run(PagedArgs& a, const Q4Cache& c, cudaStream_t s, int sms) {
-  using C = Tm<DP, F32>;
+  using C = Tm<DP, F32, NT>;
   const int tb1 = std::max(1, 128 / a.g);
   CUtensorMap mq;
   const uint64_t dq[3] = {(uint64_t)a.D, (uint64_t)a.Hq, (uint64_t)a.T};
@@ -750,10 +750,10 @@ cudaError_t run(PagedArgs& a, const Q4Cache& c, cudaStream_t s, int sms) {
   const uint32_t bq[3] = {F32 ? 32 : 64, (uint32_t)a.g, (uint32_t)tb1};
   cudaError_t e = encode_tmap(&mq, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  const void* f = reinterpret_cast<const void*>(k_paged_attn_q4_tc<DP, F32>);
+  const void* f = reinterpret_cast<const void*>(k_paged_attn_q4_tc<DP, F32, NT>);
   static std::atomic<uint64_t> ready{0};
   // the register split draws on what the launch gives
-  e = ta_prepare(f, C::smem, C::THREADS == 384 ? 166 : 128, ready);
+  e = ta_prepare(f, C::smem, C::REGS, ready);
   if (e != cudaSuccess) return e;
   const PagedWs L = paged_ws(sms, C::NT * 128, DP);
   a.part_ml = L.ml;
@@ -769,21 +769,26 @@ cudaError_t run(PagedArgs& a, const Q4Cache& c, cudaStream_t s, int sms) {
   return launch_pdl(f, dim3(sms), dim3(C::THREADS), C::smem, s, args, 1);
 }
 
+// Row tiles of a CTA.  Measured (bf16, one against two): heads of 128, mean rows of a request 48 98 and 145 us, 717 104 and
+// 116, 1024 155 and 156, 5200 135 and 129, 8192 1919 and 1822; heads of 64, 358 98 and 99, 1536 189 and 159, 8192 845 and 694.
+int row_tiles(bool f32, int D, int rows) { return !f32 && D <= 128 && rows > 1024 ? 2 : 1; }
+
 }  // namespace
 
-cudaError_t launch_paged_attn_q4_tc(PagedArgs a, const Q4Cache& c, bool f32, cudaStream_t s) {
+cudaError_t launch_paged_attn_q4_tc(PagedArgs a, const Q4Cache& c, bool f32, int rows, cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1 || sms > PG_MAX_CTAS) return cudaErrorNotSupported;
+  const bool two = row_tiles(f32, a.D, rows) == 2;
   switch (ta_width(a.D)) {
-    case 64: return f32 ? run<64, true>(a, c, s, sms) : run<64, false>(a, c, s, sms);
-    case 128: return f32 ? run<128, true>(a, c, s, sms) : run<128, false>(a, c, s, sms);
-    default: return f32 ? run<256, true>(a, c, s, sms) : run<256, false>(a, c, s, sms);
+    case 64: return f32 ? run<64, true, 1>(a, c, s, sms) : two ? run<64, false, 2>(a, c, s, sms) : run<64, false, 1>(a, c, s, sms);
+    case 128: return f32 ? run<128, true, 1>(a, c, s, sms) : two ? run<128, false, 2>(a, c, s, sms) : run<128, false, 1>(a, c, s, sms);
+    default: return f32 ? run<256, true, 1>(a, c, s, sms) : run<256, false, 1>(a, c, s, sms);
   }
 }
 
-size_t paged_attn_q4_tc_ws_bytes(const paged_shape* s) {
-  const int sms = sm_count(), dp = ta_width(s->D);
-  return paged_ws(sms > 0 ? sms : 256, dp == 256 || s->io == RGLRU_F32 ? 128 : 256, dp).total;
+size_t paged_attn_q4_tc_ws_bytes(const paged_shape* s, int rows) {
+  const int sms = sm_count();
+  return paged_ws(sms > 0 ? sms : 256, row_tiles(s->io == RGLRU_F32, s->D, rows) * 128, ta_width(s->D)).total;
 }
 
 }  // namespace rglru

@@ -281,7 +281,7 @@ int mean_rows(const paged_shape* s) {
 
 // Which of the two kernels.
 bool many_rows(const paged_shape* s) {
-  return mean_rows(s) > (s->io == RGLRU_BF16 ? TQ_FEW_ROWS : s->D > 128 ? TQ_FEW_ROWS_F32_WIDE : TQ_FEW_ROWS_F32);
+  return mean_rows(s) > (s->D <= 128 ? TQ_FEW_ROWS : s->io == RGLRU_BF16 ? TQ_FEW_ROWS_WIDE : TQ_FEW_ROWS_WIDE_F32);
 }
 
 // Write (k and v read) and read (k and v written).
@@ -355,7 +355,7 @@ extern "C" rglru_status paged_q4_read(const paged_shape* s, const paged_q4_strid
 
 extern "C" size_t paged_q4_attention_workspace_bytes(const paged_shape* s) {
   if (pg_check_cache(s) != RGLRU_OK || check_heads(s) != RGLRU_OK || check_queries(s) != RGLRU_OK) return 0;
-  return many_rows(s) ? paged_attn_q4_tc_ws_bytes(s) : paged_attn_q4_ws_bytes(s, mean_rows(s));
+  return many_rows(s) ? paged_attn_q4_tc_ws_bytes(s, mean_rows(s)) : paged_attn_q4_ws_bytes(s, mean_rows(s));
 }
 
 extern "C" rglru_status paged_q4_attention(const paged_shape* s, const paged_q4_strides* strides, const void* q,
@@ -406,6 +406,6 @@ extern "C" rglru_status paged_q4_attention(const paged_shape* s, const paged_q4_
   const Q4Cache c = {static_cast<const uint8_t*>(k_codes), static_cast<const uint8_t*>(k_scales), static_cast<const uint8_t*>(v_codes),
                      static_cast<const uint8_t*>(v_scales), t.kc_page, t.kc_token, t.kc_head, t.vc_page, t.vc_token, t.vc_head,
                      t.ks_page, t.ks_token, t.ks_head, t.vs_page, t.vs_token, t.vs_head, 0, 1};
-  if (many_rows(s)) return cuda_status(launch_paged_attn_q4_tc(a, c, s->io == RGLRU_F32, stream));
+  if (many_rows(s)) return cuda_status(launch_paged_attn_q4_tc(a, c, s->io == RGLRU_F32, mean_rows(s), stream));
   return cuda_status(launch_paged_attn_q4(a, c, s->io == RGLRU_F32, mean_rows(s), stream));
 }

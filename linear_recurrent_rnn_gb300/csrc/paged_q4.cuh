@@ -309,15 +309,16 @@ __device__ __forceinline__ void tq_row(const uint8_t* src, int r, F f) {
 }
 
 // Attention over the cache in 4 bits: few rows a request, `rows` in the mean (paged_attn_q4.cu), many rows
-// (paged_attn_q4_tc.cu).  Rows up to which the first is taken.  Measured (64 requests of 500 to 4096 keys, 32 heads on
-// 8 of 128; few against many): bf16 20 rows 119 and 138 us, 32 rows 130 and 138, 48 rows 242 and 145; float32 16 rows
-// 88 and 143, 20 rows 166 and 143; with heads of 64 73 and 107, 137 and 108; 10 heads on 1 of 256 20 rows 44 and 61, 40
-// rows 70 and 60, 50 rows 84 and 62 (1 to 7 tokens, 40 rows in the mean, window 2048: 46 and 56).
-constexpr int TQ_FEW_ROWS = 32, TQ_FEW_ROWS_F32 = 16, TQ_FEW_ROWS_F32_WIDE = 40;  // (the last: D above 128)
+// (paged_attn_q4_tc.cu).  Rows up to which the first is taken.  Measured (64 requests of 500 to 4096 keys, few against
+// many), 32 heads on 8: bf16, heads of 128, 16 rows 79 and 95 us, 20 rows 118 and 95; heads of 64 67 and 76, 97 and 76;
+// float32, heads of 128, 88 and 143, 166 and 143; heads of 64 73 and 107, 137 and 108.  10 heads on 1 of 256: bf16 30 rows
+// 50 and 54, 40 rows 59 and 52; float32 20 rows 44 and 61, 40 rows 70 and 60, 50 rows 84 and 62 (1 to 7 tokens, 40 rows in
+// the mean, window 2048: 46 and 56).
+constexpr int TQ_FEW_ROWS = 16, TQ_FEW_ROWS_WIDE = 32, TQ_FEW_ROWS_WIDE_F32 = 40;  // (wide: D above 128)
 cudaError_t launch_paged_attn_q4(PagedArgs a, const Q4Cache& c, bool f32, int rows, cudaStream_t s);
 size_t paged_attn_q4_ws_bytes(const paged_shape* s, int rows);
-cudaError_t launch_paged_attn_q4_tc(PagedArgs a, const Q4Cache& c, bool f32, cudaStream_t s);
-size_t paged_attn_q4_tc_ws_bytes(const paged_shape* s);
+cudaError_t launch_paged_attn_q4_tc(PagedArgs a, const Q4Cache& c, bool f32, int rows, cudaStream_t s);
+size_t paged_attn_q4_tc_ws_bytes(const paged_shape* s, int rows);
 // Q4Cache::s_whole (a row that is cut off is copied piece by piece, with what lies behind it as zeros).
 inline int q4_whole_scales(const PagedArgs& a, const Q4Cache& c) {
   const uint64_t on = reinterpret_cast<uintptr_t>(c.ks) | reinterpret_cast<uintptr_t>(c.vs) | c.ks_page | c.ks_token | c.ks_head |

@@ -256,6 +256,9 @@ CASES = {
     "group-12-64": ([(1, 500), (1, 129)], 24, 2, 64, 32, 200),
     "group-20-256": ([(1, 300), (1, 40)], 20, 1, 256, 16, 0),
     "group-40-192": ([(1, 700), (0, 9), (1, 127)], 40, 1, 192, 8, 0),
+    "prompts-64": ([(300, 300), (290, 500)], 16, 2, 64, 16, 0),
+    "prompts-80": ([(200, 450)], 8, 1, 80, 16, 130),
+    "prompts-128": ([(260, 700), (300, 300), (250, 900)], 10, 2, 128, 32, 0),
     "page-4096": ([(3, 5000)], 2, 1, 64, 4096, 0),
     "mixed": ([(1, 350)] * 6 + [(160, 320), (1, 1), (77, 900)], 8, 1, 128, 16, 256),
 }
