@@ -212,3 +212,49 @@ def test_a_graph_and_direct_calls_take_turns_on_a_workspace():
         other = attend(runs[1 - turn], torch.zeros_like(runs[1 - turn]["q"]))
         assert torch.equal(runs[turn]["o"], want[turn]) and torch.equal(other, want[1 - turn])
     assert R.rglru_sync_status(ws) == R.OK
+
+
+def test_calls_on_two_streams_at_once():
+    """Steps of two servers at once, each with a stream and scratch of its own, give what they give alone."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+
+    def server(n, t, kv, dtype):
+        sh = R.make_paged_shape(n, n * t, 8, 2, 128, 256, 16, 64, dtype, 300)
+        cache = R.alloc_paged_q4_cache(sh)
+        kept = [torch.randn(256 * 16, 2, 128, device="cuda", generator=g).to(dtype) for _ in range(2)]
+        fill = R.make_paged_shape(1, 256 * 16, 8, 2, 128, 256, 16, 64, dtype)
+        q = torch.randn(n * t, 8, 128, device="cuda", generator=g).to(dtype)
+        table = torch.randint(0, 256, (n, 64), device="cuda", generator=g, dtype=torch.int32)
+        cu = torch.arange(n + 1, device="cuda", dtype=torch.int32) * t
+        holders, ring, state = zeros(256), zeros(256), zeros(3)
+        first, end = zeros(n), zeros(n) + 30
+        ws, pages = R.alloc_paged_q4_workspace(sh), R.alloc_paged_pages_workspace(sh)
+        slots = torch.arange(256 * 16, device="cuda")
+        outs = [torch.zeros_like(q), torch.zeros_like(table), torch.zeros_like(ring), torch.zeros_like(state)]
+
+        def step(stream):
+            R.paged_q4_write(fill, *kept, slots, *cache, stream=stream)
+            R.paged_q4_attention(sh, q, *cache, table, cu, zeros_kv, 0.09, outs[0], None, ws, stream=stream)
+            R.paged_release(sh, first, end, table, holders, outs[2], state, outs[1], holders_out, outs[3], pages, stream=stream)
+        zeros_kv, holders_out = zeros(n) + kv, zeros(256)
+        return step, outs, ws
+
+    servers = [server(100, 1, 900, torch.bfloat16), server(3, 150, 1000, torch.float32), server(4, 200, 700, torch.bfloat16)]
+    torch.cuda.synchronize()
+    want = []
+    for step, outs, _ in servers:
+        step(None)
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs])
+        for o in outs:
+            o.zero_()
+    streams = [torch.cuda.Stream() for _ in servers]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (step, _, _), stream in zip(servers, streams):
+            step(stream)
+    torch.cuda.synchronize()
+    for (_, outs, ws), w in zip(servers, want):
+        assert R.rglru_sync_status(ws) == R.OK
+        for a, b in zip(outs, w):
+            assert torch.equal(a, b)
