@@ -22,11 +22,11 @@
 //
 // Warpgroups: softmax; control (a thread that issues S's products, one that issues O's, a warp that walks the
 // items, one that brings queries); 2 that bring keys and 2 that bring values, a unit each in turn.
-// Bound by the warps that dequantise: 1390 cycles a key tile of one head of 128, in which a scheduler issues some 800
-// instructions (57 % of its slots); each of its six warps issues in order, ten cycles an instruction, and more warps
+// Bound by the warps that dequantise: 1390 cycles a key tile of one head of 128, in which a scheduler issues some 780
+// instructions (56 % of its slots); each of its six warps issues in order, ten cycles an instruction, and more warps
 // have no registers.  That is 3.8 TB/s of codes on long sequences, where bf16's kernel reaches 6.1 TB/s of 3.6 times
 // the bytes.
-// Measured (GB300): 256 requests of 64 to 8192 keys, 32 heads on 8 of 128, 197 us (the kernel over bf16
+// Measured (GB300): 256 requests of 64 to 8192 keys, 32 heads on 8 of 128, 195 us (the kernel over bf16
 // caches: 287); 64 of 4096 keys, 16 heads on 16, 164 us (314); 152 of 16384 keys on one head, 94 us.
 // Other ways that were measured: keys from shared memory (a product of 128 x 16 x 16 takes the tensor core 39
 // cycles then, from TMEM 9); TMA and bulk copies of the codes (84 cycles a copy and SM, and a page's codes
