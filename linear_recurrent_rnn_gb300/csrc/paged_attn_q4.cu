@@ -84,6 +84,8 @@ struct Tq {
   static constexpr size_t smem = 1024 + VBUF * VB + (size_t)(TQ_KEYS + TQ_VALUES) * DEPTH * SB + QBUF * QB + 2 * PB + TQ_JOIN + 1024;
   static_assert(KT * COLS + NR - COLS <= S_WIDTH && 2 * UNITS * NR <= 128 && KBUF * COL / 2 <= 256, "TMEM");
   static_assert(DEPTH >= 2, "shared memory");
+  static_assert(KBUF >= TQ_KEYS && VBUF >= TQ_VALUES, "a stage at least for each that fills them in turn");
+  static_assert(VBUF * VB + (size_t)(TQ_KEYS + TQ_VALUES) * DEPTH * SB >= (PG_MAX_SEQS + 1) * 8, "the scan of the requests");
 };
 
 template <int DP, int R, bool F32>

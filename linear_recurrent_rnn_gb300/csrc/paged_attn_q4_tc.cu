@@ -61,6 +61,7 @@ struct Tm {
   static constexpr int DEPTH = FIT / GROUPS < 6 ? FIT / GROUPS : 6;  // units of codes on their way, of a group
   static constexpr size_t smem = 1024 + Q_BYTES + STAGES * UB + (size_t)GROUPS * DEPTH * SB + 1024;
   static_assert(DEPTH >= 2 && GROUPS <= STAGES, "shared memory");
+  static_assert(STAGES * UB + (size_t)GROUPS * DEPTH * SB >= (PG_MAX_SEQS + 1) * 8, "the scan of the requests");
 };
 
 template <int DP, bool F32, int NT_>

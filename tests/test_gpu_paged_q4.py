@@ -323,6 +323,15 @@ def test_scales_that_leave_nothing_of_the_scores(lens, io):
         compare(o, L, expect(x, scale, 70), io)
 
 
+@pytest.mark.parametrize("Hq,D,io", [(4, 64, "bf16"), (24, 64, "bf16"), (10, 256, "f32"), (48, 256, "f32")])
+def test_as_many_requests_as_there_may_be(Hq, D, io):
+    """8192 of them, most without a token; few and many rows a request."""
+    x = build([(1, 1 + n % 45) if n % 28 == 0 else (0, n % 3 * 7) for n in range(8192)], Hq, 1, D, 16, io, 31)
+    o, L, ws = attend(x, D ** -0.5)
+    assert R.rglru_sync_status(ws) == R.OK
+    compare(o, L, expect(x, D ** -0.5), io)
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_attention_repeats_bitwise_and_keeps_its_workspace(io):
     """Many CTAs share a request's keys: a second run on the same workspace, and one on another stream with its
@@ -486,6 +495,20 @@ def test_a_wait_that_runs_out_is_reported():
         o, L, ws = attend(x, 0.1)
         assert R.rglru_sync_status(ws) == R.OK
         compare(o, L, expect(x, 0.1), io)
+
+
+@pytest.mark.parametrize("io,lens,Hq", [("bf16", [(40, 900)], 2), ("bf16", [(600, 900)], 4), ("f32", [(40, 900)], 2)])
+def test_a_wait_that_runs_out_is_reported_with_many_rows(io, lens, Hq):
+    x = build(lens, Hq, 1, 64, 16, io, 25)
+    R.rglru_debug_lookback(10000, 0)
+    try:
+        _, _, ws = attend(x, 0.1)
+        assert R.rglru_sync_status(ws) == R.ERR_TIMEOUT
+    finally:
+        R.rglru_debug_lookback(0, -1)
+    o, L, ws = attend(x, 0.1)
+    assert R.rglru_sync_status(ws) == R.OK
+    compare(o, L, expect(x, 0.1), io)
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
