@@ -259,7 +259,6 @@ def _prepare_pages(case, seed, g, dev):
         x["moves"] = torch.empty(children, 2, **i32)
     elif case["op"] == "release":
         x["N"], x["table"] = N, table.contiguous()
-        x["table_out"] = x["table"].clone()
         gone = torch.randperm(N, generator=g, **dev) < _ended(case)
         x["first"] = torch.zeros(N, **i32)
         x["end"] = torch.where(gone, held, torch.zeros_like(held)).to(torch.int32)
@@ -314,9 +313,9 @@ def _run_own(x):
                              x["scale"], x["o"], x["lse"], x["workspace"])
         return {"o": x["o"], "lse": x["lse"]}
     if x["op"] == "release":
-        R.paged_release(sh, x["first"], x["end"], x["table"], x["holders"], x["free"], x["free_state"], x["table_out"],
-                        x["holders_out"], x["free_out"], x["workspace"])
-        return _told(x, "table_out", "holders_out", "free", "free_out")
+        R.paged_release(sh, x["first"], x["end"], x["table"], x["holders"], x["free"], x["free_state"], x["holders_out"], x["free_out"],
+                        x["workspace"])
+        return _told(x, "holders_out", "free", "free_out")
     if x["op"] == "fork":
         R.paged_fork(sh, x["parents"], x["children"], x["table"], x["lens"], x["holders"], x["free"], x["free_state"], x["table_out"],
                      x["lens_out"], x["holders_out"], x["moves"], x["free_out"])
@@ -446,13 +445,12 @@ def _release(x):
     n = _counts(torch.where(goes, x["table"], torch.full_like(x["table"], -1)), P)
     freed = n > x["holders"]
     x["holders_out"].copy_((x["holders"] - n).clamp(min=0))
-    x["table_out"].masked_fill_(goes, -1)
     place = (head + count + freed.cumsum(0) - 1) % P
     ring = torch.cat([x["free"], x["free"][:1]])
     ring.scatter_(0, torch.where(freed, place, torch.full_like(place, P)), torch.arange(P, dtype=torch.int32, device=head.device))
     x["free"].copy_(ring[:P])
     x["free_out"].copy_(torch.stack([head, count + freed.sum(), torch.zeros_like(head)]))
-    return _told(x, "table_out", "holders_out", "free", "free_out")
+    return _told(x, "holders_out", "free", "free_out")
 
 
 def _compact(x):
@@ -570,7 +568,7 @@ def work(case):
         held = [-(-n // s) for n in lens]
         if case["op"] == "release":
             ended = sum(sorted(held)[:_ended(case)])  # (which ones end is the seed's)
-            return {"bytes": 8 * case["N"] + 8 * ended + 8 * ended + 4 * P, "flops": 0}
+            return {"bytes": 8 * case["N"] + 4 * ended + 8 * ended + 4 * P, "flops": 0}
         page = 2 * case["layers"] * s * case["Hkv"] * case["D"] * (2 if case["type"] == "bf16" else 4)
         if case["op"] == "fork":
             copies = sum(n % s > 0 for n in lens) * case["each"]
