@@ -302,6 +302,8 @@ def _run_own(x):
         else:
             x["shape"] = R.make_paged_shape(x["N"], 0, num_pages=x["P"], page_size=x["page"], table_width=x["width"])
             x["workspace"] = R.alloc_paged_pages_workspace(x["shape"])
+            if x["op"] == "release":
+                x["table_out"] = x["table"].clone()  # (the inputs stay as they are, for another pass)
     sh = x["shape"]
     if x["op"] == "write":
         cache = (x["k_codes"], x["k_scales"], x["v_codes"], x["v_scales"])
@@ -313,8 +315,8 @@ def _run_own(x):
                              x["scale"], x["o"], x["lse"], x["workspace"])
         return {"o": x["o"], "lse": x["lse"]}
     if x["op"] == "release":
-        R.paged_release(sh, x["first"], x["end"], x["table"], x["holders"], x["free"], x["free_state"], x["holders_out"], x["free_out"],
-                        x["workspace"])
+        R.paged_release(sh, x["first"], x["end"], x["table"], x["holders"], x["free"], x["free_state"], x["table_out"],
+                        x["holders_out"], x["free_out"], x["workspace"])
         return _told(x, "holders_out", "free", "free_out")
     if x["op"] == "fork":
         R.paged_fork(sh, x["parents"], x["children"], x["table"], x["lens"], x["holders"], x["free"], x["free_state"], x["table_out"],
