@@ -61,6 +61,7 @@ struct Tq {
   static constexpr int UNITS = DP == 256 ? 2 : 1;     // of a tile
   static constexpr int COL = DP / UNITS;              // columns of one
   static constexpr int KT = R == 32 ? 1 : R == 16 || DP == 256 ? 2 : 4;  // key tiles of a step
+  static constexpr int SCORES = (KT * COLS + 15) / 16 * 16;  // of a thread and step as they are read from TMEM, 16 at once
   static constexpr uint32_t RB = COL / 2, SP = COL / 16;  // bytes of a row's codes, of its scales
   static constexpr uint32_t SB = 1024 * ((TA_BN * (RB + SP) + 1023) / 1024);  // a unit's
   static constexpr uint32_t VB = TA_BN * COL * 2;     // of a unit of values as f16
@@ -82,6 +83,7 @@ struct Tq {
   static constexpr int KBUF = 4;
   static constexpr uint32_t V_SLAB = TA_SLAB;         // 64 columns, 128-byte swizzle
   static constexpr size_t smem = 1024 + VBUF * VB + (size_t)(TQ_KEYS + TQ_VALUES) * DEPTH * SB + QBUF * QB + 2 * PB + TQ_JOIN + 1024;
+  static_assert(SCORES % 16 == 0 && SCORES >= KT * COLS && SCORES <= (int)S_WIDTH, "reads of S");
   static_assert(KT * COLS + NR - COLS <= S_WIDTH && 2 * UNITS * NR <= 128 && KBUF * COL / 2 <= 256, "TMEM");
   static_assert(DEPTH >= 2, "shared memory");
   static_assert(KBUF >= TQ_KEYS && VBUF >= TQ_VALUES, "a stage at least for each that fills them in turn");
@@ -220,9 +222,9 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
         const uint32_t b = step & 1;
         ok = ctl.wait(&s_full[b], step >> 1 & 1) && ok;
         tc::tc_fence_after();
-        float x[C::KT * C::COLS];
+        float x[C::SCORES];
 #pragma unroll
-        for (int c = 0; c < C::KT * C::COLS; c += 16)
+        for (int c = 0; c < C::SCORES; c += 16)
           tc::tmem_ld16(lanes + C::S_COL + b * C::S_WIDTH + c, *reinterpret_cast<float(*)[16]>(x + c));
         tc::tmem_ld_wait();
         tc::reg_fence(x);
