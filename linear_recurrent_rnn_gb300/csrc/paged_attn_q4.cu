@@ -389,24 +389,25 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
       if (out) break;
       const bool any = j1 > j0;
       // the rows' sums over the threads
-      {
-        float v[R];
+      float v[R];
 #pragma unroll
-        for (int c = 0; c < R / 2; ++c) {
-          v[2 * c] = l[c].x;
-          v[2 * c + 1] = l[c].y;
-        }
-        tf_combine<R>(v, [](float p, float q) { return p + q; });
-        s_red[warp][tf_column<R>()] = v[0];
-        if (R <= 8 && tid == 0)
-#pragma unroll
-          for (int c = 0; c < R / 2; ++c) reinterpret_cast<float2*>(s_ref)[c] = ref(c);
+      for (int c = 0; c < R / 2; ++c) {
+        v[2 * c] = l[c].x;
+        v[2 * c + 1] = l[c].y;
       }
+      tf_combine<R>(v, [](float p, float q) { return p + q; });
       if (any) {
         ok = ctl.wait(&pv_done[(step - 1) & 1], (step - 1) >> 1 & 1) && ok;
         tc::tc_fence_after();
         ++no;
       }
+      // Not before the wait: it ends once all four warps have handed in the last step's weights, and until then one
+      // of them may still read that step's maxima from s_red.  (Without keys nothing has been read since the barrier
+      // at the item's start.)
+      s_red[warp][tf_column<R>()] = v[0];
+      if (R <= 8 && tid == 0)
+#pragma unroll
+        for (int c = 0; c < R / 2; ++c) reinterpret_cast<float2*>(s_ref)[c] = ref(c);
       if (tf_any(!ok)) break;
       const bool whole = it.c0 == it.c1;
       const int tok0 = it.first + it.tok;

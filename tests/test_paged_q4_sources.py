@@ -55,3 +55,23 @@ def test_scores_fit_the_array_that_they_are_read_into(DP, R, F32):
     size, end = value(m.group(1), c), value(m.group(2), c)
     assert end >= c["KT"] * c["COLS"]
     assert all(at + 16 <= size for at in range(0, end, 16))
+
+
+def test_sums_are_written_once_every_warp_has_read_the_maxima():
+    """s_red holds the warps' maxima of a step, then their sums.  All threads read the maxima behind a barrier; a warp may
+    be done with its weights while another still reads, so between the weights' arrival and the sums' store
+    lies what waits for all four warps: the products of those weights, or a barrier."""
+    body, = kernels("paged_attn_q4.cu")
+    handed_in = body.index("tc::mbar_arrive(&p_full[b])")
+    store = body.index("s_red[warp]", handed_in)
+    assert re.search(r"ctl\.wait\(&pv_done\[\(step - 1\) & 1\]|tf_any\(|__syncthreads\(", body[handed_in:store])
+    read = body.index("row_sum(", store)
+    assert re.search(r"tf_any\(|__syncthreads\(", body[store:read])
+
+
+def test_every_item_begins_with_a_barrier_of_the_softmax_warps():
+    """Maxima, references and factors in shared memory are read up to the end of an item, and written from its first
+    step on."""
+    body, = kernels("paged_attn_q4.cu")
+    start = body.index("ctl.wait(&i_full[ni % TA_ITEMS]")
+    assert "tf_any(!ok)" in body[start:body.index("s_ref[", start)]
