@@ -50,7 +50,8 @@ rglru_status paged_fork(const paged_shape *shape, int32_t num_children, const in
                         int32_t *moves, int32_t *free_state_out, rglru_stream stream);
 
 /* Bytes of the scratch of paged_release and paged_compact: zero before its first use (both leave
- * it so), for one stream at a time.  0 for an unsupported shape. */
+ * all of it so, and calls of other shapes may use it where it is large enough), for one stream at a
+ * time.  0 for an unsupported shape. */
 size_t paged_pages_workspace_bytes(const paged_shape *shape);
 
 /* The entries [first_pages[n], end_pages[n]) of every row n of the block table (int32 [num_seqs],

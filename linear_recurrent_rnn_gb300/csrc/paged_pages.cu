@@ -141,17 +141,10 @@ __global__ void __launch_bounds__(PP_THREADS) k_paged_fork(const ForkArgs a) {
 }
 
 // ---------------------------------------------------------------- release and compact: a bit a page
-// Workspace: a counter of CTAs (zero between calls), at 256 a bit a page (zero between calls), then
-// a page's place among the pages that move (paged_compact).
-struct PagesWs {
-  size_t rank, total;
-};
-PagesWs pages_ws(int P) {
-  PagesWs w;
-  w.rank = 256 + align_up(((size_t)P + 31) / 32 * 4, 256);
-  w.total = w.rank + (size_t)P * 4;
-  return w;
-}
+// Workspace: a counter of CTAs, at 256 a bit a page; all zero between calls, so pools of any size may share
+// one.  Nothing else is kept there: numbers by page, left behind by a call over a small pool, would be
+// set bits to one over a larger pool.
+size_t pages_ws_bytes(int P) { return 256 + align_up(((size_t)P + 31) / 32 * 4, 256); }
 
 struct PagesArgs {
   int N, P, s_log2, width, words;
@@ -159,7 +152,6 @@ struct PagesArgs {
   const int32_t *table, *state, *holders;
   int32_t *table_out, *holders_out, *ring, *state_out, *moves;
   uint32_t *counter, *bits;
-  int32_t* rank;
 };
 
 // One bit for every page that the entries free (RELEASE) or use.  A warp takes a row and PP_COLS
@@ -314,9 +306,7 @@ __global__ void __launch_bounds__(PP_THREADS) k_paged_moves(const PagesArgs a) {
         a.moves[2 * r + 1] = p;
       }
     } else if (bit) {
-      const int r = at - kept;
-      a.moves[2 * r] = p;
-      a.rank[p] = r;
+      a.moves[2 * (at - kept)] = p;
     } else {
       a.holders_out[p] = 0;
     }
@@ -330,31 +320,73 @@ __global__ void __launch_bounds__(PP_THREADS) k_paged_moves(const PagesArgs a) {
   }
 }
 
-// The table's entries and the moved pages' holders by the new numbers.
+// The table's entries and the moved pages' holders by the new numbers.  A moved page's place is looked for among the moves,
+// which are in ascending order (an unused one, -1, is the largest as an unsigned number): every stride-th, the CTA has in
+// shared memory, between those by quarters, three loads at once.  These are scattered, a cycle of L1 each, so tasks go to
+// as many SMs as there are.  96 requests of 100 to 8000 tokens: 12.3 us the call, 234 with its copies (16 tasks a CTA 13.9;
+// quarters alone, without the samples, 236 with the copies; places kept in an array by page 10.1, but that array had to
+// be cleared by another kernel).
 __global__ void __launch_bounds__(PP_THREADS) k_paged_renumber(const PagesArgs a) {
+  __shared__ uint32_t s_from[PP_THREADS + PP_THREADS / 32];  // (a place more after 32: the halves meet in no bank)
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, s = 1 << a.s_log2;
+  const int tid = threadIdx.x, lane = tid & 31, s = 1 << a.s_log2, most = a.P / 2;
+  const int stride = (most + PP_THREADS - 1) / PP_THREADS;
+  const uint32_t sample = (int64_t)tid * stride < most ? (uint32_t)a.moves[2 * tid * stride] : ~0u;
   const int used = a.P - a.state_out[1];
-  const int64_t first = (int64_t)blockIdx.x * PP_THREADS + threadIdx.x, all = (int64_t)gridDim.x * PP_THREADS;
+  const int64_t first = (int64_t)blockIdx.x * PP_THREADS + tid, all = (int64_t)gridDim.x * PP_THREADS;
   const int chunks = (a.width + PP_COLS - 1) / PP_COLS;
   const int64_t tasks = (int64_t)a.N * chunks, step = (int64_t)gridDim.x * PP_WARPS;
-  for (int64_t t = (int64_t)blockIdx.x * PP_WARPS + (threadIdx.x >> 5); t < tasks; t += step) {
-    const int n = (int)(t / chunks), c0 = (int)(t - (int64_t)n * chunks) * PP_COLS;
-    const int hi = min((int)(((int64_t)max(a.lens[n], 0) + s - 1) >> a.s_log2), a.width);
-    const int64_t row = (int64_t)n * a.width;
-    int id[PP_COLS / 32], r[PP_COLS / 32];
+  int64_t t = (int64_t)(tid >> 5) * gridDim.x + blockIdx.x, row = 0;
+  int c0 = 0, hi = 0, id[PP_COLS / 32];
+  auto load = [&] {  // of task t
+    if (t >= tasks) return;
+    const int n = (int)(t / chunks);
+    c0 = (int)(t - (int64_t)n * chunks) * PP_COLS;
+    row = (int64_t)n * a.width;
+    hi = min((int)(((int64_t)max(a.lens[n], 0) + s - 1) >> a.s_log2), a.width);
+#pragma unroll
+    for (int e = 0; e < PP_COLS / 32; ++e) id[e] = c0 + e * 32 + lane < a.width ? a.table[row + c0 + e * 32 + lane] : -1;
+  };
+  load();
+  s_from[tid + (tid >> 5)] = sample;
+  __syncthreads();
+  for (; t < tasks; t += step, load()) {
+    int r[PP_COLS / 32];
+    bool moved[PP_COLS / 32];
 #pragma unroll
     for (int e = 0; e < PP_COLS / 32; ++e) {
-      const int col = c0 + e * 32 + lane;
-      id[e] = col < a.width ? a.table[row + col] : -1;
+      moved[e] = c0 + e * 32 + lane < hi && id[e] >= used && id[e] < a.P;
+      int at = 0;
+#pragma unroll
+      for (int d = PP_THREADS / 2; d; d >>= 1)
+        if (s_from[at + d + ((at + d) >> 5)] <= (uint32_t)id[e]) at += d;
+      r[e] = moved[e] ? at * stride : 0;
+    }
+    int d = 1;
+    while (d * 4 < stride) d *= 4;
+#pragma unroll 1
+    for (; d && stride > 1; d >>= 2) {
+      uint32_t from[PP_COLS / 32][3];
+#pragma unroll
+      for (int e = 0; e < PP_COLS / 32; ++e)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const int at = r[e] + (k + 1) * d;
+          from[e][k] = moved[e] && at < most ? (uint32_t)a.moves[2 * at] : ~0u;
+        }
+#pragma unroll
+      for (int e = 0; e < PP_COLS / 32; ++e) {
+        int below = 0;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) below += from[e][k] <= (uint32_t)id[e];
+        r[e] += below * d;
+      }
     }
 #pragma unroll
-    for (int e = 0; e < PP_COLS / 32; ++e) r[e] = c0 + e * 32 + lane < hi && id[e] >= used && id[e] < a.P ? a.rank[id[e]] : -1;
-#pragma unroll
     for (int e = 0; e < PP_COLS / 32; ++e) {
       const int col = c0 + e * 32 + lane;
-      if (col < a.width) a.table_out[row + col] = r[e] >= 0 ? a.moves[2 * r[e] + 1] : id[e];
+      if (col < a.width) a.table_out[row + col] = moved[e] ? a.moves[2 * r[e] + 1] : id[e];
     }
   }
   for (int64_t i = first; i < a.P / 2; i += all) {
@@ -491,7 +523,7 @@ extern "C" rglru_status paged_fork(const paged_shape* s, int32_t num_children, c
 }
 
 extern "C" size_t paged_pages_workspace_bytes(const paged_shape* s) {
-  return pg_check_cache(s) == RGLRU_OK ? pages_ws(s->num_pages).total : 0;
+  return pg_check_cache(s) == RGLRU_OK ? pages_ws_bytes(s->num_pages) : 0;
 }
 
 extern "C" rglru_status paged_release(const paged_shape* s, const int32_t* first_pages, const int32_t* end_pages,
@@ -554,11 +586,10 @@ extern "C" rglru_status paged_compact(const paged_shape* s, const int32_t* kv_le
   a.moves = moves;
   a.counter = static_cast<uint32_t*>(workspace);
   a.bits = a.counter + 64;
-  a.rank = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + pages_ws(a.P).rank);
   const int64_t tasks = (int64_t)a.N * ((a.width + PP_COLS - 1) / PP_COLS);
   cudaError_t e = launch(k_paged_mark<false>, ctas_for(tasks, PP_WARPS, 4 * PP_MAX_CTAS), a, stream);
   if (e == cudaSuccess) e = launch(k_paged_moves, ctas_for(a.words, PP_WARPS), a, stream);
-  if (e == cudaSuccess) e = launch(k_paged_renumber, ctas_for(tasks, PP_WARPS, 4 * PP_MAX_CTAS), a, stream);
+  if (e == cudaSuccess) e = launch(k_paged_renumber, ctas_for(tasks, 1, 4 * PP_MAX_CTAS), a, stream);
   return cuda_status(e);
 }
 
