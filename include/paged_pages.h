@@ -84,8 +84,8 @@ rglru_status paged_compact(const paged_shape *shape, const int32_t *kv_lens,
                            int32_t *free_state_out, int32_t *moves, void *workspace,
                            rglru_stream stream);
 
-/* Copies page moves[i][0] to page moves[i][1], i < num_moves (int32 [num_moves][2]), in each of
- * num_caches caches: page p of caches[c] is the page_bytes[c] bytes from
+/* Copies page moves[i][0] to page moves[i][1], i < num_moves (int32 [num_moves][2], at most 2^30),
+ * in each of num_caches caches: page p of caches[c] is the page_bytes[c] bytes from
  * caches[c] + p * page_strides[c] on (host arrays; bytes, strides at least page_bytes).  Moves
  * with a page outside [0, num_pages) are passed over.  No page is a destination twice, or a
  * destination and a source (the moves of one paged_fork or paged_compact are so).  Up to 64

@@ -605,6 +605,7 @@ extern "C" rglru_status paged_copy(const paged_shape* s, int32_t num_moves, cons
     if (!caches[c] || page_bytes[c] < 1 || page_strides[c] < page_bytes[c]) return RGLRU_ERR_INVALID_ARG;
     if (page_bytes[c] > 1 << 28) return RGLRU_ERR_UNSUPPORTED;
   }
+  if (num_moves > 1 << 30) return RGLRU_ERR_UNSUPPORTED;  // (places in the list are counted in 32 bits)
   if (num_moves == 0) return RGLRU_OK;
   CopyArgs a;
   a.M = num_moves;
