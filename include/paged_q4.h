@@ -9,8 +9,12 @@
  *   scale s = the E4M3 number nearest to a / 6 (ties to even), at least 2^-9, at most 448;
  *   code    = the number nearest to x / s among 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives,
  *             ties to the even code (0, 1, 2, 4).
- * So a value is off by at most (1 + 1/16) a / 6 while a is below 6 * 448 = 2688; above that it is cut
- * off.  Where one of the 16 is not finite the scale is NaN, and all 16 read as NaN.  A value has 6
+ * So a value is off by at most (1 + 1/16) a / 6 while a lies between 6 * 2^-6 (0.094) and 6 * 448 =
+ * 2688; above that it is cut off.  Below, where scales have fewer bits and then end, by at most
+ * a / 6 + 2^-10, or 3 * 2^-9 where that is more: a value of a hundredth is held roughly, a group with
+ * a <= 2^-11 as zeros.  No factor of a head or tensor is held: a caller whose keys or values are so
+ * small multiplies them before the write (and divides paged_q4_attention's scale, or o).
+ * Where one of the 16 is not finite the scale is NaN, and all 16 read as NaN.  A value has 6
  * significant bits at most: reading it in bf16 or float32 is exact.
  *
  * Arrays.  Codes: [num_pages][page_size][Hkv][D / 2] bytes, channel 2 i in the low half of byte i;
@@ -66,9 +70,10 @@ size_t paged_q4_attention_workspace_bytes(const paged_shape *shape);
  * waits that run out.
  * Numerics: keys and values enter the products exactly.  Queries enter as f16, each row times a
  * power of two: exact for bf16 but for elements below 2^-29 of their row's largest; float32 ones as
- * a sum of two (relative 2^-22).  Weights enter as f16, off by 2^-11 of themselves or 2^-32 of the
- * row's largest (2^-36 with up to 16 rows a request), float32 ones as a sum of two (2^-22, or 2^-36
- * of the row's largest).  Scores, softmax and sums are held in float32. */
+ * a sum of two (off by 2^-22 of themselves, or 2^-39 of their row's largest where that is more).
+ * Weights enter as f16, off by 2^-11 of themselves, or 2^-32 of the row's largest where that is more
+ * (2^-36 where requests have up to 16 rows of queries, Hq / Hkv a token, in the mean); float32 ones as
+ * a sum of two (2^-22, or 2^-36 of the row's largest).  Scores, softmax and sums are held in float32. */
 rglru_status paged_q4_attention(const paged_shape *shape, const paged_q4_strides *strides,
                                 const void *q, const void *k_codes, const void *k_scales,
                                 const void *v_codes, const void *v_scales,

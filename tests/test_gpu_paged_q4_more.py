@@ -1,5 +1,6 @@
 """Further GPU tests of the cache in 4 bits (include/paged_q4.h).  Tolerances: those of test_gpu_paged_q4.py, which
 says where they come from."""
+import numpy as np
 import pytest
 import torch
 
@@ -33,3 +34,29 @@ def test_items_of_one_step_give_the_same_bits_every_time(io, Hq, D):
     for _ in range(30):
         o2, L2, _ = attend(x, D ** -0.5, ws=ws)
         assert torch.equal(o, o2) and torch.equal(L, L2)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [20.0, 27.3, 29.55, 31.2])
+@pytest.mark.parametrize("new", [1, 24])
+def test_small_weights_with_few_and_many_rows(new, size, io):
+    """One key with weight 1 and 120 000 with 2^-size each, whose values alone are not zero.  Weights enter as f16, held
+    times 2^7 of the row's largest with many rows in bf16, else 2^11 (or as two numbers, 2^11): half of f16's smallest step,
+    2^-25, is 2^-32 or 2^-36 of the largest for each key."""
+    D, n = 64, 120001
+    x = build([(new, n)], 1, 1, D, 16, io, 31, scales=(0x38, 0x39))  # scales 1
+    x["q"].fill_(0.0)
+    x["q"][..., 0] = 1.0
+    page = int(x["table"][0, 0])
+    for c in (x["cache"][0], x["cache"][2]):
+        c.zero_()
+    x["cache"][0][page, 0, 0, 0] = 0x07       # key 0: 6 in channel 0
+    x["cache"][2][:] = 0x22                   # values 1, but key 0's 0
+    x["cache"][2][page, 0] = 0
+    scale = size * np.log(2.0) / 6            # scores size ln 2 and 0
+    o, L, _ = attend(x, scale)
+    *ref, _ = expect(x, scale)
+    compare(o, L, (*ref, n * 2.0 ** (-32 if new > 16 and io == "bf16" else -36)), io)
+    got = o[:, 0, 0].double().cpu().numpy()
+    if size == 20.0:
+        assert np.all(np.abs(got - (n - 1) * 2.0 ** -20 / (1 + (n - 1) * 2.0 ** -20)) < 1e-3)
