@@ -50,18 +50,18 @@ struct TqAbort {
   uint32_t* status;  // global
   uint32_t limit;    // of a wait, in units of 1024 ns
   __device__ __forceinline__ static uint32_t now() { return (uint32_t)(tc::global_ns() >> 10); }
-  __device__ __forceinline__ bool over(uint32_t t0, uint32_t times = 1) const {
-    if (!*reinterpret_cast<volatile uint32_t*>(flag) && now() - t0 <= limit * times) return false;
+  __device__ __forceinline__ bool over(uint32_t t0) const {
+    if (!*reinterpret_cast<volatile uint32_t*>(flag) && now() - t0 <= limit) return false;
     *reinterpret_cast<volatile uint32_t*>(flag) = 1u;
     *reinterpret_cast<volatile uint32_t*>(status) = 1u;
     return true;
   }
   // By one thread.
-  __device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity, uint32_t times = 1) const {
+  __device__ __forceinline__ bool wait1(uint64_t* bar, uint32_t parity) const {
     if (tc::mbar_try_wait(bar, parity)) return true;
     const uint32_t t0 = now();
     while (!tc::mbar_try_wait_sleep(bar, parity, 20000u))
-      if (over(t0, times)) return false;
+      if (over(t0)) return false;
     return true;
   }
   // By a converged warp; the answer is the same in all its lanes.

@@ -405,15 +405,15 @@ __device__ __noinline__ void ta_join(const PagedArgs& a, const TaItem& it, int t
 }
 
 // ---------------------------------------------------------------- keys along the lanes, few rows (tf_)
-// Or over the 128 softmax threads of a group (a named barrier each).
-__device__ __forceinline__ bool tf_any(bool x, int bar = 1) {
+// Or over the softmax threads.
+__device__ __forceinline__ bool tf_any(bool x) {
   uint32_t y;
   __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(y)
-      : "r"((uint32_t)x), "r"(bar)
+      : "r"((uint32_t)x)
       : "memory");
   return y != 0;
 }
