@@ -79,9 +79,10 @@ typedef struct {
  * free pages are free_pages[(head + i) % num_pages], i < count.  free_state_out receives the
  * head and count after the step and the number of pages that were wanted and not had (no free
  * page left, or past table_width); pages not had are written as -1, tokens without a page get
- * slot -1, as do padding rows (their position is 0).  Returning pages is the caller's: append
- * them at (head + count) % num_pages and raise count.  A table entry whose page lies wholly
- * before every later query's window is not read again, so its page may be returned early.
+ * slot -1, as do padding rows (their position is 0).  Pages go back to the ring by paged_release
+ * (paged_pages.h), or by the caller's own means: at (head + count) % num_pages, with count raised.
+ * A table entry whose page lies wholly before every later query's window is not read again, so its
+ * page may be returned early.
  * kv_lens may be cached_lens and free_state_out free_state (updated in place); no other
  * arrays may overlap. */
 rglru_status paged_plan(const paged_shape *shape, const int32_t *cached_lens,
