@@ -73,7 +73,10 @@ size_t paged_q4_attention_workspace_bytes(const paged_shape *shape);
  * a sum of two (off by 2^-22 of themselves, or 2^-39 of their row's largest where that is more).
  * Weights enter as f16, off by 2^-11 of themselves, or 2^-32 of the row's largest where that is more
  * (2^-36 where requests have up to 16 rows of queries, Hq / Hkv a token, in the mean); float32 ones as
- * a sum of two (2^-22, or 2^-36 of the row's largest).  Scores, softmax and sums are held in float32. */
+ * a sum of two (2^-22, or 2^-36 of the row's largest).  Scores, softmax and sums are held in float32.
+ * The tensor core cuts its sums to 24 bits where others round: with float32 these are sums over up to
+ * 256 keys, added up with rounding; with bf16 over all the keys of a request that one SM takes (below
+ * 3e-9 of the output a key: 2e-4 for 65536 keys, where bf16's rounding is up to 2e-3). */
 rglru_status paged_q4_attention(const paged_shape *shape, const paged_q4_strides *strides,
                                 const void *q, const void *k_codes, const void *k_scales,
                                 const void *v_codes, const void *v_scales,

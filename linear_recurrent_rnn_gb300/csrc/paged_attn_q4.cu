@@ -20,6 +20,12 @@
 // that f16's range, 2^-25 to 2^15, is used from 2^4 times the first maximum down to 2^-36 of it; the reference m
 // is moved when a weight would pass 2^15.
 //
+// The tensor core cuts what it adds to a sum where it would have to round: outputs of values of one sign come out 2.8e-9
+// too small for each key of a sum, 1.8e-4 for 65536 (bf16 rounds by up to 2e-3).  So float32's products are summed a step of 256
+// keys at a time; the softmax's threads add the steps up, a step behind, in registers, where the references' changes are
+// applied too (256 requests decoding, 32 heads on 8 of 128, 258 us without, 267 with it; 128 requests, 16 heads on one
+// of 128, 34.6 and 37.7).  Sums of 512 keys and more, and tiles of 128 keys a step with all in registers, were slower.
+//
 // Warpgroups: softmax; control (a thread that issues S's products, one that issues O's, a warp that walks the
 // items, one that brings queries); 2 that bring keys and 2 that bring values, a unit each in turn.
 // Bound by the warps that dequantise: 1390 cycles a key tile of one head of 128, in which a scheduler issues some 780
@@ -60,7 +66,7 @@ struct Tq {
   // Units: 128 keys (or values) of up to 128 columns; what is copied, dequantised and multiplied at once.
   static constexpr int UNITS = DP == 256 ? 2 : 1;     // of a tile
   static constexpr int COL = DP / UNITS;              // columns of one
-  static constexpr int KT = R == 32 ? 1 : R == 16 || DP == 256 ? 2 : 4;  // key tiles of a step
+  static constexpr int KT = R == 32 ? 1 : F32 || R == 16 || DP == 256 ? 2 : 4;  // key tiles of a step
   static constexpr int SCORES = (KT * COLS + 15) / 16 * 16;  // of a thread and step as they are read from TMEM, 16 at once
   static constexpr uint32_t RB = COL / 2, SP = COL / 16;  // bytes of a row's codes, of its scales
   static constexpr uint32_t SB = 1024 * ((TA_BN * (RB + SP) + 1023) / 1024);  // a unit's
@@ -198,11 +204,12 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
       const int j0 = it.j0, j1 = it.j1;
       const int rows = min(a.tb, it.q - it.tok) * a.g;
       const int p_first = it.kv - it.q + it.tok, p_last = p_first + min(a.tb, it.q - it.tok) - 1;
-      const uint32_t ob = no & 1, t_o = lanes + C::O_COL + ob * (C::UNITS * NR);
+      uint32_t ob = no & 1, t_o = lanes + C::O_COL + ob * (C::UNITS * NR);
       // the rows' factors, references (scores in log2 units), this thread's sums; in pairs of rows.  Of 32
-      // rows only the sums are kept in registers.
-      constexpr bool KEEP = R <= 16;
+      // rows, and of 16 in float32, only the sums are kept in registers.
+      constexpr bool KEEP = R <= 16 && !(F32 && R == 16);
       float2 factors[KEEP ? R / 2 : 1], refs[KEEP ? R / 2 : 1], l[R / 2];
+      float2 acc[F32 ? C::UNITS : 1][R / 2];  // float32: O^T, but for the products that are still to be added
       ok = ctl.wait(&r_full[ni % TA_ITEMS], ni / TA_ITEMS & 1);
       const float2* s_f2 = reinterpret_cast<const float2*>(s_factor[ni % TA_ITEMS]);
       if (!KEEP) {
@@ -214,177 +221,214 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
         if (KEEP) factors[c] = s_f2[c];
         if (KEEP) refs[c] = make_float2(0.0f, 0.0f);
         l[c] = make_float2(0.0f, 0.0f);
+        if (F32)
+#pragma unroll
+          for (int hm = 0; hm < C::UNITS; ++hm) acc[hm][c] = make_float2(0.0f, 0.0f);
       }
       auto factor = [&](int c) { return KEEP ? factors[KEEP ? c : 0] : s_f2[c]; };
       auto ref = [&](int c) { return KEEP ? refs[KEEP ? c : 0] : reinterpret_cast<const float2*>(s_ref)[c]; };
       bool out = false;
-      for (int j = j0; j < j1; j += C::KT, ++step) {
+      // (float32: once more behind the last step, for its product)
+      for (int j = j0; F32 || j < j1; j += C::KT, ++step) {
         const uint32_t b = step & 1;
-        ok = ctl.wait(&s_full[b], step >> 1 & 1) && ok;
-        tc::tc_fence_after();
-        float x[C::SCORES];
+        constexpr bool ALL = R <= 8;  // more rows would cost the registers that the steps need
+        float2 scale[ALL ? R / 2 : 1];
+        auto factor_of = [&](int c) { return ALL ? scale[ALL ? c : 0] : reinterpret_cast<const float2*>(s_scale)[c]; };
+        bool grown = false;
+        if (!F32 || j < j1) {
+          ok = ctl.wait(&s_full[b], step >> 1 & 1) && ok;
+          tc::tc_fence_after();
+          float x[C::SCORES];
 #pragma unroll
-        for (int c = 0; c < C::SCORES; c += 16)
-          tc::tmem_ld16(lanes + C::S_COL + b * C::S_WIDTH + c, *reinterpret_cast<float(*)[16]>(x + c));
-        tc::tmem_ld_wait();
-        tc::reg_fence(x);
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&s_empty[b]);
-        // scores, and those times their factors less the references (rounded once)
-        float2 z[C::KT][R / 2], y[C::KT][R / 2];
+          for (int c = 0; c < C::SCORES; c += 16)
+            tc::tmem_ld16(lanes + C::S_COL + b * C::S_WIDTH + c, *reinterpret_cast<float(*)[16]>(x + c));
+          tc::tmem_ld_wait();
+          tc::reg_fence(x);
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s_empty[b]);
+          // scores, and those times their factors less the references (rounded once)
+          float2 z[C::KT][R / 2], y[C::KT][R / 2];
 #pragma unroll
-        for (int t = 0; t < C::KT; ++t)
+          for (int t = 0; t < C::KT; ++t)
 #pragma unroll
-          for (int c = 0; c < R / 2; ++c) {
-            z[t][c] = make_float2(x[t * C::COLS + 2 * c], x[t * C::COLS + 2 * c + 1]);
-            if (F32)
-              z[t][c] = ta_add2(z[t][c], make_float2(x[t * C::COLS + (C::COLS - R) + 2 * c], x[t * C::COLS + (C::COLS - R) + 2 * c + 1]));
-            y[t][c] = ta_fma2(z[t][c], factor(c), make_float2(-ref(c).x, -ref(c).y));
-          }
-        // positions that rows do not see, and tiles past the part's last (their scores are stale)
-        const int k0 = j * TA_BN, k1 = j1 * TA_BN;
-        if (k0 + C::KT * TA_BN > min(p_first + 1, k1) || (a.window && k0 < p_last - a.window + 1)) {
-          int p = p_first, h = 0;  // the row's position
-#pragma unroll
-          for (int c = 0; c < R; ++c) {
-            const int lo = a.window ? p - k0 - tid - a.window : -1, hi = min(p, k1 - 1) - k0 - tid;  // lo < 128 t <= hi
-#pragma unroll
-            for (int t = 0; t < C::KT; ++t) {
-              float& w = c & 1 ? y[t][c / 2].y : y[t][c / 2].x;
-              if (t * TA_BN > hi || t * TA_BN <= lo) w = -INFINITY;
+            for (int c = 0; c < R / 2; ++c) {
+              z[t][c] = make_float2(x[t * C::COLS + 2 * c], x[t * C::COLS + 2 * c + 1]);
+              if (F32)
+                z[t][c] = ta_add2(z[t][c], make_float2(x[t * C::COLS + (C::COLS - R) + 2 * c], x[t * C::COLS + (C::COLS - R) + 2 * c + 1]));
+              y[t][c] = ta_fma2(z[t][c], factor(c), make_float2(-ref(c).x, -ref(c).y));
             }
-            if (++h == a.g) {
-              h = 0;
-              ++p;
-            }
-          }
-        }
-        float worst = -INFINITY;
+          // positions that rows do not see, and tiles past the part's last (their scores are stale)
+          const int k0 = j * TA_BN, k1 = j1 * TA_BN;
+          if (k0 + C::KT * TA_BN > min(p_first + 1, k1) || (a.window && k0 < p_last - a.window + 1)) {
+            int p = p_first, h = 0;  // the row's position
 #pragma unroll
-        for (int t = 0; t < C::KT; ++t)
+            for (int c = 0; c < R; ++c) {
+              const int lo = a.window ? p - k0 - tid - a.window : -1, hi = min(p, k1 - 1) - k0 - tid;  // lo < 128 t <= hi
 #pragma unroll
-          for (int c = 0; c < R / 2; ++c) worst = ta_max3(worst, y[t][c].x, y[t][c].y);
-        if (j == j0 || tf_any(!ok || worst > TQ_TOP)) {
-          // new references: the rows' maxima so far, less the shift
-          // (from the scores themselves: y has lost them where the reference was far off)
-          auto score = [&](float w, float p, float f, float m) { return w == -INFINITY ? w : fmaf(p, f, -m); };
-          float v[R];
-#pragma unroll
-          for (int c = 0; c < R / 2; ++c) {
-            v[2 * c] = v[2 * c + 1] = -INFINITY;
-#pragma unroll
-            for (int t = 0; t < C::KT; ++t) {
-              v[2 * c] = fmaxf(v[2 * c], score(y[t][c].x, z[t][c].x, factor(c).x, 0.0f));
-              v[2 * c + 1] = fmaxf(v[2 * c + 1], score(y[t][c].y, z[t][c].y, factor(c).y, 0.0f));
-            }
-          }
-          tf_combine<R>(v, [](float p, float q) { return fmaxf(p, q); });
-          s_red[warp][tf_column<R>()] = v[0];
-          if (j > j0) ok = ctl.wait(&pv_done[b ^ 1], (step - 1) >> 1 & 1) && ok;
-          if (tf_any(!ok)) {
-            out = true;
-            break;
-          }
-          // the lowest finite number: no score is below it, and a key that is not seen (-inf) weighs 0.
-          // Rows that the tile has to spare: with an infinite reference they weigh nothing and never ask
-          // for a change.
-          auto moved = [&](int c, float seen, float m0) { return c < rows ? fmaxf(seen - TQ_SHIFT, m0) : INFINITY; };
-          constexpr bool ALL = R <= 8;  // more rows would cost the registers that the steps need
-          float2 scale[ALL ? R / 2 : 1] = {};
-          if constexpr (ALL) {  // each thread all rows: one barrier
-#pragma unroll
-            for (int c = 0; c < R; c += 4) {
-              float4 t4 = *reinterpret_cast<const float4*>(&s_red[0][c]);
-#pragma unroll
-              for (int w = 1; w < 4; ++w) {
-                const float4 u = *reinterpret_cast<const float4*>(&s_red[w][c]);
-                t4 = make_float4(fmaxf(t4.x, u.x), fmaxf(t4.y, u.y), fmaxf(t4.z, u.z), fmaxf(t4.w, u.w));
+              for (int t = 0; t < C::KT; ++t) {
+                float& w = c & 1 ? y[t][c / 2].y : y[t][c / 2].x;
+                if (t * TA_BN > hi || t * TA_BN <= lo) w = -INFINITY;
               }
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float2 m0 = j == j0 ? make_float2(-FLT_MAX, -FLT_MAX) : refs[c / 2 + e];
-                const float2 m = make_float2(moved(c + 2 * e, e ? t4.z : t4.x, m0.x), moved(c + 2 * e + 1, e ? t4.w : t4.y, m0.y));
-                scale[c / 2 + e] = make_float2(m0.x == m.x ? 1.0f : ta_ex2(m0.x - m.x), m0.y == m.y ? 1.0f : ta_ex2(m0.y - m.y));
-                refs[c / 2 + e] = m;
+              if (++h == a.g) {
+                h = 0;
+                ++p;
               }
             }
-          } else {
-            if (tid < R) {
-              const float m0 = j == j0 ? -FLT_MAX : s_ref[tid];
-              const float m = moved(tid, fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), m0);
-              s_scale[tid] = m0 == m ? 1.0f : ta_ex2(m0 - m);
-              s_ref[tid] = m;
-            }
-            tf_any(false);
-            if constexpr (KEEP)
-#pragma unroll
-              for (int c = 0; c < R / 2; ++c) refs[c] = reinterpret_cast<const float2*>(s_ref)[c];
           }
-          auto factor_of = [&](int c) { return ALL ? scale[ALL ? c : 0] : reinterpret_cast<const float2*>(s_scale)[c]; };
+          float worst = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < R / 2; ++c)
+          for (int t = 0; t < C::KT; ++t)
 #pragma unroll
-            for (int t = 0; t < C::KT; ++t)
-              y[t][c] = make_float2(score(y[t][c].x, z[t][c].x, factor(c).x, ref(c).x), score(y[t][c].y, z[t][c].y, factor(c).y, ref(c).y));
-          if (j > j0) {
-            tc::tc_fence_after();
+            for (int c = 0; c < R / 2; ++c) worst = ta_max3(worst, y[t][c].x, y[t][c].y);
+          if (j == j0 || tf_any(!ok || worst > TQ_TOP)) {
+            // new references: the rows' maxima so far, less the shift
+            // (from the scores themselves: y has lost them where the reference was far off)
+            auto score = [&](float w, float p, float f, float m) { return w == -INFINITY ? w : fmaf(p, f, -m); };
+            float v[R];
 #pragma unroll
-            for (int c = 0; c < R / 2; ++c) l[c] = make_float2(l[c].x * factor_of(c).x, l[c].y * factor_of(c).y);
-            auto rescale = [&](uint32_t at, float2 f0, float2 f1) {
-              float o[4];
-              tc::tmem_ld4(at, o);
-              tc::tmem_ld_wait();
-              tc::reg_fence(o);
-              o[0] *= f0.x;
-              o[1] *= f0.y;
-              o[2] *= f1.x;
-              o[3] *= f1.y;
-              tc::tmem_st4(at, o);
-            };
-#pragma unroll 1
-            for (int hm = 0; hm < C::UNITS; ++hm) {
-              if constexpr (ALL) {
+            for (int c = 0; c < R / 2; ++c) {
+              v[2 * c] = v[2 * c + 1] = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < C::COLS; c += 4) rescale(t_o + hm * NR + c, factor_of(c % R / 2), factor_of(c % R / 2 + 1));
-              } else {
-#pragma unroll 1
-                for (int c = 0; c < C::COLS; c += 4) {
-                  const float2* f = reinterpret_cast<const float2*>(s_scale) + c % R / 2;
-                  rescale(t_o + hm * NR + c, f[0], f[1]);
+              for (int t = 0; t < C::KT; ++t) {
+                v[2 * c] = fmaxf(v[2 * c], score(y[t][c].x, z[t][c].x, factor(c).x, 0.0f));
+                v[2 * c + 1] = fmaxf(v[2 * c + 1], score(y[t][c].y, z[t][c].y, factor(c).y, 0.0f));
+              }
+            }
+            tf_combine<R>(v, [](float p, float q) { return fmaxf(p, q); });
+            s_red[warp][tf_column<R>()] = v[0];
+            if (j > j0) ok = ctl.wait(&pv_done[b ^ 1], (step - 1) >> 1 & 1) && ok;
+            if (tf_any(!ok)) {
+              out = true;
+              break;
+            }
+            // the lowest finite number: no score is below it, and a key that is not seen (-inf) weighs 0.
+            // Rows that the tile has to spare: with an infinite reference they weigh nothing and never ask
+            // for a change.
+            auto moved = [&](int c, float seen, float m0) { return c < rows ? fmaxf(seen - TQ_SHIFT, m0) : INFINITY; };
+            if constexpr (ALL) {  // each thread all rows: one barrier
+#pragma unroll
+              for (int c = 0; c < R; c += 4) {
+                float4 t4 = *reinterpret_cast<const float4*>(&s_red[0][c]);
+#pragma unroll
+                for (int w = 1; w < 4; ++w) {
+                  const float4 u = *reinterpret_cast<const float4*>(&s_red[w][c]);
+                  t4 = make_float4(fmaxf(t4.x, u.x), fmaxf(t4.y, u.y), fmaxf(t4.z, u.z), fmaxf(t4.w, u.w));
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float2 m0 = j == j0 ? make_float2(-FLT_MAX, -FLT_MAX) : refs[c / 2 + e];
+                  const float2 m = make_float2(moved(c + 2 * e, e ? t4.z : t4.x, m0.x), moved(c + 2 * e + 1, e ? t4.w : t4.y, m0.y));
+                  scale[c / 2 + e] = make_float2(m0.x == m.x ? 1.0f : ta_ex2(m0.x - m.x), m0.y == m.y ? 1.0f : ta_ex2(m0.y - m.y));
+                  refs[c / 2 + e] = m;
                 }
               }
+            } else {
+              if (tid < R) {
+                const float m0 = j == j0 ? -FLT_MAX : s_ref[tid];
+                const float m = moved(tid, fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), m0);
+                s_scale[tid] = m0 == m ? 1.0f : ta_ex2(m0 - m);
+                s_ref[tid] = m;
+              }
+              tf_any(false);
+              if constexpr (KEEP)
+#pragma unroll
+                for (int c = 0; c < R / 2; ++c) refs[c] = reinterpret_cast<const float2*>(s_ref)[c];
             }
-            tc::tmem_st_wait();
+#pragma unroll
+            for (int c = 0; c < R / 2; ++c)
+#pragma unroll
+              for (int t = 0; t < C::KT; ++t)
+                y[t][c] = make_float2(score(y[t][c].x, z[t][c].x, factor(c).x, ref(c).x), score(y[t][c].y, z[t][c].y, factor(c).y, ref(c).y));
+            if (j > j0) {
+              tc::tc_fence_after();
+              grown = true;
+#pragma unroll
+              for (int c = 0; c < R / 2; ++c) l[c] = make_float2(l[c].x * factor_of(c).x, l[c].y * factor_of(c).y);
+              auto rescale = [&](uint32_t at, float2 f0, float2 f1) {
+                float o[4];
+                tc::tmem_ld4(at, o);
+                tc::tmem_ld_wait();
+                tc::reg_fence(o);
+                o[0] *= f0.x;
+                o[1] *= f0.y;
+                o[2] *= f1.x;
+                o[3] *= f1.y;
+                tc::tmem_st4(at, o);
+              };
+#pragma unroll 1
+              for (int hm = 0; hm < (F32 ? 0 : C::UNITS); ++hm) {
+                if constexpr (ALL) {
+#pragma unroll
+                  for (int c = 0; c < C::COLS; c += 4) rescale(t_o + hm * NR + c, factor_of(c % R / 2), factor_of(c % R / 2 + 1));
+                } else {
+#pragma unroll 1
+                  for (int c = 0; c < C::COLS; c += 4) {
+                    const float2* f = reinterpret_cast<const float2*>(s_scale) + c % R / 2;
+                    rescale(t_o + hm * NR + c, f[0], f[1]);
+                  }
+                }
+              }
+              if (!F32) tc::tmem_st_wait();
+            }
           }
+          ok = ctl.wait(&pv_done[b], (step >> 1 & 1) ^ 1) && ok;  // P^T of two steps ago is used up
+#pragma unroll
+          for (int t = 0; t < C::KT; ++t) {
+            uint32_t pk[C::COLS / 2];
+#pragma unroll
+            for (int c = 0; c < R / 2; ++c) {
+              const float2 w = make_float2(ta_ex2(y[t][c].x), ta_ex2(y[t][c].y));
+              l[c] = ta_add2(l[c], w);
+              pk[c] = tq_pack(w.x, w.y);
+              if (F32) pk[(C::COLS - R) / 2 + c] = tq_rest(w.x, w.y, pk[c]);
+            }
+            // the key's row of P^T: 16-byte pieces where the tensor core's swizzle has them
+            uint8_t* row = s_p + b * C::PB + t * C::PT + tid * C::PROW;
+            const int sw = NR == 16 ? tid >> 2 & 1 : tid >> 1 & 3;
+            if constexpr (C::COLS == 4) {
+              *reinterpret_cast<uint2*>(row + (sw << 4)) = make_uint2(pk[0], pk[1]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < C::COLS / 8; ++c)
+                *reinterpret_cast<uint4*>(row + ((c ^ sw) << 4)) =
+                    make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+            }
+          }
+          tc::fence_proxy_async_smem();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&p_full[b]);
         }
-        ok = ctl.wait(&pv_done[b], (step >> 1 & 1) ^ 1) && ok;  // P^T of two steps ago is used up
+        if (F32 && j > j0) {  // the product of the step before
+          ok = ctl.wait(&pv_done[b ^ 1], (step - 1) >> 1 & 1) && ok;
+          tc::tc_fence_after();
+          const uint32_t t_b = lanes + C::O_COL + (b ^ 1) * (C::UNITS * NR);
 #pragma unroll
-        for (int t = 0; t < C::KT; ++t) {
-          uint32_t pk[C::COLS / 2];
+          for (int hm = 0; hm < (F32 ? C::UNITS : 0); ++hm) {
+            float o[F32 ? C::COLS : 16];
 #pragma unroll
-          for (int c = 0; c < R / 2; ++c) {
-            const float2 w = make_float2(ta_ex2(y[t][c].x), ta_ex2(y[t][c].y));
-            l[c] = ta_add2(l[c], w);
-            pk[c] = tq_pack(w.x, w.y);
-            if (F32) pk[(C::COLS - R) / 2 + c] = tq_rest(w.x, w.y, pk[c]);
+            for (int c = 0; c < C::COLS; c += 16) tc::tmem_ld16(t_b + hm * NR + c, *reinterpret_cast<float(*)[16]>(o + c));
+            tc::tmem_ld_wait();
+            tc::reg_fence(o);
+#pragma unroll
+            for (int c = 0; c < R / 2; ++c) {
+              acc[hm][c] = ta_add2(acc[hm][c], ta_add2(make_float2(o[2 * c], o[2 * c + 1]), make_float2(o[C::COLS - R + 2 * c], o[C::COLS - R + 2 * c + 1])));
+              if (grown) acc[hm][c] = make_float2(acc[hm][c].x * factor_of(c).x, acc[hm][c].y * factor_of(c).y);
+            }
+            if (j >= j1)  // the sums back to where they are written out from, as other types' are
+#pragma unroll
+              for (int c = 0; c < R; c += 4) {
+                const float4 v = make_float4(acc[hm][c / 2].x, acc[hm][c / 2].y, acc[hm][c / 2 + 1].x, acc[hm][c / 2 + 1].y);
+                tc::tmem_st4(t_b + hm * NR + c, *reinterpret_cast<const float(*)[4]>(&v));
+              }
           }
-          // the key's row of P^T: 16-byte pieces where the tensor core's swizzle has them
-          uint8_t* row = s_p + b * C::PB + t * C::PT + tid * C::PROW;
-          const int sw = NR == 16 ? tid >> 2 & 1 : tid >> 1 & 3;
-          if constexpr (C::COLS == 4) {
-            *reinterpret_cast<uint2*>(row + (sw << 4)) = make_uint2(pk[0], pk[1]);
-          } else {
-#pragma unroll
-            for (int c = 0; c < C::COLS / 8; ++c)
-              *reinterpret_cast<uint4*>(row + ((c ^ sw) << 4)) =
-                  make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-          }
+          if (j >= j1) tc::tmem_st_wait();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (j < j1 && lane == 0) tc::mbar_arrive(&o_empty[b ^ 1]);
         }
-        tc::fence_proxy_async_smem();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&p_full[b]);
+        if (F32 && j >= j1) break;
       }
       if (out) break;
       const bool any = j1 > j0;
@@ -400,6 +444,10 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
         ok = ctl.wait(&pv_done[(step - 1) & 1], (step - 1) >> 1 & 1) && ok;
         tc::tc_fence_after();
         ++no;
+      }
+      if (F32) {  // the last product's
+        ob = (step - 1) & 1;
+        t_o = lanes + C::O_COL + ob * (C::UNITS * NR);
       }
       // Not before the wait: it ends once all four warps have handed in the last step's weights, and until then one
       // of them may still read that step's maxima from s_red.  (Without keys nothing has been read since the barrier
@@ -427,22 +475,13 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < rows; c += 4) {
           __syncwarp();  // (TMEM is read by whole warps)
-          float o[C::UNITS][4], o2[C::UNITS][4];
+          float o[C::UNITS][4];
 #pragma unroll
-          for (int hm = 0; hm < C::UNITS; ++hm) {
+          for (int hm = 0; hm < C::UNITS; ++hm)
             if (any) tc::tmem_ld4(t_o + hm * NR + c, o[hm]);
-            if (any && F32) tc::tmem_ld4(t_o + hm * NR + (C::COLS - R) + c, o2[hm]);
-          }
           if (any) tc::tmem_ld_wait();
 #pragma unroll
-          for (int hm = 0; hm < C::UNITS; ++hm) {
-            tc::reg_fence(o[hm]);
-            if (F32) {
-              tc::reg_fence(o2[hm]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[hm][e] += o2[hm][e];
-            }
-          }
+          for (int hm = 0; hm < C::UNITS; ++hm) tc::reg_fence(o[hm]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (c + e >= rows) break;
@@ -688,13 +727,17 @@ __global__ void __launch_bounds__(TQ_THREADS, 1)
         const int j0 = it.j0, j1 = it.j1;
         tc::mbar_arrive(&i_empty[ni % TA_ITEMS]);
         if (j1 <= j0) continue;
-        const uint32_t ob = no & 1;
-        ok = ctl.wait1(&o_empty[ob], (no >> 1 & 1) ^ 1);
+        // O^T's buffer is an item's, of float32 a step's
+        if (!F32) ok = ctl.wait1(&o_empty[no & 1], (no >> 1 & 1) ^ 1);
         ++no;
-        uint32_t more = 0;  // not the item's first product
+        uint32_t more = 0;  // not the buffer's first product
         for (int j = j0; j < j1 && ok; j += C::KT, ++step) {
-          const uint32_t b = step & 1;
-          ok = ctl.wait1(&p_full[b], step >> 1 & 1);
+          const uint32_t b = step & 1, ob = F32 ? b : (no - 1) & 1;
+          if (F32) {
+            ok = ctl.wait1(&o_empty[b], (step >> 1 & 1) ^ 1);
+            more = 0;
+          }
+          ok = ok && ctl.wait1(&p_full[b], step >> 1 & 1);
           const int kt = min(C::KT, j1 - j);
 #pragma unroll 1
           for (int t = 0; t < kt && ok; ++t, more = 1)

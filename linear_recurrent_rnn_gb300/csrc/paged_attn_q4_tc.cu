@@ -8,7 +8,10 @@
 // place as f16, each row times the power of two that brings its largest element to [2^14, 2^15) (bf16's 8
 // significant bits fit f16's 11); its scores are multiplied by the inverse.  Weights are f16 and held times a
 // power of two; the maximum is moved when a weight would pass 2^15.  float32 queries and weights are sums of two f16
-// (22 bits): each of the two is multiplied with the same keys or values into the same sums, twice the products.
+// (22 bits): each of the two is multiplied with the same keys or values into the same sums, twice the products, the small
+// halves first.  The tensor core cuts what it adds to a sum (paged_attn_q4.cu has the figures), so float32's product of a
+// key tile's unit is a sum of its own in TMEM, and the row's thread adds it to the sums there, a tile behind; heads of 256 leave
+// TMEM for one S only then, and their two products take turns with the softmax (122 -> 157 us below; heads of 128 120 -> 128).
 //
 // Widths up to 128: one row tile a CTA and two warpgroups that bring keys and values, or, for long prompts in bf16, two
 // row tiles and one (row_tiles below; a second beside two tiles needs registers that softmax has: reading the
@@ -18,8 +21,8 @@
 // Measured (GB300): those chunks 1.05 PFLOP/s (1.41 over bf16 caches), with heads of 256 1.01; 20 decode rows and 4
 // chunks of 300 to 777 tokens in up to 8192, 104 us.  What bounds it: a warpgroup's 2250 cycles a unit, of which a key
 // tile has two, against 1024 of products a row tile; a lone warp a scheduler issues in order, ten cycles an
-// instruction.  float32, 4 chunks of 700 tokens in up to 4096, 16 heads on 4 of 128: 129 us (the kernel for few rows: 510),
-// 10 on 1 of 256: 148 (844).
+// instruction.  float32, 4 chunks of 700 tokens in 1000 to 4096, 16 heads on 4 of 128: 128 us, 10 on 1 of 256:
+// 157 (the kernel for few rows, before it added steps up: four and six times as much).
 #include <float.h>
 
 #include <algorithm>
@@ -55,7 +58,11 @@ struct Tm {
   static constexpr int REGS = 65536 / THREADS / 8 * 8;
   static constexpr int SOFT_REGS = NT == 2 ? 184 : GROUPS == 3 ? 192 : 224;
   static constexpr int OTHER_REGS = (REGS * THREADS - SOFT_REGS * SOFT) / (THREADS - SOFT) / 8 * 8;
-  static constexpr uint32_t S_COL = 0, O_COL = 256;   // TMEM: S/P buffers b at 128 b, O tiles
+  // TMEM: S/P buffers b at 128 b, O tiles; of float32 O's sums, and the product of a key tile's unit that is added to
+  // them (heads of 256 leave room for one S/P)
+  static constexpr int S_BUF = F32 && DP == 256 ? 1 : 2;
+  static constexpr uint32_t S_COL = 0, O_COL = 256, STEP_COL = DP == 256 ? 128 : 256 + DP;
+  static_assert(!F32 || NT == 1, "one row tile");
   static constexpr size_t Q_BYTES = (size_t)NT * SLABS * TA_SLAB;
   static constexpr int FIT = (int)((232448 - 4096 - 1024 - Q_BYTES - STAGES * UB - 1024) / SB);
   static constexpr int DEPTH = FIT / GROUPS < 6 ? FIT / GROUPS : 6;  // units of codes on their way, of a group
@@ -177,7 +184,37 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
     const int t = NT == 2 ? warp >> 2 : 0, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t t_o = lanes + C::O_COL + t * DP;
-    uint32_t cs = 0, npv = 0, nj = 0, nf = 0;  // S taken, products P V of this tile, parts handed over
+    uint32_t cs = 0, npv = 0, nj = 0, nf = 0;  // S taken, products P V of this tile (float32: of its units), parts handed over
+    // float32: the product in STEP_COL is added to the sums of unit u, or is the first of them.  The sums so far are multiplied by
+    // f, and with `old` the product too: it is of a tile before the sums' growth.
+    constexpr int ADD = 64;  // columns at once
+    auto add_product = [&](int u, bool first, bool old, float f, bool live) {
+      tc::tc_fence_after();
+      if (live) {
+        const float fx = old ? f : 1.0f;
+#pragma unroll 1
+        for (int c = 0; c < C::COL && u * C::COL + c < a.D; c += ADD) {
+          __syncwarp();
+          float x[ADD], y[ADD];
+#pragma unroll
+          for (int e = 0; e < ADD; e += 16) {
+            tc::tmem_ld16(lanes + C::STEP_COL + c + e, *reinterpret_cast<float(*)[16]>(x + e));
+            tc::tmem_ld16(t_o + u * C::COL + c + e, *reinterpret_cast<float(*)[16]>(y + e));
+          }
+          tc::tmem_ld_wait();
+          tc::reg_fence(x);
+          tc::reg_fence(y);
+#pragma unroll
+          for (int e = 0; e < ADD; ++e) x[e] = first ? x[e] * fx : fmaf(y[e], f, x[e] * fx);
+#pragma unroll
+          for (int e = 0; e < ADD; e += 16) tc::tmem_st16(t_o + u * C::COL + c + e, *reinterpret_cast<const float(*)[16]>(x + e));
+        }
+        tc::tmem_st_wait();
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&o_empty[0]);
+    };
     uint32_t here_par = 0;             // parities of j_here
     bool ok = true;
     const TaItem* rec;
@@ -199,12 +236,13 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
         if (lane == 0) tc::mbar_arrive(&f_empty[t]);
       }
       for (int j = tl.ja; j < tl.jb; ++j) {
-        const int b = NT == 2 ? t : cs & 1;
-        ok = ctl.wait(&s_full[b], (NT == 2 ? cs : cs >> 1) & 1);
+        const int b = NT == 2 ? t : C::S_BUF == 1 ? 0 : cs & 1;
+        ok = ctl.wait(&s_full[b], (NT == 2 || C::S_BUF == 1 ? cs : cs >> 1) & 1);
         ++cs;
         if (!ok) break;
         tc::tc_fence_after();
         bool waited = j == tl.ja;  // NT = 1: for the product before this one
+        float grown = 1.0f;        // float32: what the sums so far are to be multiplied by
         if (live) {
           float s[128];
           const uint32_t t_s = lanes + C::S_COL + b * 128;
@@ -235,14 +273,15 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
             const float f = top == m ? 1.0f : ta_ex2((top - m) * -sc);
             l *= f;
             m = top;
-            if (NT == 1) {
+            grown = f;
+            if (NT == 1 && !F32) {
               ok = ctl.wait(&pv_done[0], (npv + (j - tl.ja) - 1) & 1);
               waited = true;
               if (!ok) break;
               tc::tc_fence_after();
             }
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
+            for (int c = 0; c < (F32 ? 0 : DP); c += 16) {
               float o[16];
               tc::tmem_ld16(t_o + c, o);
               tc::tmem_ld_wait();
@@ -274,13 +313,23 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
           l += s2.x + s2.y;
           tc::tmem_st_wait();
         }
-        if (NT == 1 && !waited) {
+        if (NT == 1 && !F32 && !waited) {
           ok = ctl.wait(&pv_done[0], (npv + (j - tl.ja) - 1) & 1);
           if (!ok) break;
         }
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&p_full[b]);
+        if constexpr (F32) {
+          // the last unit's product of the tile before, then this tile's, but for its last unit's
+#pragma unroll 1
+          for (int u = -1; u < C::UNITS - 1 && ok; ++u) {
+            if (u < 0 && j == tl.ja) continue;
+            ok = ctl.wait(&pv_done[0], npv++ & 1);
+            if (ok) add_product(u < 0 ? C::UNITS - 1 : u, j == tl.ja + (u < 0 ? 1 : 0), u < 0, grown, live);
+          }
+          if (!ok) break;
+        }
       }
       if (!ok) break;
       const bool any = tl.jb > tl.ja;
@@ -305,10 +354,11 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
         here = *reinterpret_cast<volatile uint32_t*>(&s_here[k]);
       }
       if (any) {
-        npv += tl.jb - tl.ja;
+        npv += F32 ? 1 : tl.jb - tl.ja;
         ok = ctl.wait(&pv_done[t], (npv - 1) & 1);
         if (!ok) break;
         tc::tc_fence_after();
+        if (F32) add_product(C::UNITS - 1, tl.jb == tl.ja + 1, false, 1.0f, live);
       }
       const bool mine = r < tl.rows;
       const int row = t * 128 + r;
@@ -399,7 +449,7 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
         if (any) {
           tc::tc_fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&o_empty[t]);
+          if (!F32 && lane == 0) tc::mbar_arrive(&o_empty[t]);
         }
       } else {
         // a part: maxima, sums and unscaled O to the workspace; the last CTA of the item joins them
@@ -424,7 +474,7 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
         if (any) tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (any) tc::mbar_arrive(&o_empty[t]);
+          if (any && !F32) tc::mbar_arrive(&o_empty[t]);
           tc::mbar_arrive(j_full);
         }
         if (warp == 0) {
@@ -581,7 +631,7 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
         const uint64_t d_k = tc::smem_desc(tc::smem_u32(s_ring), 16, 1024, tc::LAYOUT_SW128);
         const uint64_t d_v = tc::smem_desc(tc::smem_u32(s_ring), TA_SLAB, 1024, tc::LAYOUT_SW128);
         uint32_t st = 0, ph = 0;            // next ring unit, parity of its `full`
-        uint32_t nq[NT] = {}, no[NT] = {};  // items of tile t so far: queries taken, O begun
+        uint32_t nq[NT] = {}, no[NT] = {};  // items of tile t so far: queries taken, O begun (float32: products of units)
         uint32_t cs[NT] = {}, cp[NT] = {};  // S of tile t issued, P taken
         bool ok = true;
         for (; ok; ++ni) {
@@ -624,7 +674,7 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
               take_k();
               if (j == tl[t].ja) ok = ok && ctl.wait1(&q_ready[t], nq[t]++ & 1);
               if (!ok) return;
-              const uint32_t b = NT == 2 ? t : cs[t] & 1;
+              const uint32_t b = NT == 2 ? t : C::S_BUF == 1 ? 0 : cs[t] & 1;
               ++cs[t];
               tc::tc_fence_after();
 #pragma unroll
@@ -634,13 +684,14 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
                   if (!ok) return;
                   tc::tc_fence_after();
                 }
+                // (the small halves first: a product is cut to the bits of the sum that it meets)
 #pragma unroll
-                for (int k = 0; k < C::COL / 16; ++k)
+                for (int x = C::NUM - 1; x >= 0; --x)
 #pragma unroll
-                  for (int x = 0; x < C::NUM; ++x)
+                  for (int k = 0; k < C::COL / 16; ++k)
                     tc::mma_bf16(tmem + C::S_COL + b * 128,
                                  d_q + (((t * C::SLABS + (u * C::COL / 64 + k / 4) * C::NUM + x) * TA_SLAB + k % 4 * 32) >> 4),
-                                 d_k + ((k_st[u] * C::UB + k / 4 * TA_SLAB + k % 4 * 32) >> 4), id_qk, u + k + x > 0);
+                                 d_k + ((k_st[u] * C::UB + k / 4 * TA_SLAB + k % 4 * 32) >> 4), id_qk, u > 0 || x < C::NUM - 1 || k > 0);
                 if (NT == 1) tc::mma_commit(&empty[k_st[u]]);  // a unit is free once read
               }
               tc::mma_commit(&s_full[b]);
@@ -648,10 +699,10 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
             };
             auto pv = [&](int t) {
               take_v();
-              const uint32_t b = NT == 2 ? t : cp[t] & 1;
-              ok = ok && ctl.wait1(&p_full[b], (NT == 2 ? cp[t] : cp[t] >> 1) & 1);
+              const uint32_t b = NT == 2 ? t : C::S_BUF == 1 ? 0 : cp[t] & 1;
+              ok = ok && ctl.wait1(&p_full[b], (NT == 2 || C::S_BUF == 1 ? cp[t] : cp[t] >> 1) & 1);
               ++cp[t];
-              if (j - 1 == tl[t].ja) ok = ok && ctl.wait1(&o_empty[t], (no[t]++ & 1) ^ 1);
+              if (!F32 && j - 1 == tl[t].ja) ok = ok && ctl.wait1(&o_empty[t], (no[t]++ & 1) ^ 1);
               if (!ok) return;
               tc::tc_fence_after();
               const uint32_t more = j - 1 > tl[t].ja;
@@ -659,22 +710,25 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
               for (int u = 0; u < C::UNITS; ++u) {
                 if (NT == 1) {
                   ok = ctl.wait1(&full[v_st[u]], v_par[u]);
+                  if (F32) ok = ok && ctl.wait1(&o_empty[t], (no[t]++ & 1) ^ 1);
                   if (!ok) return;
                   tc::tc_fence_after();
                 }
 #pragma unroll
-                for (int k = 0; k < TA_BN / 16; ++k)
+                for (int x = C::NUM - 1; x >= 0; --x)
 #pragma unroll
-                  for (int x = 0; x < C::NUM; ++x)
-                    tc::mma_ts(tmem + C::O_COL + t * DP + u * C::COL, tmem + C::S_COL + b * 128 + x * 64 + k * 8,
-                               d_v + ((v_st[u] * C::UB + k * 2048) >> 4), id_pv, k + x > 0 ? 1u : more);
+                  for (int k = 0; k < TA_BN / 16; ++k)
+                    tc::mma_ts(tmem + (F32 ? C::STEP_COL : C::O_COL + t * DP + u * C::COL), tmem + C::S_COL + b * 128 + x * 64 + k * 8,
+                               d_v + ((v_st[u] * C::UB + k * 2048) >> 4), id_pv, x < C::NUM - 1 || k > 0 ? 1u : F32 ? 0u : more);
                 if (NT == 1) tc::mma_commit(&empty[v_st[u]]);
+                if (F32) tc::mma_commit(&pv_done[t]);
               }
-              tc::mma_commit(&pv_done[t]);
+              if (!F32) tc::mma_commit(&pv_done[t]);
             };
             if (NT == 1) {
-              if (j < j1) qk(0);
-              if (j > j0 && ok) pv(0);
+              if (C::S_BUF == 1 && j > j0) pv(0);
+              if (j < j1 && ok) qk(0);
+              if (C::S_BUF == 2 && j > j0 && ok) pv(0);
             } else {
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
@@ -702,7 +756,7 @@ __global__ void __launch_bounds__(Tm<DP, F32, NT_>::THREADS, 1)
       uint32_t o[4];  // where the row's 16-byte pieces lie
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[c] = (c ^ (r & 7)) << 4;
-      TqStream<C, C::GROUPS, NT == 2 ? 2 : 3> str{a, cache, ctl, s_item, i_full, i_empty, s_copy + g * C::DEPTH * C::SB, (uint32_t)g};
+      TqStream<C, C::GROUPS, NT == 2 || C::S_BUF == 1 ? 2 : 3> str{a, cache, ctl, s_item, i_full, i_empty, s_copy + g * C::DEPTH * C::SB, (uint32_t)g};
       uint32_t rb = g, par = 1;
       while (str.issue()) {
         if (__builtin_expect(!str.come(), 0)) continue;

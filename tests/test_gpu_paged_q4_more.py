@@ -60,3 +60,36 @@ def test_small_weights_with_few_and_many_rows(new, size, io):
     got = o[:, 0, 0].double().cpu().numpy()
     if size == 20.0:
         assert np.all(np.abs(got - (n - 1) * 2.0 ** -20 / (1 + (n - 1) * 2.0 ** -20)) < 1e-3)
+
+
+# heads, head width, new tokens a request: tiles of 8 and 16 rows, and the kernel for many rows
+LONG = {"8-rows": (2, 64, 1), "8-rows-128": (8, 128, 1), "8-rows-256": (4, 256, 1), "16-rows": (16, 64, 1), "16-rows-256": (10, 192, 1),
+        "many-rows-64": (8, 64, 5), "many-rows-128": (16, 128, 4), "many-rows-256": (12, 256, 5)}
+
+
+@pytest.mark.parametrize("name", list(LONG))
+def test_float32_sums_over_long_contexts(name):
+    """160 requests over one cache of 65536 keys, whose values are all 3: so is every output.  The tensor core cuts what it adds to a
+    sum, to the sum's 24 bits; so float32 calls add up no more than 256 keys there (16 products of 16 keys), and those
+    sums in float32.  Each of a product's 16 terms and the sum so far lose less than 2^-23 of that, half of it in the mean:
+    17 / 2 * sum(k / 16, k <= 16) * 2^-23 = 72 * 2^-23 of the whole in the mean of all outputs, twice that in one.  Roundings
+    to nearest, of 256 sums, 512 weights a thread and the weights' two f16 numbers, are no bias: at most
+    (256 + 512) 2^-24 + 2^-22 in one output, 2^-22 in the mean of 160 and more rows."""
+    Hq, D, new = LONG[name]
+    n, N = 65536, 160
+    x = build([(new, n)], Hq, 1, D, 16, "f32", 41)
+    x["cache"][2].fill_(0x55)                 # 3
+    c = x["cache"][3]
+    c.copy_(torch.where(c == 0x7f, c, torch.full_like(c, 0x38)))
+    _, _, _, Hkv, _, P, s, width = x["dims"]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x["q"] = torch.randn(N * new, Hq, D, generator=g, device="cuda")
+    x["table"] = x["table"].repeat(N, 1).contiguous()
+    x["cu"] = (torch.arange(N + 1, device="cuda") * new).to(torch.int32)
+    x["kv"] = torch.full((N,), n, dtype=torch.int32, device="cuda")
+    x["dims"] = (N, N * new, Hq, Hkv, D, P, s, width)
+    o, _, ws = attend(x, 0.3 * D ** -0.5)
+    assert R.rglru_sync_status(ws) == R.OK
+    off = o.double() / 3 - 1
+    assert abs(float(off.mean())) <= 72 * 2.0 ** -23 + 2.0 ** -22
+    assert float(off.abs().max()) <= 144 * 2.0 ** -23 + 768 * 2.0 ** -24 + 2.0 ** -22
